@@ -440,6 +440,48 @@ SRNL_API const char* srnl_seq_last_error(const srnl_seq* h);
  * device before freeing. */
 SRNL_API void srnl_seq_destroy(srnl_seq* h);
 
+/* ------------------------------------------------------------------------
+ * Layer normalisation for training (the residual block's norm above is forward-only).
+ *   y = (x - mean) rstd gamma + beta,  rstd = 1 / sqrt(var + eps),  per row of dim values
+ * and its backward pass.  Rows are dense ([rows][dim] of act_dtype); statistics, sums and the
+ * gradients of gamma and beta are fp32.
+ * ---------------------------------------------------------------------- */
+typedef struct srnl_ln srnl_ln; /* opaque; owned by the library */
+
+typedef struct {
+  int dim;        /* values per row, 1..8192; rows that are whole 16-byte vectors run fastest */
+  int act_dtype;  /* srnl_dtype of x, y and their gradients */
+  float eps;      /* > 0 */
+} srnl_ln_config;
+
+/* Validate and allocate the handle and its workspace (the weights' partial gradients; it does
+ * not depend on the number of rows) on the CURRENT device.  *out is NULL on failure; the
+ * message is srnl_ln_last_error(NULL). */
+SRNL_API srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg);
+
+/* y = layer norm of x.  DEVICE pointers: x, y [rows][dim], 16-byte aligned; gamma, beta fp32
+ * [dim]; mean, rstd fp32 [rows], the statistics the backward pass reads, each may be NULL.
+ * Outputs overlap neither inputs nor one another.  rows may be any number; 0 does nothing.
+ * Asynchronous on `stream`; one kernel. */
+SRNL_API srnl_status srnl_ln_forward(srnl_ln* h, const void* x, const float* gamma, const float* beta, void* y,
+                                     float* mean, float* rstd, int64_t rows, void* stream);
+
+/* Backward pass for dy = dL/dy: dx = dL/dx (+ dres when it is not NULL: the gradient that
+ * reaches x by the residual branch), dgamma and dbeta (fp32 [dim], overwritten; each may be
+ * NULL; zeros for 0 rows).  mean and rstd are the forward's.  The sums over rows are taken in
+ * an order that depends on the shape alone: equal inputs give equal bits.  Asynchronous on
+ * `stream`; calls on one handle must not overlap on the device (they share its workspace). */
+SRNL_API srnl_status srnl_ln_backward(srnl_ln* h, const void* x, const void* dy, const void* dres,
+                                      const float* gamma, const float* mean, const float* rstd, void* dx,
+                                      float* dgamma, float* dbeta, int64_t rows, void* stream);
+
+/* Message for the last failure on this handle (h == NULL: the calling thread's last
+ * srnl_ln_create failure).  Never NULL. */
+SRNL_API const char* srnl_ln_last_error(const srnl_ln* h);
+
+/* Free the handle and its device memory.  Accepts NULL.  Synchronises the device. */
+SRNL_API void srnl_ln_destroy(srnl_ln* h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,8 @@ EXPORTED = ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host",
             "srnl_scan_backward", "srnl_seq_backward", "srnl_selftest_wait_timeout",
             "srnl_scan_noalloc_status", "srnl_selftest_noalloc_wait_timeout",
             "srnl_block_create", "srnl_block_forward", "srnl_block_device_status", "srnl_block_last_error",
-            "srnl_block_destroy")
+            "srnl_block_destroy",
+            "srnl_ln_create", "srnl_ln_forward", "srnl_ln_backward", "srnl_ln_last_error", "srnl_ln_destroy")
 
 
 class SrnlError(RuntimeError):
@@ -102,6 +103,10 @@ class _SeqParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("M_mem0", "M_k0", "M_v0", "m_eta0", "m_alpha0")]
 
 
+class _LnConfig(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("act_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -156,6 +161,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.srnl_block_destroy.argtypes = [vp]
     lib.srnl_block_destroy.restype = None
     lib.srnl_selftest_noalloc_wait_timeout.argtypes = [i, vp]
+    i64 = ctypes.c_int64
+    lib.srnl_ln_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(_LnConfig)]
+    lib.srnl_ln_forward.argtypes = [vp] * 7 + [i64, vp]
+    lib.srnl_ln_backward.argtypes = [vp] * 10 + [i64, vp]
+    lib.srnl_ln_last_error.argtypes = [vp]
+    lib.srnl_ln_last_error.restype = ctypes.c_char_p
+    lib.srnl_ln_destroy.argtypes = [vp]
+    lib.srnl_ln_destroy.restype = None
     for name in ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host", "srnl_scan_forward_noalloc",
                  "srnl_scan_route_index", "srnl_scan_gather", "srnl_scan_enable_stage_timing",
                  "srnl_scan_stage_times", "srnl_scan_device_status", "srnl_seq_create", "srnl_seq_forward",
@@ -163,7 +176,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "srnl_scan_forward_host_async", "srnl_scan_host_join", "srnl_scan_host_sync",
                  "srnl_scan_backward", "srnl_seq_backward", "srnl_selftest_wait_timeout",
                  "srnl_scan_noalloc_status", "srnl_selftest_noalloc_wait_timeout", "srnl_block_create",
-                 "srnl_block_forward", "srnl_block_device_status"):
+                 "srnl_block_forward", "srnl_block_device_status", "srnl_ln_create", "srnl_ln_forward",
+                 "srnl_ln_backward"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -529,3 +543,100 @@ def srnl_block_device_status(h: SrnlBlock) -> None:
 
 def srnl_block_destroy(h: SrnlBlock) -> None:
     h.close()
+
+
+# ------------------------------------------------ operators of a trainable block
+def _dt(v) -> int:
+    return {"f32": SRNL_F32, "bf16": SRNL_BF16}.get(v, v)
+
+
+def _torch_dtype(act_dtype: int):
+    import torch
+    return torch.bfloat16 if act_dtype == SRNL_BF16 else torch.float32
+
+
+def _dense(t, where: str, name: str, dtype, n: int) -> int:
+    """Address of a dense CUDA tensor of n values of dtype (0 for None); raises otherwise."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
+        raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a dense CUDA tensor of {n} {dtype} values, got "
+                                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+class _OpHandle:
+    """Owns one handle of an operator; ``close()`` (or GC) destroys it."""
+
+    _prefix = ""
+
+    def __init__(self, handle: int, cfg: Dict):
+        self._h = handle
+        self.cfg = dict(cfg)
+
+    @property
+    def handle(self) -> int:
+        if not self._h:
+            raise RuntimeError(f"{self._prefix} handle is closed")
+        return self._h
+
+    def _check(self, status: int, where: str):
+        if status != SRNL_OK:
+            raise SrnlError(status, where, getattr(load_library(), self._prefix + "_last_error")(self._h).decode())
+
+    def close(self):
+        if self._h:
+            getattr(load_library(), self._prefix + "_destroy")(self._h)
+            self._h = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class SrnlLn(_OpHandle):
+    """Owns one ``srnl_ln*`` handle (layer normalisation with its backward pass)."""
+
+    _prefix = "srnl_ln"
+
+
+def srnl_ln_create(cfg: Dict) -> SrnlLn:
+    """cfg keys: dim, eps (1e-6), act_dtype ("f32"/"bf16")."""
+    lib = load_library()
+    c = _LnConfig(dim=cfg["dim"], act_dtype=_dt(cfg["act_dtype"]), eps=cfg.get("eps", 1e-6))
+    h = ctypes.c_void_p()
+    st = lib.srnl_ln_create(ctypes.byref(h), ctypes.byref(c))
+    if st != SRNL_OK:
+        raise SrnlError(st, "srnl_ln_create", lib.srnl_ln_last_error(None).decode())
+    out = SrnlLn(h.value, cfg)
+    out._dim, out._dtype = c.dim, _torch_dtype(c.act_dtype)
+    return out
+
+
+def srnl_ln_forward(h: SrnlLn, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:
+    """y <- layer norm of x ([..., dim] CUDA tensors of the handle's act dtype; gamma, beta
+    float32 [dim]); mean, rstd: float32 [rows], written when given."""
+    import torch
+    w, hd, d, f32 = "srnl_ln_forward", h.handle, h._dim, torch.float32
+    rows = x.numel() // d
+    n = rows * d
+    h._check(load_library().srnl_ln_forward(
+        hd, _dense(x, w, "x", h._dtype, n), _dense(gamma, w, "gamma", f32, d), _dense(beta, w, "beta", f32, d),
+        _dense(y, w, "y", h._dtype, n), _dense(mean, w, "mean", f32, rows), _dense(rstd, w, "rstd", f32, rows), rows,
+        _stream(stream)), w)
+
+
+def srnl_ln_backward(h: SrnlLn, x, dy, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None) -> None:
+    """dx <- dL/dx for upstream dy (+ dres when given); dgamma, dbeta (float32 [dim]) are
+    overwritten when given.  mean, rstd: the forward's."""
+    import torch
+    w, hd, d, f32 = "srnl_ln_backward", h.handle, h._dim, torch.float32
+    rows = x.numel() // d
+    n = rows * d
+    h._check(load_library().srnl_ln_backward(
+        hd, _dense(x, w, "x", h._dtype, n), _dense(dy, w, "dy", h._dtype, n), _dense(dres, w, "dres", h._dtype, n),
+        _dense(gamma, w, "gamma", f32, d), _dense(mean, w, "mean", f32, rows), _dense(rstd, w, "rstd", f32, rows),
+        _dense(dx, w, "dx", h._dtype, n), _dense(dgamma, w, "dgamma", f32, d), _dense(dbeta, w, "dbeta", f32, d), rows,
+        _stream(stream)), w)

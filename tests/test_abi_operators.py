@@ -1,0 +1,38 @@
+"""Host-side refusals of the trainable block's operators: bad configurations and NULL arguments
+are turned away before any device work."""
+import ctypes
+
+import pytest
+
+import self_referential_nested_b200 as S
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from self_referential_nested_b200 import build
+    build.build()
+    return S.load_library()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dim=0), S.SRNL_E_INVAL),
+    (dict(dim=-3), S.SRNL_E_INVAL),
+    (dict(dim=8193), S.SRNL_E_UNSUPPORTED),
+    (dict(eps=0.0), S.SRNL_E_INVAL),
+    (dict(eps=float("inf")), S.SRNL_E_INVAL),
+    (dict(eps=float("nan")), S.SRNL_E_INVAL),
+    (dict(act_dtype=5), S.SRNL_E_INVAL),
+])
+def test_ln_create_rejects_bad_config_before_cuda(lib, bad, status):
+    with pytest.raises(S.SrnlError) as e:
+        S.srnl_ln_create(dict(dict(dim=64, eps=1e-6, act_dtype="f32"), **bad))
+    assert e.value.status == status and lib.srnl_ln_last_error(None)
+
+
+def test_ln_null_arguments_fail_cleanly(lib):
+    h = ctypes.c_void_p()
+    assert lib.srnl_ln_create(None, None) == S.SRNL_E_INVAL
+    assert lib.srnl_ln_create(ctypes.byref(h), None) == S.SRNL_E_INVAL and h.value is None
+    assert lib.srnl_ln_forward(*[None] * 7, 1, None) == S.SRNL_E_INVAL
+    assert lib.srnl_ln_backward(*[None] * 10, 1, None) == S.SRNL_E_INVAL
+    lib.srnl_ln_destroy(None)
