@@ -482,6 +482,70 @@ SRNL_API const char* srnl_ln_last_error(const srnl_ln* h);
 /* Free the handle and its device memory.  Accepts NULL.  Synchronises the device. */
 SRNL_API void srnl_ln_destroy(srnl_ln* h);
 
+/* ------------------------------------------------------------------------
+ * Gated feed-forward branch with its backward pass, the counterpart of the residual block's
+ * FFN for training and serving:
+ *   y = (act(x Wg^T) * (x Wu^T)) Wd^T + res
+ * bf16 tensors, fp32 accumulation on the tensor cores.  Between the products the hidden rows
+ * (and in the backward pass the gradients of the two pre-activations) are rounded to bf16.
+ * ---------------------------------------------------------------------- */
+typedef struct srnl_ffn srnl_ffn; /* opaque; owned by the library */
+
+/* SiLU: v / (1 + exp(-v)); GELU: v Phi(v), as in the residual block. */
+typedef enum { SRNL_ACT_SILU = 0, SRNL_ACT_GELU = 1 } srnl_activation;
+
+typedef struct {
+  int dim, hidden;  /* widths of x and of the hidden layer: multiples of 8, at most 65536 */
+  int max_rows;     /* most rows of a call, at most 2^24: the workspace holds max_rows x hidden
+                       bf16 values, three times that in training */
+  int activation;   /* srnl_activation */
+  int act_dtype;    /* SRNL_BF16 */
+  int training;     /* nonzero: the handle can run the backward pass */
+} srnl_ffn_config;
+
+/* Weights: DEVICE pointers to dense bf16 arrays, read by the call they are given to. */
+typedef struct {
+  const void *W_gate, *W_up; /* [hidden][dim] */
+  const void* W_down;        /* [dim][hidden] */
+} srnl_ffn_params;
+
+/* Weight gradients: DEVICE bf16 arrays in the weights' layouts, overwritten; each may be NULL. */
+typedef struct {
+  void *W_gate, *W_up; /* [hidden][dim] */
+  void* W_down;        /* [dim][hidden] */
+} srnl_ffn_grads;
+
+/* Validate and allocate the handle and its workspace on the CURRENT device.  *out is NULL on
+ * failure; the message is srnl_ffn_last_error(NULL). */
+SRNL_API srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg);
+
+/* Forward pass.  DEVICE pointers, dense bf16, 16-byte aligned: x, y [rows][dim]; res, the
+ * residual added to y, [rows][dim] or NULL; gate, up [rows][hidden] receive the
+ * pre-activations x Wg^T and x Wu^T for the backward pass, both or neither.  Outputs overlap
+ * neither inputs nor one another.  0 <= rows <= max_rows; 0 does nothing.  Asynchronous on
+ * `stream`; calls on one handle must not overlap on the device (they share its workspace). */
+SRNL_API srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* params, const void* res,
+                                      void* y, void* gate, void* up, int rows, void* stream);
+
+/* Backward pass for dy = dL/dy, from the forward's x, gate and up: dx = dL/dx (without the
+ * residual branch, whose gradient is dy itself; NULL skips it) and the weights' gradients
+ * (grads may be NULL; zeros for 0 rows).  The handle must have been created with training set
+ * (else SRNL_E_INVAL).  Equal inputs give equal bits.  Asynchronous, as the forward. */
+SRNL_API srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, const void* up, const void* dy,
+                                       const srnl_ffn_params* params, void* dx, const srnl_ffn_grads* grads,
+                                       int rows, void* stream);
+
+/* Synchronously reads the status word of the handle's kernels: SRNL_OK, or SRNL_E_TIMEOUT once
+ * a bounded in-kernel wait gave up. */
+SRNL_API srnl_status srnl_ffn_device_status(srnl_ffn* h);
+
+/* Message for the last failure on this handle (h == NULL: the calling thread's last
+ * srnl_ffn_create failure).  Never NULL. */
+SRNL_API const char* srnl_ffn_last_error(const srnl_ffn* h);
+
+/* Free the handle and its device memory.  Accepts NULL.  Synchronises the device. */
+SRNL_API void srnl_ffn_destroy(srnl_ffn* h);
+
 #ifdef __cplusplus
 }
 #endif

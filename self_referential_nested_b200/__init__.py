@@ -23,6 +23,7 @@ LIB_PATH = os.path.join(_PKG, "libsrnl_scan.so")
 SRNL_OK, SRNL_E_INVAL, SRNL_E_UNSUPPORTED, SRNL_E_CUDA, SRNL_E_NOMEM, SRNL_E_TIMEOUT = 0, -1, -2, -3, -4, -5
 SRNL_F32, SRNL_BF16 = 0, 1
 SRNL_CAP_SOFT, SRNL_CAP_HARD = 0, 1
+SRNL_ACT_SILU, SRNL_ACT_GELU = 0, 1
 STATE_FLOATS_D32 = 3 * 32 * 32 + 2 * 32
 
 NOALLOC_SCRATCH_BYTES = 32 << 20
@@ -39,7 +40,9 @@ EXPORTED = ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host",
             "srnl_scan_noalloc_status", "srnl_selftest_noalloc_wait_timeout",
             "srnl_block_create", "srnl_block_forward", "srnl_block_device_status", "srnl_block_last_error",
             "srnl_block_destroy",
-            "srnl_ln_create", "srnl_ln_forward", "srnl_ln_backward", "srnl_ln_last_error", "srnl_ln_destroy")
+            "srnl_ln_create", "srnl_ln_forward", "srnl_ln_backward", "srnl_ln_last_error", "srnl_ln_destroy",
+            "srnl_ffn_create", "srnl_ffn_forward", "srnl_ffn_backward", "srnl_ffn_device_status",
+            "srnl_ffn_last_error", "srnl_ffn_destroy")
 
 
 class SrnlError(RuntimeError):
@@ -107,6 +110,17 @@ class _LnConfig(ctypes.Structure):
     _fields_ = [("dim", ctypes.c_int), ("act_dtype", ctypes.c_int), ("eps", ctypes.c_float)]
 
 
+class _FfnConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("dim", "hidden", "max_rows", "activation", "act_dtype", "training")]
+
+
+FFN_KEYS = ("W_gate", "W_up", "W_down")
+
+
+class _FfnWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in FFN_KEYS]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -169,6 +183,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.srnl_ln_last_error.restype = ctypes.c_char_p
     lib.srnl_ln_destroy.argtypes = [vp]
     lib.srnl_ln_destroy.restype = None
+    lib.srnl_ffn_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(_FfnConfig)]
+    lib.srnl_ffn_forward.argtypes = [vp, vp, ctypes.POINTER(_FfnWeights), vp, vp, vp, vp, i, vp]
+    lib.srnl_ffn_backward.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(_FfnWeights), vp, ctypes.POINTER(_FfnWeights),
+                                      i, vp]
+    lib.srnl_ffn_device_status.argtypes = [vp]
+    lib.srnl_ffn_last_error.argtypes = [vp]
+    lib.srnl_ffn_last_error.restype = ctypes.c_char_p
+    lib.srnl_ffn_destroy.argtypes = [vp]
+    lib.srnl_ffn_destroy.restype = None
     for name in ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host", "srnl_scan_forward_noalloc",
                  "srnl_scan_route_index", "srnl_scan_gather", "srnl_scan_enable_stage_timing",
                  "srnl_scan_stage_times", "srnl_scan_device_status", "srnl_seq_create", "srnl_seq_forward",
@@ -177,7 +200,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "srnl_scan_backward", "srnl_seq_backward", "srnl_selftest_wait_timeout",
                  "srnl_scan_noalloc_status", "srnl_selftest_noalloc_wait_timeout", "srnl_block_create",
                  "srnl_block_forward", "srnl_block_device_status", "srnl_ln_create", "srnl_ln_forward",
-                 "srnl_ln_backward"):
+                 "srnl_ln_backward", "srnl_ffn_create", "srnl_ffn_forward", "srnl_ffn_backward",
+                 "srnl_ffn_device_status"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -640,3 +664,62 @@ def srnl_ln_backward(h: SrnlLn, x, dy, gamma, mean, rstd, dx, dgamma=None, dbeta
         _dense(gamma, w, "gamma", f32, d), _dense(mean, w, "mean", f32, rows), _dense(rstd, w, "rstd", f32, rows),
         _dense(dx, w, "dx", h._dtype, n), _dense(dgamma, w, "dgamma", f32, d), _dense(dbeta, w, "dbeta", f32, d), rows,
         _stream(stream)), w)
+
+
+class SrnlFfn(_OpHandle):
+    """Owns one ``srnl_ffn*`` handle (the gated feed-forward branch with its backward pass)."""
+
+    _prefix = "srnl_ffn"
+
+
+def srnl_ffn_create(cfg: Dict) -> SrnlFfn:
+    """cfg keys: dim, hidden, max_rows, activation ("silu"/"gelu"), training (False),
+    act_dtype ("bf16")."""
+    lib = load_library()
+    act = cfg.get("activation", "silu")
+    c = _FfnConfig(dim=cfg["dim"], hidden=cfg["hidden"], max_rows=cfg["max_rows"],
+                   activation={"silu": SRNL_ACT_SILU, "gelu": SRNL_ACT_GELU}.get(act, act),
+                   act_dtype=_dt(cfg.get("act_dtype", "bf16")), training=int(bool(cfg.get("training", False))))
+    h = ctypes.c_void_p()
+    st = lib.srnl_ffn_create(ctypes.byref(h), ctypes.byref(c))
+    if st != SRNL_OK:
+        raise SrnlError(st, "srnl_ffn_create", lib.srnl_ffn_last_error(None).decode())
+    out = SrnlFfn(h.value, cfg)
+    out._dim, out._hidden, out._dtype = c.dim, c.hidden, _torch_dtype(c.act_dtype)
+    return out
+
+
+def _ffn_weights(h: SrnlFfn, t: Optional[Dict], where: str) -> _FfnWeights:
+    n, t = h._dim * h._hidden, t or {}
+    return _FfnWeights(*[_dense(t.get(k), where, k, h._dtype, n) for k in FFN_KEYS])
+
+
+def srnl_ffn_forward(h: SrnlFfn, x, params: Dict, y, res=None, gate=None, up=None, stream=None) -> None:
+    """y <- (act(x W_gate^T) * (x W_up^T)) W_down^T (+ res).  x, y, res: bf16 CUDA tensors
+    [..., dim]; params: W_gate, W_up [hidden, dim], W_down [dim, hidden] in bf16; gate, up
+    [rows, hidden] keep the pre-activations for the backward pass when given."""
+    w, hd, dt = "srnl_ffn_forward", h.handle, h._dtype
+    rows = x.numel() // h._dim
+    n, f = rows * h._dim, rows * h._hidden
+    p = _ffn_weights(h, params, w)
+    h._check(load_library().srnl_ffn_forward(
+        hd, _dense(x, w, "x", dt, n), ctypes.byref(p), _dense(res, w, "res", dt, n), _dense(y, w, "y", dt, n),
+        _dense(gate, w, "gate", dt, f), _dense(up, w, "up", dt, f), rows, _stream(stream)), w)
+
+
+def srnl_ffn_backward(h: SrnlFfn, x, gate, up, dy, params: Dict, dx, grads: Optional[Dict] = None, stream=None) -> None:
+    """dx <- dL/dx for upstream dy (dx None skips it); ``grads`` maps any of FFN_KEYS to bf16
+    CUDA tensors in the weights' layouts, which are overwritten.  gate, up: the forward's."""
+    w, hd, dt = "srnl_ffn_backward", h.handle, h._dtype
+    rows = x.numel() // h._dim
+    n, f = rows * h._dim, rows * h._hidden
+    p, g = _ffn_weights(h, params, w), _ffn_weights(h, grads, w)
+    h._check(load_library().srnl_ffn_backward(
+        hd, _dense(x, w, "x", dt, n), _dense(gate, w, "gate", dt, f), _dense(up, w, "up", dt, f),
+        _dense(dy, w, "dy", dt, n), ctypes.byref(p), _dense(dx, w, "dx", dt, n), ctypes.byref(g), rows,
+        _stream(stream)), w)
+
+
+def srnl_ffn_device_status(h: SrnlFfn) -> None:
+    """Raise SrnlError if a bounded in-kernel wait of this handle ever gave up."""
+    h._check(load_library().srnl_ffn_device_status(h.handle), "srnl_ffn_device_status")

@@ -1,0 +1,664 @@
+// Gated feed-forward branch with its backward pass (sm_100a), bf16 with fp32 accumulation, for
+// training and serving the layers around the SRNL operator.
+//
+//   gate = x Wg^T, up = x Wu^T, h = act(gate) * up, y = h Wd^T + res
+//   dh = dy Wd, dgate = dh * up * act'(gate), dup = dh * act(gate),
+//   dx = dgate Wg + dup Wu, dWg = dgate^T x, dWu = dup^T x, dWd = dy^T h
+//
+// One matrix-product kernel serves all six products; what differs is which way its operands
+// lie and what its epilogue does:
+//   kGlu      both projections of a 256-token x 128-channel tile at once: Wg's rows are the first
+//             half of the product's N and Wu's the second, so act(gate) * up is formed from two
+//             accumulators of the same thread, and neither projection is written unless asked
+//   kPlain    (+ res), to bf16: y, dx (its K runs over dgate Wg, then dup Wu) and the weights'
+//             gradients (both operands read as they lie, tokens along K)
+//   kGluBack  dh stays in TMEM: the epilogue reads gate and up and writes dgate, dup and h
+//
+// The kernel is persistent; a pair of CTAs (cta_group::2) makes 256 x BN tiles.  In each CTA one
+// thread fills a ring of 64-wide K stages by TMA (128-byte swizzle; a ragged edge reads as
+// zeros), one thread of the leading CTA issues the products into one of two accumulators in
+// TMEM, and eight warps empty the other.  Results leave by TMA from per-warp staging tiles,
+// which clips them at the edges.
+//
+// Roundings: h, dgate and dup are rounded to bf16 between the products, as the tensor cores
+// take them; everything else is rounded once, on output.  gate and up are kept in bf16 for the
+// backward pass, whose definition takes them so.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+#include <mutex>
+#include <new>
+
+#include "srnl_common.cuh"
+#include "srnl_internal.h"
+#include "srnl_scan.h"
+#include "srnl_tma.cuh"
+#include "srnl_umma.cuh"
+
+namespace srnl {
+
+TensorMapEncoder ffn_tensor_map_encoder() {
+  static TensorMapEncoder enc = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      enc = reinterpret_cast<TensorMapEncoder>(fn);
+  });
+  return enc;
+}
+
+namespace {
+
+constexpr int kTileM = 256;        // rows of a pair's tile (128 per CTA)
+constexpr int kTileK = 64;         // K per stage
+constexpr int kEpiWarps = 8;
+constexpr int kFfnThreads = 32 * (4 + kEpiWarps);
+constexpr int kBox = 4096;         // a warp's staging tile: 32 rows x 64 bf16
+constexpr uint32_t kABytes = 128 * kTileK * 2;
+
+enum Epi { kPlain = 0, kGlu = 1, kGluBack = 2 };
+
+// Staging tiles per warp and ring stages: what the epilogue has in flight against how far the
+// loads run ahead, within 227 KB.
+__host__ __device__ constexpr int epi_boxes(int epi) { return epi == kGluBack ? 3 : 2; }
+__host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + (uint32_t)(bn / 2) * kTileK * 2; }
+__host__ __device__ constexpr int ring_stages(int epi, int bn) {
+  return (int)((226 * 1024 - 2048 - kEpiWarps * epi_boxes(epi) * kBox) / stage_bytes(bn));
+}
+constexpr size_t ffn_smem(int epi, int bn) {
+  return 1024 + (size_t)ring_stages(epi, bn) * stage_bytes(bn) + kEpiWarps * epi_boxes(epi) * kBox + 512;
+}
+
+struct FfnMaps {
+  CUtensorMap a[2], b[2], o[3];
+};
+
+struct FfnArgs {
+  int M, N;              // of the output (of one of two stacked outputs)
+  int k0, k1;            // stages of the first and of the second operand pair
+  int tiles_m, tiles_n;  // of all outputs
+  int stack;             // tiles_m of the first of two stacked outputs (0: one output)
+  int act, save;
+  const __nv_bfloat16 *res, *gate, *up;
+  int* err;
+};
+
+__device__ __forceinline__ void act_value(float v, int act, float& f) {
+  if (act == SRNL_ACT_SILU) f = __fdividef(v, 1.f + __expf(-v));
+  else f = 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
+}
+
+__device__ __forceinline__ void act_grad(float v, int act, float& f, float& df) {
+  if (act == SRNL_ACT_SILU) {
+    const float p = __fdividef(1.f, 1.f + __expf(-v));
+    f = v * p;
+    df = fmaf(f, 1.f - p, p);
+  } else {
+    const float p = 0.5f * (1.f + erff(v * 0.70710678118654752f));
+    f = v * p;
+    df = fmaf(v * 0.3989422804014327f, __expf(-0.5f * v * v), p);
+  }
+}
+
+// Tiles in bands of 8 along M, M fastest within a band: the pairs that run together share their
+// operands' rows in L2.
+__device__ __forceinline__ void tile_of(int t, const FfnArgs& a, int& tm, int& tn) {
+  constexpr int kBand = 8;
+  const int band = t / (kBand * a.tiles_n), first = band * kBand;
+  const int rows = min(kBand, a.tiles_m - first), in = t - band * kBand * a.tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+// 8 bf16 of a row as fp32; zeros past the row's end.
+__device__ __forceinline__ uint4 load8_row(const __nv_bfloat16* p, bool on) {
+  return on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <bool AMN, bool BMN, int EPI, int BN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
+    ffn_product_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs args) {
+  constexpr int S = ring_stages(EPI, BN);
+  constexpr uint32_t kStage = stage_bytes(BN);
+  constexpr int kBRows = BN / 2;   // of B per CTA
+  constexpr int kHalf = BN / 2;    // accumulator columns per epilogue half
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  unsigned char* boxes = smem + S * kStage;
+  unsigned long long* bars = reinterpret_cast<unsigned long long*>(boxes + kEpiWarps * epi_boxes(EPI) * kBox);
+  unsigned long long *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = bars + 2 * S + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 4);
+  int* failed = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int tiles = args.tiles_m * args.tiles_n, ktot = args.k0 + args.k1;
+
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  if (threadIdx.x == 0) {
+    *failed = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kEpiWarps);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  cluster_sync();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 1u;   // the ring starts empty
+      for (int t = pair; t < tiles; t += pairs) {
+        int tm, tn;
+        tile_of(t, args, tm, tn);
+        const int second = args.stack != 0 && tm >= args.stack;
+        const int m0 = (tm - (second ? args.stack : 0)) * kTileM + (int)rank * 128;
+        const int n0 = EPI == kGlu ? tn * (BN / 2) : tn * BN + (int)rank * kBRows;
+        for (int it = 0; it < ktot; ++it) {
+          const int two = it >= args.k0;
+          const int k = (it - (two ? args.k0 : 0)) * kTileK;
+          const CUtensorMap* am = &maps.a[args.stack != 0 ? second : two];
+          const CUtensorMap* bm = &maps.b[EPI == kGlu ? (int)rank : two];
+          mbar_wait(&empty[s], ph, failed);
+          if (*reinterpret_cast<volatile int*>(failed)) break;
+          if (rank == 0) mbar_expect(&full[s], 2 * kStage);
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
+          const uint32_t as = smem_u32(smem + s * kStage), bs = as + kABytes;
+          if constexpr (AMN) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tma_load_pair(as + i * 8192, am, m0 + 64 * i, k, bar);
+          } else {
+            tma_load_pair(as, am, k, m0, bar);
+          }
+          if constexpr (BMN) {
+#pragma unroll
+            for (int i = 0; i < kBRows / 64; ++i) tma_load_pair(bs + i * 8192, bm, n0 + 64 * i, k, bar);
+          } else {
+            tma_load_pair(bs, bm, k, n0, bar);
+          }
+          if (++s == S) { s = 0; ph ^= 1u; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_mn(kTileM, BN, AMN, BMN);
+      int s = 0, buf = 0;
+      uint32_t ph = 0u, tph = 1u;   // the accumulators start empty
+      for (int t = pair; t < tiles; t += pairs) {
+        mbar_wait(&tempty[buf], tph, failed);
+        const uint32_t acc = tmem + (uint32_t)(buf * BN);
+        for (int it = 0; it < ktot; ++it) {
+          mbar_wait(&full[s], ph, failed);
+          if (*reinterpret_cast<volatile int*>(failed)) break;
+          const uint32_t as = smem_u32(smem + s * kStage), bs = as + kABytes;
+          const uint64_t ad = AMN ? desc_mn_major(as, 8192) : desc_k_major(as);
+          const uint64_t bd = BMN ? desc_mn_major(bs, 8192) : desc_k_major(bs);
+#pragma unroll
+          for (int k = 0; k < kTileK / 16; ++k)
+            mma_pair(acc, ad + (uint64_t)(k * (AMN ? 2048 : 32) >> 4), bd + (uint64_t)(k * (BMN ? 2048 : 32) >> 4),
+                     idesc, it > 0 || k > 0);
+          mma_commit_pair(&empty[s]);
+          if (++s == S) { s = 0; ph ^= 1u; }
+        }
+        mma_commit_pair(&tfull[buf]);
+        if (++buf == 2) { buf = 0; tph ^= 1u; }
+      }
+    }
+  } else if (warp >= 4) {
+    const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
+    unsigned char* box = boxes + ew * epi_boxes(EPI) * kBox;
+    const uint32_t done = map_rank(smem_u32(tempty), 0);
+    int buf = 0, turn = 0;
+    uint32_t ph = 0u;
+    // bf16 pairs of 32 columns into a staging tile's columns 32 c .. : 16-byte units, swizzled
+    auto stage32 = [&](unsigned char* b, int c, const uint32_t (&w)[16]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<uint4*>(b + lane * 128 + (((4 * c + j) ^ (lane & 7)) << 4)) =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    };
+    // hand a staging tile to the TMA; tiles wholly past an edge are not sent
+    auto send = [&](const CUtensorMap* map, unsigned char* b, int col, int row) {
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        if (col < args.N && row < args.M) tma_store(map, smem_u32(b), col, row);
+        bulk_commit();
+      }
+    };
+    auto reuse = [&]() {   // the tile about to be written has left
+      if (lane == 0) bulk_wait_read<EPI == kGluBack ? 0 : 1>();
+      __syncwarp();
+    };
+    for (int t = pair; t < tiles; t += pairs) {
+      int tm, tn;
+      tile_of(t, args, tm, tn);
+      const int second = args.stack != 0 && tm >= args.stack;
+      const int row0 = (tm - (second ? args.stack : 0)) * kTileM + (int)rank * 128 + quarter * 32;
+      const int row = row0 + lane;
+      const uint32_t acc = tmem + (uint32_t)(buf * BN) + ((uint32_t)(32 * quarter) << 16);
+      mbar_wait(&tfull[buf], ph, failed);
+      if constexpr (EPI == kGlu) {
+        // this half's 64 hidden channels: gate in columns 64 half .., up 128 further
+        const int c0 = tn * (BN / 2) + half * 64;
+        for (int o = 0; o < (args.save ? 3 : 1); ++o) {
+          unsigned char* b = box + (turn & 1) * kBox;
+          reuse();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float g[32], u[32];
+            uint32_t w[16];
+            if (o != 2) tmem_ld32(g, acc + half * 64 + 32 * c);
+            if (o != 1) tmem_ld32(u, acc + kHalf + half * 64 + 32 * c);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (o == 0) {
+                float a, d;
+                act_value(g[2 * i], args.act, a);
+                act_value(g[2 * i + 1], args.act, d);
+                w[i] = pack_bf16(a * u[2 * i], d * u[2 * i + 1]);
+              } else {
+                w[i] = o == 1 ? pack_bf16(g[2 * i], g[2 * i + 1]) : pack_bf16(u[2 * i], u[2 * i + 1]);
+              }
+            }
+            stage32(b, c, w);
+          }
+          send(&maps.o[o], b, c0, row0);
+          ++turn;
+        }
+      } else {
+#pragma unroll 1
+        for (int cb = 0; cb < kHalf / 64; ++cb) {
+          const int col = tn * BN + half * kHalf + cb * 64;
+          unsigned char* b = box + (EPI == kGluBack ? 0 : (turn & 1) * kBox);
+          reuse();
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float v[32];
+            uint32_t w[16];
+            const int64_t at = (int64_t)row * args.N + col + 32 * c;
+            if constexpr (EPI == kPlain) {
+              tmem_ld32(v, acc + half * kHalf + cb * 64 + 32 * c);
+              uint4 r[4];
+              if (args.res != nullptr)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = load8_row(args.res + at + 8 * j, row < args.M && col + 32 * c + 8 * j < args.N);
+              tmem_wait_ld();
+              if (args.res != nullptr) {
+                const uint32_t* rw = reinterpret_cast<const uint32_t*>(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  v[2 * i] += bf16_lo(rw[i]);
+                  v[2 * i + 1] += bf16_hi(rw[i]);
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+              stage32(b, c, w);
+            } else {
+              uint4 gr[4], ur[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const bool on = row < args.M && col + 32 * c + 8 * j < args.N;
+                gr[j] = load8_row(args.gate + at + 8 * j, on);
+                ur[j] = load8_row(args.up + at + 8 * j, on);
+              }
+              tmem_ld32(v, acc + half * kHalf + cb * 64 + 32 * c);
+              tmem_wait_ld();
+              const uint32_t* gw = reinterpret_cast<const uint32_t*>(gr);
+              const uint32_t* uw = reinterpret_cast<const uint32_t*>(ur);
+              uint32_t wu[16], wh[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float f0, d0, f1, d1;
+                act_grad(bf16_lo(gw[i]), args.act, f0, d0);
+                act_grad(bf16_hi(gw[i]), args.act, f1, d1);
+                const float u0 = bf16_lo(uw[i]), u1 = bf16_hi(uw[i]);
+                w[i] = pack_bf16(v[2 * i] * u0 * d0, v[2 * i + 1] * u1 * d1);
+                wu[i] = pack_bf16(v[2 * i] * f0, v[2 * i + 1] * f1);
+                wh[i] = pack_bf16(f0 * u0, f1 * u1);
+              }
+              stage32(b, c, w);
+              stage32(b + kBox, c, wu);
+              stage32(b + 2 * kBox, c, wh);
+            }
+          }
+          if constexpr (EPI == kPlain) {
+            send(&maps.o[second], b, col, row0);
+          } else {
+            send(&maps.o[0], b, col, row0);
+            send(&maps.o[1], b + kBox, col, row0);
+            send(&maps.o[2], b + 2 * kBox, col, row0);
+          }
+          ++turn;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(done + (uint32_t)buf * 8);
+      if (++buf == 2) { buf = 0; ph ^= 1u; }
+    }
+    if (lane == 0) bulk_wait_all();
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(failed)) {   // a wait gave up: let the copies in flight land, then report
+    if (threadIdx.x == 0) atomicExch(args.err, SRNL_E_TIMEOUT);
+    const unsigned long long t0 = global_ns();
+    for (int i = 0; i < (1 << 20) && global_ns() - t0 < 1000000ull; ++i) {}
+  }
+  cluster_sync();   // neither CTA leaves while the other may still signal it
+  if (warp == 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+// ------------------------------------------------------------------ host side
+// bf16 [outer][inner] row-major, boxes of 64 inner values x `rows`.
+bool ffn_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int rows) {
+  const TensorMapEncoder enc = ffn_tensor_map_encoder();
+  const cuuint64_t dim[2] = {(cuuint64_t)inner, (cuuint64_t)outer}, str[1] = {(cuuint64_t)inner * 2};
+  const cuuint32_t box[2] = {64u, (cuuint32_t)rows}, est[2] = {1u, 1u};
+  return enc != nullptr &&
+         enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, str, box, est,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int ceil_div(int64_t a, int b) { return (int)((a + b - 1) / b); }
+
+template <bool AMN, bool BMN, int EPI, int BN>
+cudaError_t launch_product(const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
+  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
+  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+  ffn_product_kernel<AMN, BMN, EPI, BN><<<2 * pairs, kFfnThreads, ffn_smem(EPI, BN), s>>>(maps, a);
+  return cudaGetLastError();
+}
+
+template <bool AMN, bool BMN, int EPI, int BN>
+cudaError_t prepare_product() {
+  return cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)ffn_smem(EPI, BN));
+}
+
+}  // namespace
+}  // namespace srnl
+
+// ------------------------------------------------------------------ C ABI
+struct srnl_ffn {
+  srnl_ffn_config cfg{};
+  int device = 0, sms = 0;
+  // workspace, bf16 [max_rows][hidden]: the branch's hidden rows; in training also dgate, dup
+  __nv_bfloat16 *hid = nullptr, *dgate = nullptr, *dup = nullptr;
+  int* dev_err = nullptr;
+  char err[256] = "";
+};
+
+namespace {
+
+using bf16 = __nv_bfloat16;
+thread_local char g_ffn_create_error[256] = "";
+
+srnl_status ffn_fail(srnl_ffn* h, srnl_status st, const char* msg) {
+  snprintf(h != nullptr ? h->err : g_ffn_create_error, 256, "%s", msg);
+  return st;
+}
+
+srnl_status ffn_cuda_fail(srnl_ffn* h, cudaError_t e, const char* what) {
+  char msg[256];
+  snprintf(msg, sizeof msg, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+  return ffn_fail(h, e == cudaErrorMemoryAllocation ? SRNL_E_NOMEM : SRNL_E_CUDA, msg);
+}
+
+void ffn_free(srnl_ffn* h) {
+  void* ptrs[] = {h->hid, h->dgate, h->dup, h->dev_err};
+  for (void* p : ptrs)
+    if (p != nullptr) cudaFree(p);
+}
+
+struct Span {
+  const void* p;
+  size_t n;
+  const char* name;
+};
+
+// Alignment of every given buffer, and no output over an input or another output.
+srnl_status ffn_check(srnl_ffn* h, const Span* in, int ni, const Span* out, int no) {
+  char msg[256];
+  auto over = [](const Span& a, const Span& b) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && x < y + b.n && y < x + a.n;
+  };
+  for (int i = 0; i < ni + no; ++i) {
+    const Span& s = i < ni ? in[i] : out[i - ni];
+    if (reinterpret_cast<uintptr_t>(s.p) & 15u) {
+      snprintf(msg, sizeof msg, "%s must be 16-byte aligned", s.name);
+      return ffn_fail(h, SRNL_E_INVAL, msg);
+    }
+  }
+  for (int i = 0; i < no; ++i)
+    for (int j = 0; j < ni + i; ++j) {
+      const Span& s = j < ni ? in[j] : out[j - ni];
+      if (over(out[i], s)) {
+        snprintf(msg, sizeof msg, "%s overlaps %s", out[i].name, s.name);
+        return ffn_fail(h, SRNL_E_INVAL, msg);
+      }
+    }
+  int cur = -1;
+  const cudaError_t e = cudaGetDevice(&cur);
+  if (e != cudaSuccess) return ffn_cuda_fail(h, e, "cudaGetDevice");
+  if (cur != h->device) return ffn_fail(h, SRNL_E_INVAL, "the current device is not the handle's device");
+  return SRNL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg) {
+  using namespace srnl;
+  if (out == nullptr) return ffn_fail(nullptr, SRNL_E_INVAL, "out is NULL");
+  *out = nullptr;
+  if (cfg == nullptr) return ffn_fail(nullptr, SRNL_E_INVAL, "cfg is NULL");
+  if (cfg->dim <= 0 || cfg->hidden <= 0 || cfg->max_rows <= 0)
+    return ffn_fail(nullptr, SRNL_E_INVAL, "dim, hidden and max_rows must be positive");
+  if (cfg->activation != SRNL_ACT_SILU && cfg->activation != SRNL_ACT_GELU)
+    return ffn_fail(nullptr, SRNL_E_INVAL, "activation must be SRNL_ACT_SILU or SRNL_ACT_GELU");
+  if (cfg->act_dtype != SRNL_BF16) return ffn_fail(nullptr, SRNL_E_UNSUPPORTED, "the branch takes bf16 activations");
+  if (cfg->dim % 8 != 0 || cfg->hidden % 8 != 0)
+    return ffn_fail(nullptr, SRNL_E_UNSUPPORTED, "dim and hidden must be multiples of 8");
+  if (cfg->dim > 65536 || cfg->hidden > 65536)
+    return ffn_fail(nullptr, SRNL_E_UNSUPPORTED, "dim and hidden must be at most 65536");
+  if (cfg->max_rows > (1 << 24)) return ffn_fail(nullptr, SRNL_E_UNSUPPORTED, "max_rows must be at most 2^24");
+  srnl_ffn* h = new (std::nothrow) srnl_ffn;
+  if (h == nullptr) return ffn_fail(nullptr, SRNL_E_NOMEM, "host allocation failed");
+  h->cfg = *cfg;
+  const size_t bytes = (size_t)cfg->max_rows * cfg->hidden * 2;
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
+  if (e == cudaSuccess) e = cudaMalloc(&h->hid, bytes);
+  if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dgate, bytes);
+  if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dup, bytes);
+  if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
+  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kPlain, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kPlain, 256>();
+  if (e == cudaSuccess) e = prepare_product<true, true, kPlain, 256>();
+  if (e == cudaSuccess && ffn_tensor_map_encoder() == nullptr) e = cudaErrorNotSupported;
+  if (e != cudaSuccess) {
+    const srnl_status st = ffn_cuda_fail(nullptr, e, "feed-forward create");
+    ffn_free(h);
+    delete h;
+    return st;
+  }
+  *out = h;
+  return SRNL_OK;
+}
+
+srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* p, const void* res, void* y,
+                             void* gate, void* up, int rows, void* stream) {
+  using namespace srnl;
+  if (h == nullptr) return ffn_fail(nullptr, SRNL_E_INVAL, "handle is NULL");
+  h->err[0] = 0;
+  const srnl_ffn_config& c = h->cfg;
+  if (rows < 0 || rows > c.max_rows) return ffn_fail(h, SRNL_E_INVAL, "rows must be between 0 and max_rows");
+  if (rows == 0) return SRNL_OK;
+  if (x == nullptr || y == nullptr || p == nullptr || p->W_gate == nullptr || p->W_up == nullptr || p->W_down == nullptr)
+    return ffn_fail(h, SRNL_E_INVAL, "x, y or a weight is NULL");
+  if ((gate == nullptr) != (up == nullptr)) return ffn_fail(h, SRNL_E_INVAL, "gate and up are kept together or not at all");
+  const int64_t M = rows, D = c.dim, F = c.hidden;
+  const size_t nx = (size_t)M * D * 2, nf = (size_t)M * F * 2, nw = (size_t)D * F * 2;
+  const Span in[] = {{x, nx, "x"}, {p->W_gate, nw, "W_gate"}, {p->W_up, nw, "W_up"}, {p->W_down, nw, "W_down"}, {res, nx, "res"}};
+  const Span out[] = {{y, nx, "y"}, {gate, nf, "gate"}, {up, nf, "up"}};
+  const srnl_status st = ffn_check(h, in, 5, out, 3);
+  if (st != SRNL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  FfnMaps m;
+  memset(&m, 0, sizeof m);
+  FfnArgs a{};
+  a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
+  a.tiles_m = ceil_div(M, kTileM); a.tiles_n = ceil_div(F, 128);
+  a.act = c.activation; a.save = gate != nullptr; a.err = h->dev_err;
+  bool ok = ffn_map(&m.a[0], x, D, M, 128) && ffn_map(&m.b[0], p->W_gate, D, F, 128) &&
+            ffn_map(&m.b[1], p->W_up, D, F, 128) && ffn_map(&m.o[0], h->hid, F, M, 32) &&
+            (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32) && ffn_map(&m.o[2], up, F, M, 32)));
+  if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+  cudaError_t e = launch_product<false, false, kGlu, 256>(m, a, h->sms, s);
+  if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward projections launch");
+  FfnArgs b{};
+  b.M = rows; b.N = (int)D; b.k0 = ceil_div(F, kTileK);
+  b.tiles_m = a.tiles_m; b.tiles_n = ceil_div(D, 256);
+  b.res = static_cast<const bf16*>(res); b.err = h->dev_err;
+  ok = ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, 128) && ffn_map(&m.o[0], y, D, M, 32);
+  if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+  e = launch_product<false, false, kPlain, 256>(m, b, h->sms, s);
+  return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward output launch");
+}
+
+srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, const void* up, const void* dy,
+                              const srnl_ffn_params* p, void* dx, const srnl_ffn_grads* grads, int rows, void* stream) {
+  using namespace srnl;
+  if (h == nullptr) return ffn_fail(nullptr, SRNL_E_INVAL, "handle is NULL");
+  h->err[0] = 0;
+  const srnl_ffn_config& c = h->cfg;
+  if (!c.training) return ffn_fail(h, SRNL_E_INVAL, "the backward pass needs a handle created with training set");
+  if (rows < 0 || rows > c.max_rows) return ffn_fail(h, SRNL_E_INVAL, "rows must be between 0 and max_rows");
+  srnl_ffn_grads g{};
+  if (grads != nullptr) g = *grads;
+  const int64_t M = rows, D = c.dim, F = c.hidden;
+  const size_t nx = (size_t)M * D * 2, nf = (size_t)M * F * 2, nw = (size_t)D * F * 2;
+  if (rows > 0 && (x == nullptr || gate == nullptr || up == nullptr || dy == nullptr || p == nullptr ||
+                   p->W_gate == nullptr || p->W_up == nullptr || p->W_down == nullptr))
+    return ffn_fail(h, SRNL_E_INVAL, "x, gate, up, dy or a weight is NULL");
+  srnl_ffn_params w{};
+  if (p != nullptr) w = *p;
+  const Span in[] = {{x, nx, "x"}, {gate, nf, "gate"}, {up, nf, "up"}, {dy, nx, "dy"},
+                     {w.W_gate, nw, "W_gate"}, {w.W_up, nw, "W_up"}, {w.W_down, nw, "W_down"}};
+  const Span out[] = {{dx, nx, "dx"}, {g.W_gate, nw, "grads.W_gate"}, {g.W_up, nw, "grads.W_up"}, {g.W_down, nw, "grads.W_down"}};
+  const srnl_status st = ffn_check(h, in, 7, out, 4);
+  if (st != SRNL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {   // sums over no tokens
+    void* const outs[] = {g.W_gate, g.W_up, g.W_down};
+    for (void* o : outs) {
+      const cudaError_t e = o != nullptr ? cudaMemsetAsync(o, 0, nw, s) : cudaSuccess;
+      if (e != cudaSuccess) return ffn_cuda_fail(h, e, "gradient reset");
+    }
+    return SRNL_OK;
+  }
+  if (dx == nullptr && g.W_gate == nullptr && g.W_up == nullptr && g.W_down == nullptr) return SRNL_OK;
+  FfnMaps m;
+  memset(&m, 0, sizeof m);
+  // dgate, dup and h from dh = dy Wd
+  FfnArgs a{};
+  a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
+  a.tiles_m = ceil_div(M, kTileM); a.tiles_n = ceil_div(F, 256);
+  a.act = c.activation; a.err = h->dev_err;
+  a.gate = static_cast<const bf16*>(gate); a.up = static_cast<const bf16*>(up);
+  bool ok = ffn_map(&m.a[0], dy, D, M, 128) && ffn_map(&m.b[0], w.W_down, F, D, 64) &&
+            ffn_map(&m.o[0], h->dgate, F, M, 32) && ffn_map(&m.o[1], h->dup, F, M, 32) && ffn_map(&m.o[2], h->hid, F, M, 32);
+  if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+  cudaError_t e = launch_product<false, true, kGluBack, 256>(m, a, h->sms, s);
+  if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward backward launch");
+  if (dx != nullptr) {
+    FfnArgs b{};
+    b.M = rows; b.N = (int)D; b.k0 = b.k1 = ceil_div(F, kTileK);
+    b.tiles_m = a.tiles_m; b.tiles_n = ceil_div(D, 256); b.err = h->dev_err;
+    ok = ffn_map(&m.a[0], h->dgate, F, M, 128) && ffn_map(&m.a[1], h->dup, F, M, 128) &&
+         ffn_map(&m.b[0], w.W_gate, D, F, 64) && ffn_map(&m.b[1], w.W_up, D, F, 64) && ffn_map(&m.o[0], dx, D, M, 32);
+    if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+    e = launch_product<false, true, kPlain, 256>(m, b, h->sms, s);
+    if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward input gradient launch");
+  }
+  if (g.W_gate != nullptr || g.W_up != nullptr) {
+    // one launch for both: their tiles stacked along M
+    const bool both = g.W_gate != nullptr && g.W_up != nullptr;
+    const void* d0 = g.W_gate != nullptr ? h->dgate : h->dup;
+    void* o0 = g.W_gate != nullptr ? g.W_gate : g.W_up;
+    FfnArgs b{};
+    b.M = (int)F; b.N = (int)D; b.k0 = ceil_div(M, kTileK);
+    b.stack = both ? ceil_div(F, kTileM) : 0;
+    b.tiles_m = ceil_div(F, kTileM) * (both ? 2 : 1); b.tiles_n = ceil_div(D, 256); b.err = h->dev_err;
+    ok = ffn_map(&m.a[0], d0, F, M, 64) && ffn_map(&m.b[0], x, D, M, 64) && ffn_map(&m.o[0], o0, D, F, 32) &&
+         (!both || (ffn_map(&m.a[1], h->dup, F, M, 64) && ffn_map(&m.o[1], g.W_up, D, F, 32)));
+    if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+    e = launch_product<true, true, kPlain, 256>(m, b, h->sms, s);
+    if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
+  }
+  if (g.W_down != nullptr) {
+    FfnArgs b{};
+    b.M = (int)D; b.N = (int)F; b.k0 = ceil_div(M, kTileK);
+    b.tiles_m = ceil_div(D, kTileM); b.tiles_n = ceil_div(F, 256); b.err = h->dev_err;
+    ok = ffn_map(&m.a[0], dy, D, M, 64) && ffn_map(&m.b[0], h->hid, F, M, 64) && ffn_map(&m.o[0], g.W_down, F, D, 32);
+    if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+    e = launch_product<true, true, kPlain, 256>(m, b, h->sms, s);
+    if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
+  }
+  return SRNL_OK;
+}
+
+srnl_status srnl_ffn_device_status(srnl_ffn* h) {
+  if (h == nullptr) return ffn_fail(nullptr, SRNL_E_INVAL, "handle is NULL");
+  int v = 0;
+  const cudaError_t e = cudaMemcpy(&v, h->dev_err, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return ffn_cuda_fail(h, e, "status read");
+  return v == 0 ? SRNL_OK : ffn_fail(h, static_cast<srnl_status>(v), "a bounded in-kernel wait gave up");
+}
+
+const char* srnl_ffn_last_error(const srnl_ffn* h) { return h != nullptr ? h->err : g_ffn_create_error; }
+
+void srnl_ffn_destroy(srnl_ffn* h) {
+  if (h == nullptr) return;
+  int prev = -1;
+  if (cudaGetDevice(&prev) == cudaSuccess && prev != h->device) cudaSetDevice(h->device);
+  cudaDeviceSynchronize();
+  ffn_free(h);
+  if (prev >= 0 && prev != h->device) cudaSetDevice(prev);
+  delete h;
+}
+
+}  // extern "C"

@@ -36,3 +36,30 @@ def test_ln_null_arguments_fail_cleanly(lib):
     assert lib.srnl_ln_forward(*[None] * 7, 1, None) == S.SRNL_E_INVAL
     assert lib.srnl_ln_backward(*[None] * 10, 1, None) == S.SRNL_E_INVAL
     lib.srnl_ln_destroy(None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(dim=0), S.SRNL_E_INVAL),
+    (dict(hidden=-8), S.SRNL_E_INVAL),
+    (dict(max_rows=0), S.SRNL_E_INVAL),
+    (dict(activation=2), S.SRNL_E_INVAL),
+    (dict(act_dtype="f32"), S.SRNL_E_UNSUPPORTED),
+    (dict(dim=60), S.SRNL_E_UNSUPPORTED),
+    (dict(hidden=12), S.SRNL_E_UNSUPPORTED),
+    (dict(dim=65544), S.SRNL_E_UNSUPPORTED),
+    (dict(max_rows=(1 << 24) + 1), S.SRNL_E_UNSUPPORTED),
+])
+def test_ffn_create_rejects_bad_config_before_cuda(lib, bad, status):
+    with pytest.raises(S.SrnlError) as e:
+        S.srnl_ffn_create(dict(dict(dim=64, hidden=128, max_rows=4), **bad))
+    assert e.value.status == status and lib.srnl_ffn_last_error(None)
+
+
+def test_ffn_null_arguments_fail_cleanly(lib):
+    h = ctypes.c_void_p()
+    assert lib.srnl_ffn_create(None, None) == S.SRNL_E_INVAL
+    assert lib.srnl_ffn_create(ctypes.byref(h), None) == S.SRNL_E_INVAL and h.value is None
+    assert lib.srnl_ffn_forward(*[None] * 7, 1, None) == S.SRNL_E_INVAL
+    assert lib.srnl_ffn_backward(*[None] * 8, 1, None) == S.SRNL_E_INVAL
+    assert lib.srnl_ffn_device_status(None) == S.SRNL_E_INVAL
+    lib.srnl_ffn_destroy(None)
