@@ -546,6 +546,59 @@ SRNL_API const char* srnl_ffn_last_error(const srnl_ffn* h);
 /* Free the handle and its device memory.  Accepts NULL.  Synchronises the device. */
 SRNL_API void srnl_ffn_destroy(srnl_ffn* h);
 
+/* ------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the plain decayed memory beside the SRNL
+ * sequence layer, for prompts and training (chunked) and for single tokens.  Per (batch, head)
+ *   S_t = g S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t        (S d x d fp32, g the head's decay)
+ * bf16 tokens, fp32 states.  Heads are d-wide slices of a token's row, as in the sequence layer.
+ * ---------------------------------------------------------------------- */
+typedef struct srnl_lattn srnl_lattn; /* opaque; owned by the library */
+
+typedef struct {
+  int B, T;      /* sequences and tokens of a sequence (its padded length) */
+  int heads, d;  /* heads, and their width: 32, 64 or 128; B x heads at most 65535 */
+  int ld;        /* elements between tokens of q, k, v and of dq, dk, dv; 0 means heads x d.  A
+                    multiple of 8: slices of one row of a joint projection have ld = 3 heads x d */
+  int act_dtype; /* SRNL_BF16 */
+} srnl_lattn_config;
+
+/* Validate and allocate the handle and its workspace (the states between the segments that a
+ * long sequence is split into) on the CURRENT device.  decay: HOST fp32 [heads], each in
+ * (0, 1], copied.  *out is NULL on failure; the message is srnl_lattn_last_error(NULL). */
+SRNL_API srnl_status srnl_lattn_create(srnl_lattn** out, const srnl_lattn_config* cfg, const float* decay);
+
+/* Forward pass.  DEVICE pointers, 16-byte aligned: q, k, v bf16 [B][T] rows, ld elements apart;
+ * o bf16 [B][T][heads x d], dense.  lengths: int32 [B] on the device or NULL (T everywhere);
+ * a sequence's tokens from its length on are neither read nor written (a length is clamped to
+ * 0..T).  state_in: fp32 [B][heads][d][d] (rows of k, columns of v), the memory before the
+ * first token, or NULL for zeros; state_out: the memory after the last one, or NULL.  Outputs
+ * overlap neither inputs nor one another.  A NaN or infinity in a token may reach the outputs
+ * of its sequence's head from 127 tokens before it on, never other sequences or heads.
+ * Asynchronous on `stream`; calls on one handle must not overlap on the device. */
+SRNL_API srnl_status srnl_lattn_forward(srnl_lattn* h, const void* q, const void* k, const void* v, void* o,
+                                        const int* lengths, const float* state_in, float* state_out, void* stream);
+
+/* Backward pass for d_o = dL/do (dense) and, when not NULL, dstate_out = dL/dstate_out: dq, dk
+ * and dv (rows ld elements apart; tokens from a sequence's length on are left as they were)
+ * and, when not NULL, dstate_in = dL/dstate_in.  Nothing of the forward is kept: the states are
+ * formed again.  The decays are constants.  Equal inputs give equal bits.  Asynchronous. */
+SRNL_API srnl_status srnl_lattn_backward(srnl_lattn* h, const void* q, const void* k, const void* v, const void* d_o,
+                                         void* dq, void* dk, void* dv, const int* lengths, const float* state_in,
+                                         const float* dstate_out, float* dstate_in, void* stream);
+
+/* One token of each sequence: q, k, v bf16 [B] rows, ld elements apart; o bf16 [B][heads x d];
+ * state fp32 [B][heads][d][d], updated in place (the decays, then the token).  Asynchronous;
+ * reads and writes the state once. */
+SRNL_API srnl_status srnl_lattn_step(srnl_lattn* h, const void* q, const void* k, const void* v, void* o, float* state,
+                                     void* stream);
+
+/* Message for the last failure on this handle (h == NULL: the calling thread's last
+ * srnl_lattn_create failure).  Never NULL. */
+SRNL_API const char* srnl_lattn_last_error(const srnl_lattn* h);
+
+/* Free the handle and its device memory.  Accepts NULL.  Synchronises the device. */
+SRNL_API void srnl_lattn_destroy(srnl_lattn* h);
+
 #ifdef __cplusplus
 }
 #endif

@@ -42,7 +42,9 @@ EXPORTED = ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host",
             "srnl_block_destroy",
             "srnl_ln_create", "srnl_ln_forward", "srnl_ln_backward", "srnl_ln_last_error", "srnl_ln_destroy",
             "srnl_ffn_create", "srnl_ffn_forward", "srnl_ffn_backward", "srnl_ffn_device_status",
-            "srnl_ffn_last_error", "srnl_ffn_destroy")
+            "srnl_ffn_last_error", "srnl_ffn_destroy",
+            "srnl_lattn_create", "srnl_lattn_forward", "srnl_lattn_backward", "srnl_lattn_step",
+            "srnl_lattn_last_error", "srnl_lattn_destroy")
 
 
 class SrnlError(RuntimeError):
@@ -121,6 +123,10 @@ class _FfnWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in FFN_KEYS]
 
 
+class _LattnConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "heads", "d", "ld", "act_dtype")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -192,6 +198,14 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.srnl_ffn_last_error.restype = ctypes.c_char_p
     lib.srnl_ffn_destroy.argtypes = [vp]
     lib.srnl_ffn_destroy.restype = None
+    lib.srnl_lattn_create.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(_LattnConfig), vp]
+    lib.srnl_lattn_forward.argtypes = [vp] * 9
+    lib.srnl_lattn_backward.argtypes = [vp] * 13
+    lib.srnl_lattn_step.argtypes = [vp] * 7
+    lib.srnl_lattn_last_error.argtypes = [vp]
+    lib.srnl_lattn_last_error.restype = ctypes.c_char_p
+    lib.srnl_lattn_destroy.argtypes = [vp]
+    lib.srnl_lattn_destroy.restype = None
     for name in ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host", "srnl_scan_forward_noalloc",
                  "srnl_scan_route_index", "srnl_scan_gather", "srnl_scan_enable_stage_timing",
                  "srnl_scan_stage_times", "srnl_scan_device_status", "srnl_seq_create", "srnl_seq_forward",
@@ -201,7 +215,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "srnl_scan_noalloc_status", "srnl_selftest_noalloc_wait_timeout", "srnl_block_create",
                  "srnl_block_forward", "srnl_block_device_status", "srnl_ln_create", "srnl_ln_forward",
                  "srnl_ln_backward", "srnl_ffn_create", "srnl_ffn_forward", "srnl_ffn_backward",
-                 "srnl_ffn_device_status"):
+                 "srnl_ffn_device_status", "srnl_lattn_create", "srnl_lattn_forward", "srnl_lattn_backward",
+                 "srnl_lattn_step"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -723,3 +738,80 @@ def srnl_ffn_backward(h: SrnlFfn, x, gate, up, dy, params: Dict, dx, grads: Opti
 def srnl_ffn_device_status(h: SrnlFfn) -> None:
     """Raise SrnlError if a bounded in-kernel wait of this handle ever gave up."""
     h._check(load_library().srnl_ffn_device_status(h.handle), "srnl_ffn_device_status")
+
+
+class SrnlLattn(_OpHandle):
+    """Owns one ``srnl_lattn*`` handle (linear attention with a decay for each head)."""
+
+    _prefix = "srnl_lattn"
+
+    def _rows(self, t, where: str, name: str, tokens: int) -> int:
+        """Address of bf16 token rows ([tokens..., heads * d], the handle's ld elements apart)."""
+        c = self._c
+        if t is None:
+            return 0
+        D = c.heads * c.d
+        shape = (c.B, c.T, D) if tokens else (c.B, D)
+        # dimensions of size one have no stride to speak of
+        st = [s for s, n in zip(t.stride(), t.shape) if n > 1] if tuple(t.shape) == shape else None
+        want = [s for s, n in zip(((c.T * self._ld,) if tokens else ()) + (self._ld, 1), shape) if n > 1]
+        if st != want or t.dtype is not self._dtype or not t.is_cuda:
+            raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a CUDA tensor {shape} of {self._dtype} with rows "
+                                                 f"{self._ld} elements apart, got {tuple(t.shape)} {t.dtype} "
+                                                 f"{t.stride()} on {t.device}")
+        return t.data_ptr()
+
+
+def srnl_lattn_create(cfg: Dict, decay: np.ndarray) -> SrnlLattn:
+    """cfg keys: B, T, heads, d (32, 64 or 128), ld (0 = heads * d), act_dtype ("bf16").
+    decay: float32 host array [heads], each in (0, 1]."""
+    lib = load_library()
+    c = _LattnConfig(B=cfg["B"], T=cfg["T"], heads=cfg["heads"], d=cfg["d"], ld=cfg.get("ld", 0),
+                     act_dtype=_dt(cfg.get("act_dtype", "bf16")))
+    keep = np.ascontiguousarray(decay, dtype=np.float32)
+    if keep.shape != (c.heads,):
+        raise SrnlError(SRNL_E_INVAL, "srnl_lattn_create", f"decay must have the shape ({c.heads},)")
+    h = ctypes.c_void_p()
+    st = lib.srnl_lattn_create(ctypes.byref(h), ctypes.byref(c), keep.ctypes.data)
+    if st != SRNL_OK:
+        raise SrnlError(st, "srnl_lattn_create", lib.srnl_lattn_last_error(None).decode())
+    out = SrnlLattn(h.value, cfg)
+    out._c, out._ld, out._dtype = c, c.ld or c.heads * c.d, _torch_dtype(c.act_dtype)
+    return out
+
+
+def srnl_lattn_forward(h: SrnlLattn, q, k, v, o, lengths=None, state_in=None, state_out=None, stream=None) -> None:
+    """o <- linear attention of q, k, v (bf16 [B, T, heads * d], tokens ld elements apart).
+    lengths: int32 [B]; state_in, state_out: float32 [B, heads, d, d]."""
+    import torch
+    w, hd, c = "srnl_lattn_forward", h.handle, h._c
+    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, torch.float32
+    h._check(load_library().srnl_lattn_forward(
+        hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(o, w, "o", h._dtype, n),
+        _dense(lengths, w, "lengths", torch.int32, c.B), _dense(state_in, w, "state_in", f32, s),
+        _dense(state_out, w, "state_out", f32, s), _stream(stream)), w)
+
+
+def srnl_lattn_backward(h: SrnlLattn, q, k, v, do, dq, dk, dv, lengths=None, state_in=None, dstate_out=None,
+                        dstate_in=None, stream=None) -> None:
+    """dq, dk, dv <- the gradients for upstream do (dense) and dstate_out; dstate_in receives the
+    gradient of state_in when given."""
+    import torch
+    w, hd, c = "srnl_lattn_backward", h.handle, h._c
+    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, torch.float32
+    h._check(load_library().srnl_lattn_backward(
+        hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(do, w, "do", h._dtype, n),
+        h._rows(dq, w, "dq", 1), h._rows(dk, w, "dk", 1), h._rows(dv, w, "dv", 1),
+        _dense(lengths, w, "lengths", torch.int32, c.B), _dense(state_in, w, "state_in", f32, s),
+        _dense(dstate_out, w, "dstate_out", f32, s), _dense(dstate_in, w, "dstate_in", f32, s), _stream(stream)), w)
+
+
+def srnl_lattn_step(h: SrnlLattn, q, k, v, o, state, stream=None) -> None:
+    """One token of each sequence: q, k, v, o bf16 [B, heads * d]; state float32
+    [B, heads, d, d], updated in place."""
+    import torch
+    w, hd, c = "srnl_lattn_step", h.handle, h._c
+    h._check(load_library().srnl_lattn_step(
+        hd, h._rows(q, w, "q", 0), h._rows(k, w, "k", 0), h._rows(v, w, "v", 0),
+        _dense(o, w, "o", h._dtype, c.B * c.heads * c.d),
+        _dense(state, w, "state", torch.float32, c.B * c.heads * c.d * c.d), _stream(stream)), w)

@@ -63,3 +63,39 @@ def test_ffn_null_arguments_fail_cleanly(lib):
     assert lib.srnl_ffn_backward(*[None] * 8, 1, None) == S.SRNL_E_INVAL
     assert lib.srnl_ffn_device_status(None) == S.SRNL_E_INVAL
     lib.srnl_ffn_destroy(None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(B=0), S.SRNL_E_INVAL),
+    (dict(T=-1), S.SRNL_E_INVAL),
+    (dict(heads=0), S.SRNL_E_INVAL),
+    (dict(d=48), S.SRNL_E_UNSUPPORTED),
+    (dict(d=256), S.SRNL_E_UNSUPPORTED),
+    (dict(act_dtype="f32"), S.SRNL_E_UNSUPPORTED),
+    (dict(B=40000), S.SRNL_E_UNSUPPORTED),
+    (dict(T=(1 << 24) + 1), S.SRNL_E_UNSUPPORTED),
+    (dict(ld=64), S.SRNL_E_INVAL),
+    (dict(ld=132), S.SRNL_E_INVAL),
+])
+def test_lattn_create_rejects_bad_config_before_cuda(lib, bad, status):
+    cfg = dict(dict(B=2, T=8, heads=2, d=64), **bad)
+    with pytest.raises(S.SrnlError) as e:
+        S.srnl_lattn_create(cfg, [0.9] * cfg["heads"])
+    assert e.value.status == status and lib.srnl_lattn_last_error(None)
+
+
+@pytest.mark.parametrize("decay", [[0.0, 0.5], [1.5, 0.5], [0.5, float("nan")], [-0.1, 0.5], [0.5], [0.5, 0.5, 0.5]])
+def test_lattn_create_rejects_bad_decays_before_cuda(lib, decay):
+    with pytest.raises(S.SrnlError) as e:
+        S.srnl_lattn_create(dict(B=2, T=8, heads=2, d=64), decay)
+    assert e.value.status == S.SRNL_E_INVAL
+
+
+def test_lattn_null_arguments_fail_cleanly(lib):
+    h = ctypes.c_void_p()
+    assert lib.srnl_lattn_create(None, None, None) == S.SRNL_E_INVAL
+    assert lib.srnl_lattn_create(ctypes.byref(h), None, None) == S.SRNL_E_INVAL and h.value is None
+    assert lib.srnl_lattn_forward(*[None] * 9) == S.SRNL_E_INVAL
+    assert lib.srnl_lattn_backward(*[None] * 13) == S.SRNL_E_INVAL
+    assert lib.srnl_lattn_step(*[None] * 7) == S.SRNL_E_INVAL
+    lib.srnl_lattn_destroy(None)

@@ -1,0 +1,397 @@
+"""Linear attention with a decay for each head (srnl_lattn_*): prompts, gradients and single
+tokens against the definition in 64 bits, written out as a sum over all pairs of tokens.
+
+Tolerances.  half = 2^-8 bounds a bf16 rounding relative to the value.  An output is rounded
+once.  The masked a b^T of a chunk (at most the 127 tokens before and the token itself) is
+rounded: errors of zero mean and a standard deviation of at most half / sqrt(3) each, seven
+standard deviations of their sum.  The state as an operand and the rows of its update are split
+into two bf16 parts: 2^-16 of the magnitude each; fp32 sums and powers are counted as another
+half of that pair.  States are fp32: the split of the update's rows and the fp32 sums alone.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import self_referential_nested_b200 as S
+
+pytestmark = pytest.mark.gpu
+
+HALF = 2.0 ** -8
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from self_referential_nested_b200 import build
+    build.build()
+    torch.cuda.set_device(0)
+
+
+def make(B, T, H, d, seed=0, packed=False):
+    g = torch.Generator().manual_seed(seed)
+    D = H * d
+    x = torch.randn(B, T, 4, D, generator=g)
+    x[:, :, 0] *= d ** -0.5
+    x = x.to(BF).cuda()
+    t = {n: (x[:, :, i] if packed and n != "do" else x[:, :, i].contiguous()) for i, n in enumerate(("q", "k", "v", "do"))}
+    t["s0"] = torch.randn(B, H, d, d, generator=g).cuda()
+    t["ds"] = torch.randn(B, H, d, d, generator=g).cuda()
+    t["ld"] = 4 * D if packed else 0
+    return t
+
+
+def heads(x, d):
+    B, T, D = x.shape
+    return x.double().view(B, T, D // d, d).transpose(1, 2)
+
+
+def pair_sum(a, b, c, w, near):
+    """sum_j w_tj (a_t . b_j) c_j, its magnitude, and the spread of the rounded near pairs."""
+    p = (a @ b.transpose(-1, -2)) * w
+    return p @ c, ((a.abs() @ b.abs().transpose(-1, -2)) * w) @ c.abs(), ((p * near) ** 2) @ (c ** 2)
+
+
+def reference(t, decay, lens, with_s0, with_ds):
+    """{name: (value, magnitude, spread)} of o, dq, dk, dv and the states."""
+    d = t["s0"].shape[-1]
+    q, k, v, do = (heads(t[n], d) for n in ("q", "k", "v", "do"))
+    B, H, T, _ = q.shape
+    lg = torch.tensor(decay, device="cuda", dtype=torch.float64).log()
+    n = torch.tensor(lens, device="cuda")
+    i = torch.arange(T, device="cuda")
+    live = (i < n[:, None])[:, None, :, None].double()
+    q, k, v, do = (x * live for x in (q, k, v, do))
+    e = (i[:, None] - i).double()
+    w = torch.where(e >= 0, torch.exp(lg[:, None, None] * e.clamp_min(0)), 0.0)[None]
+    near = ((e >= 0) & (e < 128)).double()
+    s0 = t["s0"].double() * with_s0
+    ds = t["ds"].double() * with_ds
+    fore = torch.exp(lg[None, :, None] * (i + 1.0))[..., None]
+    back = torch.exp(lg[None, :, None] * (n[:, None, None] - 1 - i).clamp_min(0).double())[..., None]
+    whole = torch.exp(lg * n[:, None])[..., None, None]
+    wt, nt = w.transpose(-1, -2), near.t()
+
+    def plus(x, a, f, z):
+        return x[0] + (a * f) @ z, x[1] + (a.abs() * f) @ z.abs(), x[2]
+
+    out = {"o": plus(pair_sum(q, k, v, w, near), q, fore, s0),
+           "dq": plus(pair_sum(do, v, k, w, near), do, fore, s0.transpose(-1, -2)),
+           "dk": plus(pair_sum(v, do, q, wt, nt), v, back, ds.transpose(-1, -2)),
+           "dv": plus(pair_sum(k, q, do, wt, nt), k, back, ds)}
+    out = {m: tuple((y * live).transpose(1, 2).reshape(B, T, H * d) for y in x) for m, x in out.items()}
+    st = (k * back).transpose(-1, -2), (q * fore).transpose(-1, -2)
+    out["state"] = st[0] @ v + whole * s0, st[0].abs() @ v.abs() + whole * s0.abs()
+    out["dstate"] = st[1] @ do + whole * ds, st[1].abs() @ do.abs() + whole * ds.abs()
+    return out
+
+
+def within(got, ref, magnitude, spread=None):
+    assert bool(torch.isfinite(got).all())
+    tol = 1.5 * 2.0 ** -16 * magnitude if spread is None else \
+        HALF * ref.abs() + 7 * HALF / math.sqrt(3) * spread.sqrt() + 1.5 * 2.0 ** -15 * magnitude
+    worst = ((got.double() - ref).abs() / (tol + 1e-30)).max()
+    assert float(worst) <= 1, float(worst)
+
+
+CASES = [  # B, T, heads, d, lengths, packed
+    (1, 1, 1, 32, None, False), (2, 5, 3, 64, None, True), (1, 7, 2, 128, None, False),
+    (3, 64, 2, 32, [64, 0, 1], False), (3, 65, 2, 64, [65, 63, 64], True), (2, 128, 1, 128, None, True),
+    (3, 129, 2, 128, [129, 0, 128], False), (2, 300, 5, 64, [300, 299], False), (4, 333, 3, 32, [1, 333, 200, 64], True),
+    (1, 2100, 2, 64, None, False), (2, 1500, 1, 128, [1500, 700], False), (2, 1200, 2, 32, [900, 1200], True),
+    (40, 70, 4, 64, None, False),
+]
+
+
+@pytest.mark.parametrize("state", [False, True])
+@pytest.mark.parametrize("B,T,H,d,lens,packed", CASES)
+def test_forward_and_backward(B, T, H, d, lens, packed, state):
+    t = make(B, T, H, d, seed=T + d, packed=packed)
+    decay = np.array([[1.0, 0.5, 0.97, 0.999, 1e-6][i % 5] for i in range(H)], dtype=np.float32)
+    n = torch.tensor(lens, device="cuda", dtype=torch.int32) if lens else None
+    D = H * d
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d, ld=t["ld"]), decay)
+    try:
+        o = torch.full((B, T, D), 7.0, device="cuda", dtype=BF)
+        so, dsi = torch.full_like(t["s0"], 7.0), torch.full_like(t["s0"], 7.0)
+        S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=n, state_in=t["s0"] if state else None,
+                             state_out=so if state else None)
+        g = torch.full((B, T, 4, D), 7.0, device="cuda", dtype=BF)
+        dq, dk, dv = ((g[:, :, i] if packed else torch.full((B, T, D), 7.0, device="cuda", dtype=BF)) for i in range(3))
+        S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], dq, dk, dv, lengths=n,
+                              state_in=t["s0"] if state else None, dstate_out=t["ds"] if state else None,
+                              dstate_in=dsi if state else None)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    ln = lens or [T] * B
+    ref = reference(t, decay, ln, state, state)
+    for name, got in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+        for b in range(B):
+            assert bool((got[b, ln[b]:] == 7).all()), name   # rows behind a sequence stay
+            if ln[b]:
+                within(got[b, :ln[b]], *(x[b, :ln[b]] for x in ref[name]))
+    if packed:
+        assert bool((g[:, :, 3] == 7).all())
+    if state:
+        within(so, *ref["state"])
+        within(dsi, *ref["dstate"])
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_gradients_against_differences(d):
+    """The loss is bilinear in each input, so a difference over a step of one is its gradient."""
+    B, T, H = 2, 150, 2
+    t = make(B, T, H, d, seed=1)
+    decay = np.array([0.9, 0.995], dtype=np.float32)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+    try:
+        g = {n: torch.empty_like(t["q"]) for n in "qkv"}
+        g["s0"] = torch.empty_like(t["s0"])
+        S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], g["q"], g["k"], g["v"], state_in=t["s0"],
+                              dstate_out=t["ds"], dstate_in=g["s0"])
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    gen = torch.Generator().manual_seed(7)
+    for name, grad in g.items():
+        v = torch.randn(grad.shape, generator=gen).cuda().double()
+
+        def loss(s):
+            u = dict(t)
+            u[name] = t[name].double() + s * v
+            r = reference(u, decay, [T] * B, True, True)
+            return float((r["o"][0] * t["do"].double()).sum() + (r["state"][0] * t["ds"].double()).sum())
+
+        num = loss(0.5) - loss(-0.5)
+        # n independent roundings, two a value (its own, and its pairs'): seven standard deviations
+        rms = float((grad.double() * v).square().sum().sqrt())
+        rel = 7 * HALF / math.sqrt(3) * math.sqrt(2) if grad.dtype is BF else 7 * 1.5 * 2.0 ** -16
+        assert abs(num - float((grad.double() * v).sum())) <= rel * rms + 2.0 ** -15 * float((grad.double() * v).abs().sum())
+
+
+@pytest.mark.parametrize("B,H,d", [(1, 1, 32), (3, 2, 64), (2, 3, 128), (70, 4, 64)])
+def test_a_prompt_then_tokens(B, H, d):
+    """A prompt's state carried on token by token gives the longer prompt's outputs and state."""
+    T, more = 90, 5
+    t = make(B, T + more, H, d, seed=d)
+    decay = np.linspace(0.8, 1.0, H).astype(np.float32)
+    cut = {n: t[n][:, :T].contiguous() for n in "qkv"}
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+    try:
+        o, st = torch.empty(B, T, H * d, device="cuda", dtype=BF), torch.empty_like(t["s0"])
+        S.srnl_lattn_forward(h, cut["q"], cut["k"], cut["v"], o, state_in=t["s0"], state_out=st)
+        steps = []
+        for i in range(T, T + more):
+            one = torch.empty(B, H * d, device="cuda", dtype=BF)
+            S.srnl_lattn_step(h, *(t[n][:, i].contiguous() for n in "qkv"), one, st)
+            steps.append(one)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    ref = reference(t, decay, [T + more] * B, True, False)
+    within(torch.cat([o, torch.stack(steps, 1)], 1), *ref["o"])
+    within(st, *ref["state"])
+
+
+def test_step_rows_of_a_joint_projection():
+    B, H, d = 5, 2, 64
+    D = H * d
+    x = torch.randn(B, 3, D, generator=torch.Generator().manual_seed(3)).to(BF).cuda()
+    s0 = torch.randn(B, H, d, d, generator=torch.Generator().manual_seed(4)).cuda()
+    h = S.srnl_lattn_create(dict(B=B, T=1, heads=H, d=d, ld=3 * D), np.array([0.5, 1.0], np.float32))
+    try:
+        o, st = torch.empty(B, D, device="cuda", dtype=BF), s0.clone()
+        S.srnl_lattn_step(h, x[:, 0], x[:, 1], x[:, 2], o, st)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    q, k, v = (x[:, i].double().view(B, H, d) for i in range(3))
+    ref = torch.tensor([0.5, 1.0], device="cuda", dtype=torch.float64)[:, None, None] * s0.double() + k[..., None] * v[..., None, :]
+    # a product and a sum; d products and sums
+    assert bool(((st.double() - ref).abs() <= 2.0 ** -23 * (s0.double().abs() + (k[..., None] * v[..., None, :]).abs())).all())
+    out = (q[..., None] * ref).sum(2)
+    mag = (q.abs()[..., None] * ref.abs()).sum(2)
+    assert bool(((o.double().view(B, H, d) - out).abs() <= HALF * out.abs() + 2.0 ** -17 * mag).all())
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_a_sequence_touches_no_other(d):
+    B, T, H = 3, 200, 2
+    t = make(B, T, H, d, seed=11)
+    n = torch.tensor([200, 100, 150], device="cuda", dtype=torch.int32)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.array([0.9, 0.99], np.float32))
+    try:
+        def both():
+            o, g = torch.zeros_like(t["q"]), [torch.zeros_like(t["q"]) for _ in range(3)]
+            st = torch.empty_like(t["s0"])
+            S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=n, state_out=st)
+            S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], *g, lengths=n)
+            torch.cuda.synchronize()
+            return [o, *g, st]
+
+        before = both()
+        for x in "qkv":   # behind the lengths, and one head of sequence 0
+            t[x][1, 100:] = float("nan")
+            t[x][2, 150:] = float("inf")
+            t[x][0, 50, d:] = float("nan")
+        t["do"][1, 100:] = float("nan")
+        after = both()
+    finally:
+        h.close()
+    for a, b in zip(before, after):
+        assert torch.equal(a[1:], b[1:])
+        if a.dim() == 3:
+            assert torch.equal(a[0, :, :d], b[0, :, :d]) and bool(torch.isnan(b[0, 50:, d:]).any())
+
+
+def test_lengths_outside_the_range_are_clamped():
+    B, T, H, d = 2, 70, 1, 64
+    t = make(B, T, H, d, seed=2)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.array([0.9], np.float32))
+    try:
+        def go(lens):
+            o, st = torch.zeros_like(t["q"]), torch.empty_like(t["s0"])
+            S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=torch.tensor(lens, device="cuda", dtype=torch.int32),
+                                 state_in=t["s0"], state_out=st)
+            torch.cuda.synchronize()
+            return o, st
+
+        a, b = go([1 << 30, -5]), go([T, 0])
+    finally:
+        h.close()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert torch.equal(a[1][1], t["s0"][1]) and not a[0][1].any()
+
+
+def test_a_decay_next_to_one_over_a_long_sequence():
+    """g = 1 - 2^-20 over 2^18 tokens of ones: the state is a geometric sum, 2^20 (1 - g^n)."""
+    T, d = 1 << 18, 32
+    g = np.float32(1 - 2.0 ** -20)
+    one = torch.ones(1, T, d, device="cuda", dtype=BF)
+    h = S.srnl_lattn_create(dict(B=1, T=T, heads=1, d=d), np.array([g]))
+    try:
+        o, st = torch.empty_like(one), torch.empty(1, 1, d, d, device="cuda")
+        S.srnl_lattn_forward(h, one, one, one, o, state_out=st)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    G = float(g)
+    want = (1 - math.exp(T * math.log(G))) / (1 - G)
+    assert float((st.double() - want).abs().max()) <= 1.5 * 2.0 ** -16 * want
+
+
+def test_rows_beyond_32_bits():
+    """A row pitch that puts the last tokens past 2^31 elements; a short memory makes the last
+    outputs a sum over few tokens."""
+    T, d, ld = 70000, 32, 32768
+    buf = torch.zeros(1, T, ld, device="cuda", dtype=BF)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    sl = [buf[:, :, i * d:(i + 1) * d] for i in range(3)]
+    for x in sl:
+        x.copy_(torch.randn(1, T, d, device="cuda", generator=gen))
+    h = S.srnl_lattn_create(dict(B=1, T=T, heads=1, d=d, ld=ld), np.array([0.5], np.float32))
+    try:
+        o = torch.empty(1, T, d, device="cuda", dtype=BF)
+        S.srnl_lattn_forward(h, *sl, o)
+        dq, dk, dv = (buf[:, :, (i + 3) * d:(i + 4) * d] for i in range(3))
+        S.srnl_lattn_backward(h, *sl, o, dq, dk, dv)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    n = 300
+    for lo in (0, T - n):
+        t = {m: x[:, lo:lo + n] for m, x in zip("qkv", sl)}
+        t["do"] = o[:, lo:lo + n]
+        t["s0"] = t["ds"] = torch.zeros(1, 1, d, d, device="cuda")
+        ref = reference(t, [0.5], [n], False, False)
+        a, b = (0, n - 100) if lo == 0 else (100, n)   # 100 tokens away the rest is worth 2^-100
+        for name, got in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+            within(got[:, lo + a:lo + b], *(x[:, a:b] for x in ref[name]))
+
+
+@pytest.mark.parametrize("B,T,H,d", [(1, 1000, 1, 64), (2, 200, 3, 128)])
+def test_two_calls_a_stream_and_a_graph_give_equal_bits(B, T, H, d):
+    t = make(B, T, H, d, seed=9)
+    decay = np.full(H, 0.98, np.float32)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+    h2 = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+    try:
+        def step(h, stream=None):
+            outs = [torch.empty_like(t["q"]) for _ in range(4)] + [torch.empty_like(t["s0"]) for _ in range(2)]
+
+            def go():
+                S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], outs[0], state_in=t["s0"], state_out=outs[4], stream=stream)
+                S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], *outs[1:4], state_in=t["s0"],
+                                      dstate_out=t["ds"], dstate_in=outs[5], stream=stream)
+
+            return go, outs
+
+        go0, o0 = step(h)
+        go0()
+        torch.cuda.synchronize()
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        go1, o1 = step(h, s1)
+        go2, o2 = step(h2, s2)
+        go1()
+        go2()
+        torch.cuda.synchronize()
+        go3, o3 = step(h)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go3()
+        graph.replay()
+        torch.cuda.synchronize()
+        for o in (o1, o2, o3):
+            assert all(torch.equal(a, b) for a, b in zip(o, o0))
+        del graph
+    finally:
+        h.close()
+        h2.close()
+
+
+def test_refusals():
+    B, T, H, d = 2, 9, 2, 32
+    t = make(B, T, H, d)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.array([0.9, 0.9], np.float32))
+    try:
+        o = torch.empty_like(t["q"])
+
+        def refused(text, call, *a, **kw):
+            with pytest.raises(S.SrnlError) as e:
+                call(h, *a, **kw)
+            assert e.value.status == S.SRNL_E_INVAL and text in str(e.value), str(e.value)
+
+        q, k, v = t["q"], t["k"], t["v"]
+        refused("q must be", S.srnl_lattn_forward, q[:, :5], k, v, o)
+        refused("k must be", S.srnl_lattn_forward, q, k.float(), v, o)
+        refused("v must be", S.srnl_lattn_forward, q, k, make(B, T, H, d, packed=True)["v"], o)
+        refused("o must be", S.srnl_lattn_forward, q, k, v, o[:1])
+        refused("lengths must be", S.srnl_lattn_forward, q, k, v, o, lengths=torch.tensor([1, 2], device="cuda"))
+        refused("state_in must be", S.srnl_lattn_forward, q, k, v, o, state_in=t["s0"][:1])
+        refused("NULL", S.srnl_lattn_forward, q, None, v, o)
+        refused("o overlaps q", S.srnl_lattn_forward, q, k, v, q)
+        refused("state_out overlaps state_in", S.srnl_lattn_forward, q, k, v, o, state_in=t["s0"], state_out=t["s0"])
+        refused("dv overlaps dq", S.srnl_lattn_backward, q, k, v, t["do"], o, torch.empty_like(o), o)
+        refused("dk overlaps do", S.srnl_lattn_backward, q, k, v, t["do"], o, t["do"], torch.empty_like(o))
+        refused("q must be", S.srnl_lattn_step, q, k, v, o, t["s0"])
+        one = [x[:, 0].contiguous() for x in (q, k, v)]
+        refused("o overlaps q", S.srnl_lattn_step, *one, one[0], t["s0"])
+        refused("NULL", S.srnl_lattn_step, *one, torch.empty_like(one[0]), None)
+        # slices of one row do not overlap, slices that share columns do
+        x = torch.zeros(B, T, 4 * H * d, device="cuda", dtype=BF)
+        hp = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d, ld=4 * H * d), np.array([0.9, 0.9], np.float32))
+        try:
+            sl = [x[:, :, i * 16:i * 16 + H * d] for i in range(4)]
+            with pytest.raises(S.SrnlError) as e:
+                S.srnl_lattn_backward(hp, q_ := sl[0], q_, q_, t["do"], sl[1], x[:, :, 128:192], x[:, :, 192:256])
+            assert "dq overlaps q" in str(e.value)
+            S.srnl_lattn_backward(hp, q_, q_, q_, t["do"], *(x[:, :, i * 64:i * 64 + 64] for i in (1, 2, 3)))
+            torch.cuda.synchronize()
+        finally:
+            hp.close()
+    finally:
+        h.close()
