@@ -236,8 +236,9 @@ def _ptr(t) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
+        # the current stream's address without a Stream object: 0.2 us a call in place of 3.4
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -594,13 +595,14 @@ def _torch_dtype(act_dtype: int):
     return torch.bfloat16 if act_dtype == SRNL_BF16 else torch.float32
 
 
-def _dense(t, where: str, name: str, dtype, n: int) -> int:
-    """Address of a dense CUDA tensor of n values of dtype (0 for None); raises otherwise."""
+def _dense(h: "_OpHandle", t, where: str, name: str, dtype, n: int) -> int:
+    """Address of a dense tensor of n values of dtype on the handle's device (0 for None);
+    raises otherwise."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.numel() != n or not t.is_cuda or not t.is_contiguous():
-        raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a dense CUDA tensor of {n} {dtype} values, got "
-                                             f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != h._device or not t.is_contiguous():
+        raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a dense CUDA tensor of {n} {dtype} values on device "
+                                             f"{h._device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
@@ -610,8 +612,11 @@ class _OpHandle:
     _prefix = ""
 
     def __init__(self, handle: int, cfg: Dict):
+        import torch
         self._h = handle
         self.cfg = dict(cfg)
+        self._device = torch.cuda.current_device()   # where create allocated
+        self._f32, self._i32 = torch.float32, torch.int32
 
     @property
     def handle(self) -> int:
@@ -657,27 +662,25 @@ def srnl_ln_create(cfg: Dict) -> SrnlLn:
 def srnl_ln_forward(h: SrnlLn, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:
     """y <- layer norm of x ([..., dim] CUDA tensors of the handle's act dtype; gamma, beta
     float32 [dim]); mean, rstd: float32 [rows], written when given."""
-    import torch
-    w, hd, d, f32 = "srnl_ln_forward", h.handle, h._dim, torch.float32
+    w, hd, d, f32 = "srnl_ln_forward", h.handle, h._dim, h._f32
     rows = x.numel() // d
     n = rows * d
     h._check(load_library().srnl_ln_forward(
-        hd, _dense(x, w, "x", h._dtype, n), _dense(gamma, w, "gamma", f32, d), _dense(beta, w, "beta", f32, d),
-        _dense(y, w, "y", h._dtype, n), _dense(mean, w, "mean", f32, rows), _dense(rstd, w, "rstd", f32, rows), rows,
+        hd, _dense(h, x, w, "x", h._dtype, n), _dense(h, gamma, w, "gamma", f32, d), _dense(h, beta, w, "beta", f32, d),
+        _dense(h, y, w, "y", h._dtype, n), _dense(h, mean, w, "mean", f32, rows), _dense(h, rstd, w, "rstd", f32, rows), rows,
         _stream(stream)), w)
 
 
 def srnl_ln_backward(h: SrnlLn, x, dy, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None) -> None:
     """dx <- dL/dx for upstream dy (+ dres when given); dgamma, dbeta (float32 [dim]) are
     overwritten when given.  mean, rstd: the forward's."""
-    import torch
-    w, hd, d, f32 = "srnl_ln_backward", h.handle, h._dim, torch.float32
+    w, hd, d, f32 = "srnl_ln_backward", h.handle, h._dim, h._f32
     rows = x.numel() // d
     n = rows * d
     h._check(load_library().srnl_ln_backward(
-        hd, _dense(x, w, "x", h._dtype, n), _dense(dy, w, "dy", h._dtype, n), _dense(dres, w, "dres", h._dtype, n),
-        _dense(gamma, w, "gamma", f32, d), _dense(mean, w, "mean", f32, rows), _dense(rstd, w, "rstd", f32, rows),
-        _dense(dx, w, "dx", h._dtype, n), _dense(dgamma, w, "dgamma", f32, d), _dense(dbeta, w, "dbeta", f32, d), rows,
+        hd, _dense(h, x, w, "x", h._dtype, n), _dense(h, dy, w, "dy", h._dtype, n), _dense(h, dres, w, "dres", h._dtype, n),
+        _dense(h, gamma, w, "gamma", f32, d), _dense(h, mean, w, "mean", f32, rows), _dense(h, rstd, w, "rstd", f32, rows),
+        _dense(h, dx, w, "dx", h._dtype, n), _dense(h, dgamma, w, "dgamma", f32, d), _dense(h, dbeta, w, "dbeta", f32, d), rows,
         _stream(stream)), w)
 
 
@@ -706,7 +709,7 @@ def srnl_ffn_create(cfg: Dict) -> SrnlFfn:
 
 def _ffn_weights(h: SrnlFfn, t: Optional[Dict], where: str) -> _FfnWeights:
     n, t = h._dim * h._hidden, t or {}
-    return _FfnWeights(*[_dense(t.get(k), where, k, h._dtype, n) for k in FFN_KEYS])
+    return _FfnWeights(*[_dense(h, t.get(k), where, k, h._dtype, n) for k in FFN_KEYS])
 
 
 def srnl_ffn_forward(h: SrnlFfn, x, params: Dict, y, res=None, gate=None, up=None, stream=None) -> None:
@@ -718,8 +721,8 @@ def srnl_ffn_forward(h: SrnlFfn, x, params: Dict, y, res=None, gate=None, up=Non
     n, f = rows * h._dim, rows * h._hidden
     p = _ffn_weights(h, params, w)
     h._check(load_library().srnl_ffn_forward(
-        hd, _dense(x, w, "x", dt, n), ctypes.byref(p), _dense(res, w, "res", dt, n), _dense(y, w, "y", dt, n),
-        _dense(gate, w, "gate", dt, f), _dense(up, w, "up", dt, f), rows, _stream(stream)), w)
+        hd, _dense(h, x, w, "x", dt, n), ctypes.byref(p), _dense(h, res, w, "res", dt, n), _dense(h, y, w, "y", dt, n),
+        _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f), rows, _stream(stream)), w)
 
 
 def srnl_ffn_backward(h: SrnlFfn, x, gate, up, dy, params: Dict, dx, grads: Optional[Dict] = None, stream=None) -> None:
@@ -730,8 +733,8 @@ def srnl_ffn_backward(h: SrnlFfn, x, gate, up, dy, params: Dict, dx, grads: Opti
     n, f = rows * h._dim, rows * h._hidden
     p, g = _ffn_weights(h, params, w), _ffn_weights(h, grads, w)
     h._check(load_library().srnl_ffn_backward(
-        hd, _dense(x, w, "x", dt, n), _dense(gate, w, "gate", dt, f), _dense(up, w, "up", dt, f),
-        _dense(dy, w, "dy", dt, n), ctypes.byref(p), _dense(dx, w, "dx", dt, n), ctypes.byref(g), rows,
+        hd, _dense(h, x, w, "x", dt, n), _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f),
+        _dense(h, dy, w, "dy", dt, n), ctypes.byref(p), _dense(h, dx, w, "dx", dt, n), ctypes.byref(g), rows,
         _stream(stream)), w)
 
 
@@ -747,18 +750,15 @@ class SrnlLattn(_OpHandle):
 
     def _rows(self, t, where: str, name: str, tokens: int) -> int:
         """Address of bf16 token rows ([tokens..., heads * d], the handle's ld elements apart)."""
-        c = self._c
         if t is None:
             return 0
-        D = c.heads * c.d
-        shape = (c.B, c.T, D) if tokens else (c.B, D)
+        shape, want = self._layout[tokens]
         # dimensions of size one have no stride to speak of
-        st = [s for s, n in zip(t.stride(), t.shape) if n > 1] if tuple(t.shape) == shape else None
-        want = [s for s, n in zip(((c.T * self._ld,) if tokens else ()) + (self._ld, 1), shape) if n > 1]
-        if st != want or t.dtype is not self._dtype or not t.is_cuda:
+        ok = t.shape == shape and (t.stride() == want or all(a == b or n == 1 for a, b, n in zip(t.stride(), want, shape)))
+        if not ok or t.dtype is not self._dtype or t.get_device() != self._device:
             raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a CUDA tensor {shape} of {self._dtype} with rows "
-                                                 f"{self._ld} elements apart, got {tuple(t.shape)} {t.dtype} "
-                                                 f"{t.stride()} on {t.device}")
+                                                 f"{self._ld} elements apart on device {self._device}, got "
+                                                 f"{tuple(t.shape)} {t.dtype} {t.stride()} on {t.device}")
         return t.data_ptr()
 
 
@@ -776,42 +776,42 @@ def srnl_lattn_create(cfg: Dict, decay: np.ndarray) -> SrnlLattn:
     if st != SRNL_OK:
         raise SrnlError(st, "srnl_lattn_create", lib.srnl_lattn_last_error(None).decode())
     out = SrnlLattn(h.value, cfg)
-    out._c, out._ld, out._dtype = c, c.ld or c.heads * c.d, _torch_dtype(c.act_dtype)
+    D = c.heads * c.d
+    ld = c.ld or D
+    out._c, out._ld, out._dtype = c, ld, _torch_dtype(c.act_dtype)
+    out._layout = ((c.B, D), (ld, 1)), ((c.B, c.T, D), (c.T * ld, ld, 1))   # shape and strides: a step's rows, a prompt's
     return out
 
 
 def srnl_lattn_forward(h: SrnlLattn, q, k, v, o, lengths=None, state_in=None, state_out=None, stream=None) -> None:
     """o <- linear attention of q, k, v (bf16 [B, T, heads * d], tokens ld elements apart).
     lengths: int32 [B]; state_in, state_out: float32 [B, heads, d, d]."""
-    import torch
     w, hd, c = "srnl_lattn_forward", h.handle, h._c
-    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, torch.float32
+    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, h._f32
     h._check(load_library().srnl_lattn_forward(
-        hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(o, w, "o", h._dtype, n),
-        _dense(lengths, w, "lengths", torch.int32, c.B), _dense(state_in, w, "state_in", f32, s),
-        _dense(state_out, w, "state_out", f32, s), _stream(stream)), w)
+        hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(h, o, w, "o", h._dtype, n),
+        _dense(h, lengths, w, "lengths", h._i32, c.B), _dense(h, state_in, w, "state_in", f32, s),
+        _dense(h, state_out, w, "state_out", f32, s), _stream(stream)), w)
 
 
 def srnl_lattn_backward(h: SrnlLattn, q, k, v, do, dq, dk, dv, lengths=None, state_in=None, dstate_out=None,
                         dstate_in=None, stream=None) -> None:
     """dq, dk, dv <- the gradients for upstream do (dense) and dstate_out; dstate_in receives the
     gradient of state_in when given."""
-    import torch
     w, hd, c = "srnl_lattn_backward", h.handle, h._c
-    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, torch.float32
+    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, h._f32
     h._check(load_library().srnl_lattn_backward(
-        hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(do, w, "do", h._dtype, n),
+        hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(h, do, w, "do", h._dtype, n),
         h._rows(dq, w, "dq", 1), h._rows(dk, w, "dk", 1), h._rows(dv, w, "dv", 1),
-        _dense(lengths, w, "lengths", torch.int32, c.B), _dense(state_in, w, "state_in", f32, s),
-        _dense(dstate_out, w, "dstate_out", f32, s), _dense(dstate_in, w, "dstate_in", f32, s), _stream(stream)), w)
+        _dense(h, lengths, w, "lengths", h._i32, c.B), _dense(h, state_in, w, "state_in", f32, s),
+        _dense(h, dstate_out, w, "dstate_out", f32, s), _dense(h, dstate_in, w, "dstate_in", f32, s), _stream(stream)), w)
 
 
 def srnl_lattn_step(h: SrnlLattn, q, k, v, o, state, stream=None) -> None:
     """One token of each sequence: q, k, v, o bf16 [B, heads * d]; state float32
     [B, heads, d, d], updated in place."""
-    import torch
     w, hd, c = "srnl_lattn_step", h.handle, h._c
     h._check(load_library().srnl_lattn_step(
         hd, h._rows(q, w, "q", 0), h._rows(k, w, "k", 0), h._rows(v, w, "v", 0),
-        _dense(o, w, "o", h._dtype, c.B * c.heads * c.d),
-        _dense(state, w, "state", torch.float32, c.B * c.heads * c.d * c.d), _stream(stream)), w)
+        _dense(h, o, w, "o", h._dtype, c.B * c.heads * c.d),
+        _dense(h, state, w, "state", h._f32, c.B * c.heads * c.d * c.d), _stream(stream)), w)
