@@ -459,8 +459,8 @@ typedef struct {
  * message is srnl_ln_last_error(NULL). */
 SRNL_API srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg);
 
-/* y = layer norm of x.  DEVICE pointers: x, y [rows][dim], 16-byte aligned; gamma, beta fp32
- * [dim]; mean, rstd fp32 [rows], the statistics the backward pass reads, each may be NULL.
+/* y = layer norm of x.  DEVICE pointers: x, y [rows][dim] and gamma, beta fp32 [dim], 16-byte
+ * aligned; mean, rstd fp32 [rows], the statistics the backward pass reads, each may be NULL.
  * Outputs overlap neither inputs nor one another.  rows may be any number; 0 does nothing.
  * Asynchronous on `stream`; one kernel. */
 SRNL_API srnl_status srnl_ln_forward(srnl_ln* h, const void* x, const float* gamma, const float* beta, void* y,

@@ -7,15 +7,20 @@
 //             dx = rstd (w - sum(w) / D - xhat sum(w xhat) / D) [+ dres],
 //             dgamma = sum_rows dy xhat, dbeta = sum_rows dy
 //
-// Both passes are bound by memory: each input row is read once into registers and each output
-// row written once.  All statistics, sums and gradients of gamma and beta are fp32; only y and
-// dx are rounded, once, to the activations' type.
+// Both passes are bound by memory: each input is read once and each output written once.  All
+// statistics, sums and gradients of gamma and beta are fp32; only y and dx are rounded, once,
+// to the activations' type.
 //
-// Layout of the work: a row belongs to a group of lanes.  Rows of up to 128 16-byte vectors
-// take 8, 16 or 32 lanes of a warp (a 64-channel bf16 row is 8 vectors: a whole warp on it
-// would leave 24 lanes idle), longer rows a block.  Groups walk the rows with the stride of
-// the grid and load their next row before they reduce the present one, so gamma and beta stay
-// in registers and a load is always in flight.
+// Layout of the work: a row belongs to a group of lanes that hold it in registers between the
+// sums and the output: 8 to 32 lanes of a warp for rows of up to 128 16-byte vectors, a block for
+// longer ones.  A lane owns the same columns in every row it meets, so the weights' gradients
+// stay in its registers until the end.  Several rows are taken at once where they are short, so
+// that enough loads are in flight.  The arithmetic goes in pairs (two fp32 operations an
+// instruction): at full bandwidth the issue slots, not the loads, come next.
+//
+// Rows that are not whole 16-byte vectors: a group strides over the rows by a multiple of the
+// vector's length, so all its rows start at the same offset within a vector.  Its lanes stay on
+// aligned vectors; only the two at a row's ends, shared with its neighbours, go value by value.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,62 +37,103 @@ namespace srnl {
 namespace {
 
 constexpr int kNormMaxDim = 8192;
-constexpr int kNormWaves = 4;      // partial sums of the weights' gradients: at most this many blocks per SM
+constexpr int kNormBlocks = 8;     // most blocks per SM, and partial sums of the weights' gradients
 
-// V consecutive values of a row, as fp32.
-template <typename T, int V>
-__device__ __forceinline__ void load_vec(const T* p, float* v) {
-  if constexpr (V == 1) {
-    if constexpr (sizeof(T) == 2) v[0] = __bfloat162float(*p);
-    else v[0] = *p;
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// 16 bytes of a row as fp32 pairs, and back.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& raw, float2* v) {
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
+    for (int i = 0; i < 4; ++i) v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   } else {
-    const float4 a = *reinterpret_cast<const float4*>(p);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    v[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
   }
 }
-
-template <typename T, int V>
-__device__ __forceinline__ void store_vec(T* p, const float* v) {
-  if constexpr (V == 1) {
-    if constexpr (sizeof(T) == 2) *p = __float2bfloat16_rn(v[0]);
-    else *p = v[0];
-  } else if constexpr (sizeof(T) == 2) {
+template <typename T>
+__device__ __forceinline__ uint4 repack(const float2* v) {
+  if constexpr (sizeof(T) == 2) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[i].x, v[i].y);
       w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   } else {
-    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    return make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
   }
 }
 
-// Sums over a row's group: LPR lanes of a warp, or (LPR == 0) the whole block.
-template <int LPR, int N>
-__device__ __forceinline__ void group_sum(float (&s)[N], float* red) {
-  constexpr int W = LPR == 0 ? 32 : LPR;
+// The V values at column c of a row (c < 0 or c + V > dim only for odd rows: the rest is zero).
+template <typename T, bool ODD>
+__device__ __forceinline__ uint4 load_cols(const T* row, int c, int dim) {
+  constexpr int V = 16 / sizeof(T);
+  if (!ODD || (c >= 0 && c + V <= dim)) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int o = W / 2; o > 0; o >>= 1)
+  for (int e = 0; e < V; ++e)
+    if (c + e >= 0 && c + e < dim) {
+      if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)__bfloat16_as_ushort(row[c + e]) << (16 * (e & 1));
+      else w[e] = __float_as_uint(row[c + e]);
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T, bool ODD>
+__device__ __forceinline__ void store_cols(T* row, int c, int dim, const float2* v) {
+  constexpr int V = 16 / sizeof(T);
+  const uint4 raw = repack<T>(v);
+  if (!ODD || (c >= 0 && c + V <= dim)) {
+    *reinterpret_cast<uint4*>(row + c) = raw;
+    return;
+  }
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (c + e >= 0 && c + e < dim) {
+      if constexpr (sizeof(T) == 2) row[c + e] = __ushort_as_bfloat16((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+      else row[c + e] = __uint_as_float(w[e]);
+    }
+}
+// V weights at column c, as pairs.
+template <int V, bool ODD>
+__device__ __forceinline__ void load_weights(const float* p, int c, int dim, float2* v) {
+  if (!ODD) {
+#pragma unroll
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 f = *reinterpret_cast<const float4*>(p + c + 4 * i);
+      v[2 * i] = make_float2(f.x, f.y);
+      v[2 * i + 1] = make_float2(f.z, f.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      const int k = c + 2 * i;
+      v[i].x = k >= 0 && k < dim ? p[k] : 0.f;
+      v[i].y = k + 1 >= 0 && k + 1 < dim ? p[k + 1] : 0.f;
+    }
+  }
+}
+
+// Sums of N values over a row's lanes: LPR of a warp, or (LPR == 0) the block, by way of red
+// ([16 warps][N]; calls alternate between two of them, so that one barrier a call is enough).
+template <int LPR, int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
+#pragma unroll
+  for (int o = (LPR == 0 ? 32 : LPR) / 2; o > 0; o >>= 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-  if constexpr (LPR == 0) {   // red: two alternating halves of [warps][N], so one barrier per sum is enough
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  if constexpr (LPR == 0) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     if (lane == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) red[warp * N + i] = s[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = lane < nw ? red[lane * N + i] : 0.f;
+    for (int i = 0; i < N; ++i) s[i] = lane < warps ? red[lane * N + i] : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -95,183 +141,287 @@ __device__ __forceinline__ void group_sum(float (&s)[N], float* red) {
   }
 }
 
-// T: activations' type; V: values per load; LPR: lanes per row (0: a block per row); PER:
-// loads per lane and row.
-template <typename T, int V, int LPR, int PER>
-__global__ void __launch_bounds__(LPR == 0 ? 512 : 256)
+constexpr int kLongThreads = 544;   // 8192 columns and an odd start: 1025 bf16 vectors by two, 2049 fp32 ones by four
+// Most threads of a block, and the blocks whose registers an SM has to hold.
+__host__ __device__ constexpr int norm_threads(int lpr, int per, bool bwd) {
+  return lpr == 0 ? (per == 1 ? 256 : kLongThreads) : bwd ? 128 : 256;
+}
+__host__ __device__ constexpr int norm_resident(int lpr, int per, bool bwd) {
+  return lpr == 0 ? (per == 1 ? (bwd ? 2 : 4) : (bwd ? 1 : 2)) : bwd ? 4 : 3;
+}
+
+// LPR: lanes per row (0: a block); PER: vectors per lane; R: rows at once.
+template <typename T, int LPR, int PER, int R, bool ODD>
+__global__ void __launch_bounds__(norm_threads(LPR, PER, false), norm_resident(LPR, PER, false))
     norm_forward_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
                         T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t rows,
                         int dim, float eps) {
-  constexpr int N = PER * V;
-  __shared__ float red[LPR == 0 ? 32 : 1];
-  const int lanes = LPR == 0 ? blockDim.x : LPR;
-  const int lane = LPR == 0 ? threadIdx.x : threadIdx.x % LPR;
-  const int64_t first = LPR == 0 ? blockIdx.x : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
-  const int64_t step = LPR == 0 ? gridDim.x : (int64_t)gridDim.x * blockDim.x / LPR;
+  constexpr int V = 16 / sizeof(T), H = V / 2;
+  // gamma and beta in registers, else from L1 for each R rows (an odd row's value by value)
+  constexpr bool kKeep = LPR != 0 && PER * V <= (ODD ? 24 : 16);
+  __shared__ float red[LPR == 0 ? 2 * 18 * R : 1];
+  const int lanes = LPR == 0 ? blockDim.x : LPR, lane = LPR == 0 ? threadIdx.x : threadIdx.x % LPR;
+  const int64_t group = LPR == 0 ? blockIdx.x : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
+  const int64_t groups = LPR == 0 ? gridDim.x : (int64_t)gridDim.x * blockDim.x / LPR;
+  // of the warp's first group: all lanes of a warp make the same passes
+  const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (threadIdx.x % 32) / LPR;
+  const int c0 = lane * V - (ODD ? (int)(group * dim % V) : 0), cs = lanes * V;
   const float inv_d = 1.f / (float)dim;
-  float g[N], b[N], v[N];
   bool on[PER];
+  float2 g[kKeep ? PER * H : 1], b[kKeep ? PER * H : 1];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int c = (i * lanes + lane) * V;
-    on[i] = c < dim;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      g[i * V + e] = on[i] ? gamma[c + e] : 0.f;
-      b[i * V + e] = on[i] ? beta[c + e] : 0.f;
-      v[i * V + e] = 0.f;
-    }
-    if (on[i] && first < rows) load_vec<T, V>(x + first * dim + c, v + i * V);
-  }
-  // Every lane of a warp makes the same number of passes, so the warp's shuffles stay whole:
-  // the bound is that of the warp's first row.
-  const int64_t lead = LPR == 0 || LPR == 32 ? first : first - (threadIdx.x % 32) / LPR;
-  int64_t r = first;
-  for (int64_t base = lead; base < rows; base += step, r += step) {
-    float nx[N];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) nx[i * V + e] = 0.f;
-      if (on[i] && r + step < rows) load_vec<T, V>(x + (r + step) * dim + (i * lanes + lane) * V, nx + i * V);
-    }
-    float s[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[0] += v[i];
-    group_sum<LPR, 1>(s, red);
-    const float mean = s[0] * inv_d;
-    float q[1] = {0.f};
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float c = on[i] ? v[i * V + e] - mean : 0.f;
-        q[0] = fmaf(c, c, q[0]);
+    on[i] = c0 + i * cs < dim && (!ODD || c0 + i * cs + V > 0);
+    if constexpr (kKeep)
+      if (on[i]) {
+        load_weights<V, ODD>(gamma, c0 + i * cs, dim, g + i * H);
+        load_weights<V, ODD>(beta, c0 + i * cs, dim, b + i * H);
       }
-    group_sum<LPR, 1>(q, red + (LPR == 0 ? 16 : 0));
-    const float rstd = rsqrtf(q[0] * inv_d + eps);
-    if (r < rows) {
+  }
+  uint4 raw[R][PER];
+  auto load = [&](int64_t from) {
+#pragma unroll
+    for (int q = 0; q < R; ++q)
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        if (!on[i]) continue;
-        float o[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) o[e] = fmaf((v[i * V + e] - mean) * rstd, g[i * V + e], b[i * V + e]);
-        store_vec<T, V>(y + r * dim + (i * lanes + lane) * V, o);
+        raw[q][i] = make_uint4(0u, 0u, 0u, 0u);
+        const int64_t r = from + q * groups;
+        if (on[i] && r < rows) raw[q][i] = load_cols<T, ODD>(x + r * dim, c0 + i * cs, dim);
       }
-      if (lane == 0) {
-        if (mean_out != nullptr) mean_out[r] = mean;
-        if (rstd_out != nullptr) rstd_out[r] = rstd;
+  };
+  if (LPR == 0) load(group);
+  for (int64_t r0 = group, base = lead; base < rows; r0 += groups * R, base += groups * R) {
+    float2 v[R][PER * H];
+    float s[R];
+    if (LPR != 0) load(r0);
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        unpack<T>(raw[q][i], v[q] + i * H);
+#pragma unroll
+        for (int e = 0; e < H; ++e) t = __fadd2_rn(t, v[q][i * H + e]);
+      }
+      s[q] = t.x + t.y;
+    }
+    if (LPR == 0) load(r0 + groups * R);   // a block waits on its barriers: the next rows are on their way meanwhile
+    row_sum<LPR, R>(s, red);
+    float mean[R];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      mean[q] = s[q] * inv_d;
+      float2 t = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int c = c0 + i * cs;
+        if (!on[i]) continue;
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          float2 d = __fadd2_rn(v[q][i * H + e], both(-mean[q]));
+          if (ODD && (c < 0 || c + V > dim)) {
+            if (c + 2 * e < 0 || c + 2 * e >= dim) d.x = 0.f;
+            if (c + 2 * e + 1 < 0 || c + 2 * e + 1 >= dim) d.y = 0.f;
+          }
+          v[q][i * H + e] = d;
+          t = __ffma2_rn(d, d, t);
+        }
+      }
+      s[q] = t.x + t.y;
+    }
+    row_sum<LPR, R>(s, red + (LPR == 0 ? 18 * R : 0));
+#pragma unroll
+    for (int q = 0; q < R; ++q) s[q] = rsqrtf(s[q] * inv_d + eps);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (!on[i]) continue;
+      const int c = c0 + i * cs;
+      float2 gw[H], bw[H];
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int e = 0; e < H; ++e) { gw[e] = g[i * H + e]; bw[e] = b[i * H + e]; }
+      } else {
+        load_weights<V, ODD>(gamma, c, dim, gw);
+        load_weights<V, ODD>(beta, c, dim, bw);
+      }
+#pragma unroll
+      for (int q = 0; q < R; ++q) {
+        const int64_t r = r0 + q * groups;
+        if (r >= rows) continue;
+        float2 o[H];
+#pragma unroll
+        for (int e = 0; e < H; ++e) o[e] = __ffma2_rn(__fmul2_rn(v[q][i * H + e], both(s[q])), gw[e], bw[e]);
+        store_cols<T, ODD>(y + r * dim, c, dim, o);
       }
     }
+    if (lane == 0) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = nx[i];
+      for (int q = 0; q < R; ++q) {
+        const int64_t r = r0 + q * groups;
+        if (r < rows && mean_out != nullptr) mean_out[r] = mean[q];
+        if (r < rows && rstd_out != nullptr) rstd_out[r] = s[q];
+      }
+    }
   }
 }
 
-// dx per row, and per block the partial sums of dgamma and dbeta: part[block][2][dim].  A lane
-// owns the same columns in every row it meets, so its sums stay in registers until the end.
-template <typename T, int V, int LPR, int PER>
-__global__ void __launch_bounds__(LPR == 0 ? 512 : 256)
+// dx per row, and per block the partial sums of dgamma and dbeta: part[block][2][dim].
+template <typename T, int LPR, int PER, int R, bool ODD>
+__global__ void __launch_bounds__(norm_threads(LPR, PER, true), norm_resident(LPR, PER, true))
     norm_backward_kernel(const T* __restrict__ x, const T* __restrict__ dy, const T* __restrict__ dres,
                          const float* __restrict__ gamma, const float* __restrict__ mean_in,
                          const float* __restrict__ rstd_in, T* __restrict__ dx, float* __restrict__ part,
                          int64_t rows, int dim) {
-  constexpr int N = PER * V;
-  extern __shared__ float fold[];   // warps sharing columns: [2][dim]
-  __shared__ float red[LPR == 0 ? 64 : 1];
-  const int lanes = LPR == 0 ? blockDim.x : LPR;
-  const int lane = LPR == 0 ? threadIdx.x : threadIdx.x % LPR;
-  const int64_t first = LPR == 0 ? blockIdx.x : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
-  const int64_t step = LPR == 0 ? gridDim.x : (int64_t)gridDim.x * blockDim.x / LPR;
+  constexpr int V = 16 / sizeof(T), H = V / 2;
+  extern __shared__ float fold[];   // [warps][2][dim]: groups of different warps share columns
+  __shared__ float red[LPR == 0 ? 2 * 18 * 2 * R : 1];
+  const int lanes = LPR == 0 ? blockDim.x : LPR, lane = LPR == 0 ? threadIdx.x : threadIdx.x % LPR;
+  const int64_t group = LPR == 0 ? blockIdx.x : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
+  const int64_t groups = LPR == 0 ? gridDim.x : (int64_t)gridDim.x * blockDim.x / LPR;
+  const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (threadIdx.x % 32) / LPR;
+  const int sh = ODD ? (int)(group * dim % V) : 0, c0 = lane * V - sh, cs = lanes * V;
   const float inv_d = 1.f / (float)dim;
-  float dg[N], db[N];
+  bool on[PER];
+  constexpr bool kKeep = LPR != 0 && PER * V <= 16;
+  float2 dg[PER * H], db[PER * H], g[kKeep ? PER * H : 1];
 #pragma unroll
-  for (int i = 0; i < N; ++i) dg[i] = db[i] = 0.f;
-  const int64_t lead = LPR == 0 || LPR == 32 ? first : first - (threadIdx.x % 32) / LPR;
-  int64_t r = first;
+  for (int i = 0; i < PER; ++i) {
+    on[i] = c0 + i * cs < dim && (!ODD || c0 + i * cs + V > 0);
+    if constexpr (kKeep)
+      if (on[i]) load_weights<V, ODD>(gamma, c0 + i * cs, dim, g + i * H);
+#pragma unroll
+    for (int e = 0; e < H; ++e) dg[i * H + e] = db[i * H + e] = make_float2(0.f, 0.f);
+  }
   int flip = 0;
-  for (int64_t base = lead; base < rows; base += step, r += step) {
-    float xh[N], w[N];
-    const bool live = r < rows;
-    const float mean = live ? mean_in[r] : 0.f, rstd = live ? rstd_in[r] : 0.f;
-    float s[2] = {0.f, 0.f};
+  uint4 xr[R][PER], yr[R][PER], er[R][PER];
+  float mean[R], rstd[R];
+  auto load = [&](int64_t from) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = (i * lanes + lane) * V;
+    for (int q = 0; q < R; ++q) {
+      const int64_t r = from + q * groups;
+      mean[q] = r < rows ? mean_in[r] : 0.f;
+      rstd[q] = r < rows ? rstd_in[r] : 0.f;
 #pragma unroll
-      for (int e = 0; e < V; ++e) xh[i * V + e] = w[i * V + e] = 0.f;
-      if (live && c < dim) {
-        load_vec<T, V>(x + r * dim + c, xh + i * V);
-        load_vec<T, V>(dy + r * dim + c, w + i * V);
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const int k = i * V + e;
-          xh[k] = (xh[k] - mean) * rstd;
-          dg[k] = fmaf(w[k], xh[k], dg[k]);
-          db[k] += w[k];
-          w[k] *= gamma[c + e];
-          s[0] += w[k];
-          s[1] = fmaf(w[k], xh[k], s[1]);
+      for (int i = 0; i < PER; ++i) {
+        xr[q][i] = yr[q][i] = er[q][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (on[i] && r < rows) {
+          xr[q][i] = load_cols<T, ODD>(x + r * dim, c0 + i * cs, dim);
+          yr[q][i] = load_cols<T, ODD>(dy + r * dim, c0 + i * cs, dim);
+          if (dres != nullptr) er[q][i] = load_cols<T, ODD>(dres + r * dim, c0 + i * cs, dim);
         }
       }
     }
-    group_sum<LPR, 2>(s, red + (LPR == 0 ? 32 * flip : 0));
-    flip ^= 1;
-    if (live) {
-      const float a = s[0] * inv_d, bq = s[1] * inv_d;
+  };
+  // Between a block's barriers its next rows are on their way; not with two bf16 vectors a lane,
+  // whose sums leave no registers for it (8192 columns: 139 us without, 175 us with).
+  constexpr bool kAhead = LPR == 0 && PER * V < (sizeof(T) == 2 ? 16 : 32);
+  if (kAhead) load(group);
+  for (int64_t r0 = group, base = lead; base < rows; r0 += groups * R, base += groups * R, flip ^= 1) {
+    float s[2 * R], f[R];
+    uint4 res[R][PER];
+    if (!kAhead) load(r0);
+    // values past a row's ends have dy = 0 and add nothing to any sum
+    float2 xh[R][PER * H], w[R][PER * H];
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      float2 t = make_float2(0.f, 0.f), u = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int c = (i * lanes + lane) * V;
-        if (c >= dim) continue;
-        float o[V];
-        if (dres != nullptr) load_vec<T, V>(dres + r * dim + c, o);
+        float2 xv[H], yv[H], gw[H];
+        unpack<T>(xr[q][i], xv);
+        unpack<T>(yr[q][i], yv);
+        if (!on[i]) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float d = rstd * (w[i * V + e] - a - xh[i * V + e] * bq);
-          o[e] = dres != nullptr ? d + o[e] : d;
+          for (int e = 0; e < H; ++e) gw[e] = make_float2(0.f, 0.f);
+        } else if constexpr (kKeep) {
+#pragma unroll
+          for (int e = 0; e < H; ++e) gw[e] = g[i * H + e];
+        } else {
+          load_weights<V, ODD>(gamma, c0 + i * cs, dim, gw);
         }
-        store_vec<T, V>(dx + r * dim + c, o);
+#pragma unroll
+        for (int e = 0; e < H; ++e) {
+          const int k = i * H + e;
+          xh[q][k] = __fmul2_rn(__fadd2_rn(xv[e], both(-mean[q])), both(rstd[q]));
+          dg[k] = __ffma2_rn(yv[e], xh[q][k], dg[k]);
+          db[k] = __fadd2_rn(db[k], yv[e]);
+          w[q][k] = __fmul2_rn(yv[e], gw[e]);
+          t = __fadd2_rn(t, w[q][k]);
+          u = __ffma2_rn(w[q][k], xh[q][k], u);
+        }
+      }
+      s[2 * q] = t.x + t.y;
+      s[2 * q + 1] = u.x + u.y;
+    }
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      f[q] = rstd[q];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) res[q][i] = er[q][i];
+    }
+    if (kAhead) load(r0 + groups * R);
+    row_sum<LPR, 2 * R>(s, red + (LPR == 0 ? 18 * 2 * R * flip : 0));
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const int64_t r = r0 + q * groups;
+      if (r >= rows) continue;
+      const float2 a = both(-s[2 * q] * inv_d), m = both(-s[2 * q + 1] * inv_d);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (!on[i]) continue;
+        float2 o[H];
+        unpack<T>(res[q][i], o);
+#pragma unroll
+        for (int e = 0; e < H; ++e)
+          o[e] = __ffma2_rn(__ffma2_rn(xh[q][i * H + e], m, __fadd2_rn(w[q][i * H + e], a)), both(f[q]), o[e]);
+        store_cols<T, ODD>(dx + r * dim, c0 + i * cs, dim, o);
       }
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;");
+  // groups in one order: those of a warp with equal columns, then the warps; an odd row's groups
+  // start at different columns, so each adds its own in turn
   float* mine = part + (int64_t)blockIdx.x * 2 * dim;
+  auto put = [&](float* to, bool add) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const int c = c0 + i * cs + e, k = i * H + e / 2;
+        if (!on[i] || c >= dim || (ODD && c < 0)) continue;
+        const float p = e & 1 ? dg[k].y : dg[k].x, q = e & 1 ? db[k].y : db[k].x;
+        to[c] = add ? to[c] + p : p;
+        to[dim + c] = add ? to[dim + c] + q : q;
+      }
+  };
   if constexpr (LPR == 0) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int c = (i * lanes + lane) * V;
-      if (c < dim)
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-          mine[c + e] = dg[i * V + e];
-          mine[dim + c + e] = db[i * V + e];
-        }
-    }
+    put(mine, false);
   } else {
-    // groups of one warp first, then the warps one after the other: a fixed order
+    const int warp = threadIdx.x >> 5;
+    float* to = fold + warp * 2 * dim;
+    if constexpr (!ODD) {
 #pragma unroll
-    for (int o = LPR; o < 32; o <<= 1)
+      for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        dg[i] += __shfl_xor_sync(0xffffffffu, dg[i], o);
-        db[i] += __shfl_xor_sync(0xffffffffu, db[i], o);
-      }
-    for (int k = 0; k < (int)(blockDim.x >> 5); ++k) {
-      if ((int)(threadIdx.x >> 5) == k && (threadIdx.x & 31) < LPR) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int c = (i * lanes + lane) * V;
-          if (c < dim)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-              fold[c + e] = (k == 0 ? 0.f : fold[c + e]) + dg[i * V + e];
-              fold[dim + c + e] = (k == 0 ? 0.f : fold[dim + c + e]) + db[i * V + e];
-            }
+        for (int k = 0; k < PER * H; ++k) {
+          dg[k].x += __shfl_xor_sync(0xffffffffu, dg[k].x, o);
+          dg[k].y += __shfl_xor_sync(0xffffffffu, dg[k].y, o);
+          db[k].x += __shfl_xor_sync(0xffffffffu, db[k].x, o);
+          db[k].y += __shfl_xor_sync(0xffffffffu, db[k].y, o);
         }
+      if ((threadIdx.x & 31) < LPR) put(to, false);
+    } else {
+      for (int k = 0; k < 32 / LPR; ++k) {
+        if ((int)(threadIdx.x & 31) / LPR == k) put(to, k > 0);
+        __syncwarp();
       }
-      __syncthreads();
     }
-    for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) mine[c] = fold[c];
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) {
+      float t = 0.f;
+      for (int k = 0; k < (int)(blockDim.x >> 5); ++k) t += fold[k * 2 * dim + c];
+      mine[c] = t;
+    }
   }
 }
 
@@ -283,8 +433,9 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* __r
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;   // column of [2][dim]
   float s = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // launched while the rows' kernel still runs
   if (c < 2 * dim) {
-#pragma unroll 4
+#pragma unroll 8
     for (int b = warp; b < blocks; b += 32) s += part[(int64_t)b * 2 * dim + c];
   }
   sm[warp][lane] = s;
@@ -301,61 +452,61 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* __r
   }
 }
 
+// The lanes a row length takes.
 struct NormPlan {
-  int V, lpr, per, threads;
+  int lpr, per, threads;   // threads of a block per row (lpr == 0)
+  bool odd;                // rows that are not whole 16-byte vectors
 };
 
-// The lanes a row takes.  16-byte loads need rows that are whole vectors (dim a multiple of 8
-// in bf16, 4 in fp32); other widths go value by value.
 NormPlan norm_plan(int dim, int esize) {
   NormPlan p{};
-  p.V = (dim * esize) % 16 == 0 ? 16 / esize : 1;
-  const int n = dim / p.V;
-  p.threads = 256;
-  if (p.V > 1) {
-    if (n <= 8) { p.lpr = 8; p.per = 1; }
-    else if (n <= 16) { p.lpr = 16; p.per = 1; }
-    else if (n <= 32) { p.lpr = 32; p.per = 1; }
-    else if (n <= 64) { p.lpr = 32; p.per = 2; }
-    else if (n <= 128) { p.lpr = 32; p.per = 4; }
-    else {
-      p.lpr = 0;
-      p.per = n <= 256 ? 1 : n <= 512 ? 2 : 4;
-      p.threads = ((n + p.per - 1) / p.per + 31) / 32 * 32;
-    }
-  } else {
-    if (n <= 32) { p.lpr = 32; p.per = 1; }
-    else if (n <= 128) { p.lpr = 32; p.per = 4; }
-    else if (n <= 512) { p.lpr = 32; p.per = 16; }
-    else { p.lpr = 0; p.per = 16; p.threads = ((n + 15) / 16 + 31) / 32 * 32; }
+  const int V = 16 / esize;
+  p.odd = dim % V != 0;
+  const int n = (dim + (p.odd ? V - 1 : 0) + V - 1) / V;   // vectors a row may touch
+  if (n <= 8) { p.lpr = 8; p.per = 1; }
+  else if (n <= 16) { p.lpr = 16; p.per = 1; }
+  else if (n <= 32) { p.lpr = 16; p.per = 2; }
+  else if (n <= 48) { p.lpr = 16; p.per = 3; }
+  else if (n <= 64) { p.lpr = 32; p.per = 2; }
+  else if (n <= 96) { p.lpr = 32; p.per = 3; }
+  else if (n <= 128) { p.lpr = 32; p.per = 4; }
+  else {
+    p.lpr = 0;
+    p.per = n <= 256 ? 1 : n <= 2 * kLongThreads ? 2 : 4;
+    p.threads = ((n + p.per - 1) / p.per + 31) / 32 * 32;
   }
   return p;
 }
 
-int norm_blocks(const NormPlan& p, int64_t rows, int sms, int per_sm) {
-  const int64_t per_block = p.lpr == 0 ? 1 : p.threads / p.lpr;
-  const int64_t need = (rows + per_block - 1) / per_block;
-  const int64_t most = (int64_t)sms * per_sm;
-  return (int)(need < most ? need : most);
+// Blocks of a call: what the SMs hold at once, or fewer for few rows; groups a multiple of 8 (a
+// vector's values), which an odd row's groups rely on.
+int norm_blocks(const NormPlan& p, int threads, int64_t rows, int sms, int per_sm) {
+  const int per_block = p.lpr == 0 ? 1 : threads / p.lpr;
+  const int64_t need = (rows + per_block - 1) / per_block, most = (int64_t)sms * per_sm;
+  const int blocks = (int)(need < most ? need : most);
+  return p.odd && per_block % 8 != 0 ? (blocks + 7) / 8 * 8 : blocks;
 }
 
-// Calls F with the template parameters of a plan; false for a plan that does not exist.
-#define SRNL_NORM_DISPATCH(T, CALL)                                                                       \
-  do {                                                                                                    \
-    constexpr int W = 16 / sizeof(T);                                                                     \
-    if (p.V == 1) {                                                                                       \
-      if (p.lpr == 32 && p.per == 1) { CALL(T, 1, 32, 1); }                                               \
-      else if (p.lpr == 32 && p.per == 4) { CALL(T, 1, 32, 4); }                                          \
-      else if (p.lpr == 32) { CALL(T, 1, 32, 16); }                                                       \
-      else { CALL(T, 1, 0, 16); }                                                                         \
-    } else if (p.lpr == 8) { CALL(T, W, 8, 1); }                                                          \
-    else if (p.lpr == 16) { CALL(T, W, 16, 1); }                                                          \
-    else if (p.lpr == 32 && p.per == 1) { CALL(T, W, 32, 1); }                                            \
-    else if (p.lpr == 32 && p.per == 2) { CALL(T, W, 32, 2); }                                            \
-    else if (p.lpr == 32) { CALL(T, W, 32, 4); }                                                          \
-    else if (p.per == 1) { CALL(T, W, 0, 1); }                                                            \
-    else if (p.per == 2) { CALL(T, W, 0, 2); }                                                            \
-    else { CALL(T, W, 0, 4); }                                                                            \
+// Short rows go several at a time, so that a lane has two to four vectors in flight.
+#define SRNL_NORM_PLAN(T, ODD, FWD, CALL)                                  \
+  do {                                                                     \
+    if (p.lpr == 8) { CALL(T, 8, 1, (FWD ? 4 : 2), ODD); }                 \
+    else if (p.lpr == 16 && p.per == 1) { CALL(T, 16, 1, (FWD ? 4 : 2), ODD); } \
+    else if (p.lpr == 16 && p.per == 2) { CALL(T, 16, 2, (FWD ? 2 : 1), ODD); } \
+    else if (p.lpr == 16) { CALL(T, 16, 3, 1, ODD); }                      \
+    else if (p.lpr == 32 && p.per == 2) { CALL(T, 32, 2, (FWD ? 2 : 1), ODD); } \
+    else if (p.lpr == 32 && p.per == 3) { CALL(T, 32, 3, 1, ODD); }        \
+    else if (p.lpr == 32) { CALL(T, 32, 4, 1, ODD); }                      \
+    else if (p.per == 1) { CALL(T, 0, 1, 2, ODD); }                        \
+    else if (p.per == 2) { CALL(T, 0, 2, 1, ODD); }                        \
+    else if (sizeof(T) == 4) { CALL(T, 0, (sizeof(T) == 4 ? 4 : 2), 1, ODD); } \
+  } while (0)
+#define SRNL_NORM_DISPATCH(FWD, CALL)                                      \
+  do {                                                                     \
+    if (bf16 && p.odd) SRNL_NORM_PLAN(__nv_bfloat16, true, FWD, CALL);     \
+    else if (bf16) SRNL_NORM_PLAN(__nv_bfloat16, false, FWD, CALL);        \
+    else if (p.odd) SRNL_NORM_PLAN(float, true, FWD, CALL);                \
+    else SRNL_NORM_PLAN(float, false, FWD, CALL);                          \
   } while (0)
 
 }  // namespace
@@ -366,7 +517,8 @@ struct srnl_ln {
   srnl_ln_config cfg{};
   int device = 0, sms = 0;
   srnl::NormPlan plan{};
-  float* part = nullptr;   // [kNormWaves * sms][2][dim]
+  int fwd_per_sm = 1, bwd_per_sm = 1;   // blocks an SM holds
+  float* part = nullptr;                // [bwd_per_sm * sms + 8][2][dim]
   char err[256] = "";
 };
 
@@ -419,8 +571,25 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
   h->plan = srnl::norm_plan(cfg->dim, cfg->act_dtype == SRNL_BF16 ? 2 : 4);
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
+  if (e == cudaSuccess) {
+    const srnl::NormPlan& p = h->plan;
+    const bool bf16 = cfg->act_dtype == SRNL_BF16;
+    const int ft = p.lpr == 0 ? p.threads : 256, bt = p.lpr == 0 ? p.threads : 128;
+    const size_t smem = p.lpr == 0 ? 0 : (size_t)(bt / 32) * 2 * cfg->dim * sizeof(float);
+#define SRNL_NORM_OCC(T, LPR, PER, R, ODD)                                                                             \
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD>, ft, 0)
+    SRNL_NORM_DISPATCH(true, SRNL_NORM_OCC);
+#undef SRNL_NORM_OCC
+#define SRNL_NORM_OCC(T, LPR, PER, R, ODD)                                                                             \
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD>, bt, smem)
+    if (e == cudaSuccess) SRNL_NORM_DISPATCH(false, SRNL_NORM_OCC);
+#undef SRNL_NORM_OCC
+    if (h->fwd_per_sm < 1) h->fwd_per_sm = 1;
+    if (h->bwd_per_sm < 1) h->bwd_per_sm = 1;
+    if (h->bwd_per_sm > srnl::kNormBlocks) h->bwd_per_sm = srnl::kNormBlocks;
+  }
   if (e == cudaSuccess)
-    e = cudaMalloc(&h->part, (size_t)h->sms * srnl::kNormWaves * 2 * cfg->dim * sizeof(float));
+    e = cudaMalloc(&h->part, ((size_t)h->sms * h->bwd_per_sm + 8) * 2 * cfg->dim * sizeof(float));
   if (e != cudaSuccess) {
     const srnl_status st = ln_cuda_fail(nullptr, e, "layer norm create");
     delete h;
@@ -438,9 +607,9 @@ srnl_status srnl_ln_forward(srnl_ln* h, const void* x, const float* gamma, const
   if (rows == 0) return SRNL_OK;
   if (x == nullptr || y == nullptr || gamma == nullptr || beta == nullptr)
     return ln_fail(h, SRNL_E_INVAL, "x, y, gamma or beta is NULL");
-  if (!ln_aligned(x, 16) || !ln_aligned(y, 16)) return ln_fail(h, SRNL_E_INVAL, "x and y must be 16-byte aligned");
-  if (!ln_aligned(gamma, 4) || !ln_aligned(beta, 4) || !ln_aligned(mean, 4) || !ln_aligned(rstd, 4))
-    return ln_fail(h, SRNL_E_INVAL, "gamma, beta, mean and rstd must be 4-byte aligned");
+  if (!ln_aligned(x, 16) || !ln_aligned(y, 16) || !ln_aligned(gamma, 16) || !ln_aligned(beta, 16))
+    return ln_fail(h, SRNL_E_INVAL, "x, y, gamma and beta must be 16-byte aligned");
+  if (!ln_aligned(mean, 4) || !ln_aligned(rstd, 4)) return ln_fail(h, SRNL_E_INVAL, "mean and rstd must be 4-byte aligned");
   const bool bf16 = h->cfg.act_dtype == SRNL_BF16;
   const int dim = h->cfg.dim;
   const size_t n = (size_t)rows * dim * (bf16 ? 2 : 4), nr = (size_t)rows * 4, nd = (size_t)dim * 4;
@@ -455,13 +624,12 @@ srnl_status srnl_ln_forward(srnl_ln* h, const void* x, const float* gamma, const
   if (st != SRNL_OK) return st;
   const srnl::NormPlan& p = h->plan;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int blocks = srnl::norm_blocks(p, rows, h->sms, 16);
-#define SRNL_NORM_FWD(T, V, LPR, PER)                                                                              \
-  srnl::norm_forward_kernel<T, V, LPR, PER><<<blocks, p.threads, 0, s>>>(                                          \
+  const int threads = p.lpr == 0 ? p.threads : 256, blocks = srnl::norm_blocks(p, threads, rows, h->sms, h->fwd_per_sm);
+#define SRNL_NORM_RUN(T, LPR, PER, R, ODD)                                                      \
+  srnl::norm_forward_kernel<T, LPR, PER, R, ODD><<<blocks, threads, 0, s>>>(                    \
       static_cast<const T*>(x), gamma, beta, static_cast<T*>(y), mean, rstd, rows, dim, h->cfg.eps)
-  if (bf16) SRNL_NORM_DISPATCH(__nv_bfloat16, SRNL_NORM_FWD);
-  else SRNL_NORM_DISPATCH(float, SRNL_NORM_FWD);
-#undef SRNL_NORM_FWD
+  SRNL_NORM_DISPATCH(true, SRNL_NORM_RUN);
+#undef SRNL_NORM_RUN
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SRNL_OK : ln_cuda_fail(h, e, "layer norm launch");
 }
@@ -474,10 +642,10 @@ srnl_status srnl_ln_backward(srnl_ln* h, const void* x, const void* dy, const vo
   if (rows < 0) return ln_fail(h, SRNL_E_INVAL, "rows must be >= 0");
   if (rows > 0 && (x == nullptr || dy == nullptr || dx == nullptr || gamma == nullptr || mean == nullptr || rstd == nullptr))
     return ln_fail(h, SRNL_E_INVAL, "x, dy, dx, gamma, mean or rstd is NULL");
-  if (!ln_aligned(x, 16) || !ln_aligned(dy, 16) || !ln_aligned(dres, 16) || !ln_aligned(dx, 16))
-    return ln_fail(h, SRNL_E_INVAL, "x, dy, dres and dx must be 16-byte aligned");
-  if (!ln_aligned(gamma, 4) || !ln_aligned(mean, 4) || !ln_aligned(rstd, 4) || !ln_aligned(dgamma, 4) || !ln_aligned(dbeta, 4))
-    return ln_fail(h, SRNL_E_INVAL, "gamma, mean, rstd, dgamma and dbeta must be 4-byte aligned");
+  if (!ln_aligned(x, 16) || !ln_aligned(dy, 16) || !ln_aligned(dres, 16) || !ln_aligned(dx, 16) || !ln_aligned(gamma, 16))
+    return ln_fail(h, SRNL_E_INVAL, "x, dy, dres, dx and gamma must be 16-byte aligned");
+  if (!ln_aligned(mean, 4) || !ln_aligned(rstd, 4) || !ln_aligned(dgamma, 4) || !ln_aligned(dbeta, 4))
+    return ln_fail(h, SRNL_E_INVAL, "mean, rstd, dgamma and dbeta must be 4-byte aligned");
   const bool bf16 = h->cfg.act_dtype == SRNL_BF16;
   const int dim = h->cfg.dim;
   const size_t n = (size_t)rows * dim * (bf16 ? 2 : 4), nr = (size_t)rows * 4, nd = (size_t)dim * 4;
@@ -493,22 +661,30 @@ srnl_status srnl_ln_backward(srnl_ln* h, const void* x, const void* dy, const vo
   if (st != SRNL_OK) return st;
   const srnl::NormPlan& p = h->plan;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int blocks = srnl::norm_blocks(p, rows, h->sms, srnl::kNormWaves);
+  const int threads = p.lpr == 0 ? p.threads : 128, blocks = srnl::norm_blocks(p, threads, rows, h->sms, h->bwd_per_sm);
   if (rows > 0) {
-    const size_t smem = p.lpr == 0 ? 0 : (size_t)2 * dim * sizeof(float);
-#define SRNL_NORM_BWD(T, V, LPR, PER)                                                                              \
-  srnl::norm_backward_kernel<T, V, LPR, PER><<<blocks, p.threads, smem, s>>>(                                      \
-      static_cast<const T*>(x), static_cast<const T*>(dy), static_cast<const T*>(dres), gamma, mean, rstd,         \
+    const size_t smem = p.lpr == 0 ? 0 : (size_t)(threads / 32) * 2 * dim * sizeof(float);
+#define SRNL_NORM_RUN(T, LPR, PER, R, ODD)                                                                     \
+  srnl::norm_backward_kernel<T, LPR, PER, R, ODD><<<blocks, threads, smem, s>>>(                               \
+      static_cast<const T*>(x), static_cast<const T*>(dy), static_cast<const T*>(dres), gamma, mean, rstd,     \
       static_cast<T*>(dx), h->part, rows, dim)
-    if (bf16) SRNL_NORM_DISPATCH(__nv_bfloat16, SRNL_NORM_BWD);
-    else SRNL_NORM_DISPATCH(float, SRNL_NORM_BWD);
-#undef SRNL_NORM_BWD
+    SRNL_NORM_DISPATCH(false, SRNL_NORM_RUN);
+#undef SRNL_NORM_RUN
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return ln_cuda_fail(h, e, "layer norm backward launch");
   }
   if (dgamma != nullptr || dbeta != nullptr) {
-    srnl::norm_weight_grad_kernel<<<(2 * dim + 31) / 32, 1024, 0, s>>>(h->part, blocks, dim, dgamma, dbeta);
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t lc{};
+    lc.gridDim = dim3((unsigned)((2 * dim + 31) / 32));
+    lc.blockDim = dim3(1024);
+    lc.stream = s;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = &at;
+    lc.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&lc, srnl::norm_weight_grad_kernel, static_cast<const float*>(h->part), blocks,
+                                             dim, dgamma, dbeta);
     if (e != cudaSuccess) return ln_cuda_fail(h, e, "layer norm weight gradient launch");
   }
   return SRNL_OK;

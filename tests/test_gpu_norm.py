@@ -56,7 +56,8 @@ def reference(t, eps):
 
 SHAPES = [(1, 1), (5, 3), (1, 8), (7, 33), (3, 64), (1000, 64), (37, 100), (65, 128), (9, 129), (130, 256), (21, 257),
           (196, 384), (11, 512), (13, 513), (50, 1000), (600, 1024), (5, 1025), (17, 2048), (301, 2560), (9, 4096),
-          (3, 8191), (4, 8192), (5000, 96)]
+          (3, 8191), (4, 8192), (5000, 96), (4001, 7), (3003, 2051), (2500, 1023), (700, 4096), (1, 8192),
+          (2000, 8), (999, 2044)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -234,6 +235,7 @@ def test_refusals():
         refused("overlaps", y=x)
         buf = torch.zeros(5 * 64 + 8, device="cuda", dtype=torch.bfloat16)
         refused("aligned", x=buf[1:321].view(5, 64))
+        refused("aligned", gamma=torch.ones(65, device="cuda")[1:])
         refused("overlap", mean=torch.zeros(5, device="cuda"), rstd=y.view(torch.float32).view(-1)[:5])
         st = torch.zeros(5, device="cuda")
         with pytest.raises(S.SrnlError) as e:
