@@ -168,6 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 1u;   // the ring starts empty
+      const uint32_t lead = map_rank(smem_u32(full), 0), ring = smem_u32(smem);
       for (int t = pair; t < tiles; t += pairs) {
         int tm, tn;
         tile_of(t, args, tm, tn);
@@ -179,11 +180,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           const int k = (it - (two ? args.k0 : 0)) * kTileK;
           const CUtensorMap* am = &maps.a[args.stack != 0 ? second : two];
           const CUtensorMap* bm = &maps.b[EPI == kGlu ? (int)rank : two];
-          mbar_wait(&empty[s], ph, failed);
-          if (*reinterpret_cast<volatile int*>(failed)) break;
+          if (!mbar_pass(&empty[s], ph, failed)) break;
           if (rank == 0) mbar_expect(&full[s], 2 * kStage);
-          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
-          const uint32_t as = smem_u32(smem + s * kStage), bs = as + kABytes;
+          const uint32_t bar = lead + (uint32_t)s * 8, as = ring + s * kStage, bs = as + kABytes;
           if constexpr (AMN) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) tma_load_pair(as + i * 8192, am, m0 + 64 * i, k, bar);
@@ -205,15 +204,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       constexpr uint32_t idesc = idesc_mn(kTileM, BN, AMN, BMN);
       int s = 0, buf = 0;
       uint32_t ph = 0u, tph = 1u;   // the accumulators start empty
+      const uint32_t ring = smem_u32(smem);
+      const uint64_t ad0 = AMN ? desc_mn_major(ring, 8192) : desc_k_major(ring);
+      const uint64_t bd0 = BMN ? desc_mn_major(ring + kABytes, 8192) : desc_k_major(ring + kABytes);
       for (int t = pair; t < tiles; t += pairs) {
-        mbar_wait(&tempty[buf], tph, failed);
+        mbar_pass(&tempty[buf], tph, failed);
+        tmem_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * BN);
         for (int it = 0; it < ktot; ++it) {
-          mbar_wait(&full[s], ph, failed);
-          if (*reinterpret_cast<volatile int*>(failed)) break;
-          const uint32_t as = smem_u32(smem + s * kStage), bs = as + kABytes;
-          const uint64_t ad = AMN ? desc_mn_major(as, 8192) : desc_k_major(as);
-          const uint64_t bd = BMN ? desc_mn_major(bs, 8192) : desc_k_major(bs);
+          if (!mbar_pass(&full[s], ph, failed)) break;
+          tmem_fence_after();
+          const uint64_t ad = ad0 + (uint64_t)(s * (kStage >> 4)), bd = bd0 + (uint64_t)(s * (kStage >> 4));
 #pragma unroll
           for (int k = 0; k < kTileK / 16; ++k)
             mma_pair(acc, ad + (uint64_t)(k * (AMN ? 2048 : 32) >> 4), bd + (uint64_t)(k * (BMN ? 2048 : 32) >> 4),
