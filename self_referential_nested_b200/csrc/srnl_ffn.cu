@@ -73,11 +73,12 @@ __host__ __device__ constexpr int ring_stages(int epi, int bn) {
   return (int)((226 * 1024 - 2048 - kEpiWarps * epi_boxes(epi) * kBox) / stage_bytes(bn));
 }
 constexpr size_t ffn_smem(int epi, int bn) {
-  return 1024 + (size_t)ring_stages(epi, bn) * stage_bytes(bn) + kEpiWarps * epi_boxes(epi) * kBox + 512;
+  return 1024 + (size_t)ring_stages(epi, bn) * stage_bytes(bn) + kEpiWarps * epi_boxes(epi) * kBox + 512;   // 512: the barriers
 }
 
 struct FfnMaps {
   CUtensorMap a[2], b[2], o[3];
+  CUtensorMap in[2];   // kGluBack: gate, up
 };
 
 struct FfnArgs {
@@ -85,25 +86,31 @@ struct FfnArgs {
   int k0, k1;            // stages of the first and of the second operand pair
   int tiles_m, tiles_n;  // of all outputs
   int stack;             // tiles_m of the first of two stacked outputs (0: one output)
-  int act, save;
-  const __nv_bfloat16 *res, *gate, *up;
+  int save;
+  const __nv_bfloat16* res;
   int* err;
 };
 
-__device__ __forceinline__ void act_value(float v, int act, float& f) {
-  if (act == SRNL_ACT_SILU) f = __fdividef(v, 1.f + __expf(-v));
-  else f = 0.5f * v * (1.f + erff(v * 0.70710678118654752f));
-}
-
-__device__ __forceinline__ void act_grad(float v, int act, float& f, float& df) {
-  if (act == SRNL_ACT_SILU) {
+// act(v) and its derivative.  Both need one exponential and one reciprocal.  GELU's Phi is
+// 1 - erfc(v / sqrt 2) / 2 with erfc by Abramowitz and Stegun, Handbook of Mathematical
+// Functions, 7.1.26 (absolute error 1.5e-7, against 2^-9 of the bf16 it is rounded to): 14
+// instructions, where erff takes about 30 and bound the projections' epilogue (51 us at
+// 12544 x 256 x 1024).
+template <int ACT>
+__device__ __forceinline__ void activation(float v, float& f, float& df) {
+  if constexpr (ACT == SRNL_ACT_SILU) {
     const float p = __fdividef(1.f, 1.f + __expf(-v));
     f = v * p;
     df = fmaf(f, 1.f - p, p);
   } else {
-    const float p = 0.5f * (1.f + erff(v * 0.70710678118654752f));
+    const float z = fabsf(v) * 0.70710678118654752f;
+    const float t = __fdividef(1.f, fmaf(0.3275911f, z, 1.f));
+    const float e = __expf(-z * z);
+    const float c = t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+    const float tail = 0.5f * c * e;
+    const float p = v >= 0.f ? 1.f - tail : tail;
     f = v * p;
-    df = fmaf(v * 0.3989422804014327f, __expf(-0.5f * v * v), p);
+    df = fmaf(v * 0.3989422804014327f, e, p);
   }
 }
 
@@ -122,7 +129,7 @@ __device__ __forceinline__ uint4 load8_row(const __nv_bfloat16* p, bool on) {
   return on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
-template <bool AMN, bool BMN, int EPI, int BN>
+template <bool AMN, bool BMN, int EPI, int ACT, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     ffn_product_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs args) {
   constexpr int S = ring_stages(EPI, BN);
@@ -134,7 +141,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
   unsigned char* boxes = smem + S * kStage;
   unsigned long long* bars = reinterpret_cast<unsigned long long*>(boxes + kEpiWarps * epi_boxes(EPI) * kBox);
   unsigned long long *full = bars, *empty = bars + S, *tfull = bars + 2 * S, *tempty = bars + 2 * S + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 4);
+  unsigned long long* inbar = bars + 2 * S + 4;   // kGluBack: [warp][2], gate and up have arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(inbar + 2 * kEpiWarps);
   int* failed = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,6 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 2 * kEpiWarps);
     }
+    for (int i = 0; i < 2 * kEpiWarps; ++i) mbar_init(&inbar[i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -249,9 +258,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       }
     };
     auto reuse = [&]() {   // the tile about to be written has left
-      if (lane == 0) bulk_wait_read<EPI == kGluBack ? 0 : 1>();
+      if (lane == 0) bulk_wait_read<1>();
       __syncwarp();
     };
+    // kGluBack works in pieces of 32 rows x 32 columns (2 KB, 64-byte swizzle): gate and up arrive
+    // by TMA a piece ahead, dgate and dup are written over them and leave by TMA, h beside them.
+    constexpr int kPieces = kHalf / 32, kPiece = 2048;
+    unsigned long long* mybar = inbar + 2 * ew;
+    auto fetch = [&](int t, int c, int b) {   // lane 0: piece c of tile t into buffer b
+      int tm, tn;
+      tile_of(t, args, tm, tn);
+      const int row = tm * kTileM + (int)rank * 128 + quarter * 32, col = tn * BN + half * kHalf + 32 * c;
+      mbar_expect(&mybar[b], 2 * kPiece);
+      tma_load_own(smem_u32(box + b * 3 * kPiece), &maps.in[0], col, row, &mybar[b]);
+      tma_load_own(smem_u32(box + b * 3 * kPiece + kPiece), &maps.in[1], col, row, &mybar[b]);
+    };
+    int piece = 0;   // pieces so far: buffer piece & 1, phase (piece >> 1) & 1
+    if (EPI == kGluBack && lane == 0 && pair < tiles) fetch(pair, 0, 0);
     for (int t = pair; t < tiles; t += pairs) {
       int tm, tn;
       tile_of(t, args, tm, tn);
@@ -259,7 +282,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       const int row0 = (tm - (second ? args.stack : 0)) * kTileM + (int)rank * 128 + quarter * 32;
       const int row = row0 + lane;
       const uint32_t acc = tmem + (uint32_t)(buf * BN) + ((uint32_t)(32 * quarter) << 16);
-      mbar_wait(&tfull[buf], ph, failed);
+      mbar_pass(&tfull[buf], ph, failed);
+      tmem_fence_after();
       if constexpr (EPI == kGlu) {
         // this half's 64 hidden channels: gate in columns 64 half .., up 128 further
         const int c0 = tn * (BN / 2) + half * 64;
@@ -273,86 +297,96 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
             if (o != 2) tmem_ld32(g, acc + half * 64 + 32 * c);
             if (o != 1) tmem_ld32(u, acc + kHalf + half * 64 + 32 * c);
             tmem_wait_ld();
+            if (o == 0) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (o == 0) {
-                float a, d;
-                act_value(g[2 * i], args.act, a);
-                act_value(g[2 * i + 1], args.act, d);
-                w[i] = pack_bf16(a * u[2 * i], d * u[2 * i + 1]);
-              } else {
-                w[i] = o == 1 ? pack_bf16(g[2 * i], g[2 * i + 1]) : pack_bf16(u[2 * i], u[2 * i + 1]);
+              for (int i = 0; i < 16; ++i) {
+                float f0, f1, d;
+                activation<ACT>(g[2 * i], f0, d);
+                activation<ACT>(g[2 * i + 1], f1, d);
+                w[i] = pack_bf16(f0 * u[2 * i], f1 * u[2 * i + 1]);
               }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) w[i] = o == 1 ? pack_bf16(g[2 * i], g[2 * i + 1]) : pack_bf16(u[2 * i], u[2 * i + 1]);
             }
             stage32(b, c, w);
           }
           send(&maps.o[o], b, c0, row0);
           ++turn;
         }
+      } else if constexpr (EPI == kGluBack) {
+#pragma unroll 1
+        for (int c = 0; c < kPieces; ++c, ++piece) {
+          const int b = piece & 1, col = tn * BN + half * kHalf + 32 * c;
+          unsigned char* at = box + b * 3 * kPiece;
+          if (lane == 0) {   // the other buffer's results have left: the next piece may come
+            bulk_wait_read<0>();
+            if (c + 1 < kPieces) fetch(t, c + 1, b ^ 1);
+            else if (t + pairs < tiles) fetch(t + pairs, 0, b ^ 1);
+          }
+          __syncwarp();
+          float v[32];
+          tmem_ld32(v, acc + half * kHalf + 32 * c);
+          mbar_pass(&mybar[b], (piece >> 1) & 1, failed);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            unsigned char* p = at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4);
+            const uint4 g4 = *reinterpret_cast<const uint4*>(p), u4 = *reinterpret_cast<const uint4*>(p + kPiece);
+            const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w}, uw[4] = {u4.x, u4.y, u4.z, u4.w};
+            uint32_t dg[4], du[4], hh[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float v0 = v[8 * j + 2 * i], v1 = v[8 * j + 2 * i + 1], u0 = bf16_lo(uw[i]), u1 = bf16_hi(uw[i]);
+              float f0, d0, f1, d1;
+              activation<ACT>(bf16_lo(gw[i]), f0, d0);
+              activation<ACT>(bf16_hi(gw[i]), f1, d1);
+              dg[i] = pack_bf16(v0 * u0 * d0, v1 * u1 * d1);
+              du[i] = pack_bf16(v0 * f0, v1 * f1);
+              hh[i] = pack_bf16(f0 * u0, f1 * u1);
+            }
+            *reinterpret_cast<uint4*>(p) = make_uint4(dg[0], dg[1], dg[2], dg[3]);
+            *reinterpret_cast<uint4*>(p + kPiece) = make_uint4(du[0], du[1], du[2], du[3]);
+            *reinterpret_cast<uint4*>(p + 2 * kPiece) = make_uint4(hh[0], hh[1], hh[2], hh[3]);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (col < args.N && row0 < args.M)
+              for (int o = 0; o < 3; ++o) tma_store(&maps.o[o], smem_u32(at + o * kPiece), col, row0);
+            bulk_commit();
+          }
+        }
       } else {
 #pragma unroll 1
         for (int cb = 0; cb < kHalf / 64; ++cb) {
           const int col = tn * BN + half * kHalf + cb * 64;
-          unsigned char* b = box + (EPI == kGluBack ? 0 : (turn & 1) * kBox);
+          unsigned char* b = box + (turn & 1) * kBox;
           reuse();
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             float v[32];
             uint32_t w[16];
             const int64_t at = (int64_t)row * args.N + col + 32 * c;
-            if constexpr (EPI == kPlain) {
-              tmem_ld32(v, acc + half * kHalf + cb * 64 + 32 * c);
-              uint4 r[4];
-              if (args.res != nullptr)
+            tmem_ld32(v, acc + half * kHalf + cb * 64 + 32 * c);
+            uint4 r[4];
+            if (args.res != nullptr)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = load8_row(args.res + at + 8 * j, row < args.M && col + 32 * c + 8 * j < args.N);
-              tmem_wait_ld();
-              if (args.res != nullptr) {
-                const uint32_t* rw = reinterpret_cast<const uint32_t*>(r);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  v[2 * i] += bf16_lo(rw[i]);
-                  v[2 * i + 1] += bf16_hi(rw[i]);
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-              stage32(b, c, w);
-            } else {
-              uint4 gr[4], ur[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const bool on = row < args.M && col + 32 * c + 8 * j < args.N;
-                gr[j] = load8_row(args.gate + at + 8 * j, on);
-                ur[j] = load8_row(args.up + at + 8 * j, on);
-              }
-              tmem_ld32(v, acc + half * kHalf + cb * 64 + 32 * c);
-              tmem_wait_ld();
-              const uint32_t* gw = reinterpret_cast<const uint32_t*>(gr);
-              const uint32_t* uw = reinterpret_cast<const uint32_t*>(ur);
-              uint32_t wu[16], wh[16];
+              for (int j = 0; j < 4; ++j) r[j] = load8_row(args.res + at + 8 * j, row < args.M && col + 32 * c + 8 * j < args.N);
+            tmem_wait_ld();
+            if (args.res != nullptr) {
+              const uint32_t* rw = reinterpret_cast<const uint32_t*>(r);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                float f0, d0, f1, d1;
-                act_grad(bf16_lo(gw[i]), args.act, f0, d0);
-                act_grad(bf16_hi(gw[i]), args.act, f1, d1);
-                const float u0 = bf16_lo(uw[i]), u1 = bf16_hi(uw[i]);
-                w[i] = pack_bf16(v[2 * i] * u0 * d0, v[2 * i + 1] * u1 * d1);
-                wu[i] = pack_bf16(v[2 * i] * f0, v[2 * i + 1] * f1);
-                wh[i] = pack_bf16(f0 * u0, f1 * u1);
+                v[2 * i] += bf16_lo(rw[i]);
+                v[2 * i + 1] += bf16_hi(rw[i]);
               }
-              stage32(b, c, w);
-              stage32(b + kBox, c, wu);
-              stage32(b + 2 * kBox, c, wh);
             }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+            stage32(b, c, w);
           }
-          if constexpr (EPI == kPlain) {
-            send(&maps.o[second], b, col, row0);
-          } else {
-            send(&maps.o[0], b, col, row0);
-            send(&maps.o[1], b + kBox, col, row0);
-            send(&maps.o[2], b + 2 * kBox, col, row0);
-          }
+          send(&maps.o[second], b, col, row0);
           ++turn;
         }
       }
@@ -377,30 +411,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// bf16 [outer][inner] row-major, boxes of 64 inner values x `rows`.
-bool ffn_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int rows) {
+// bf16 [outer][inner] row-major, boxes of `cols` inner values (64: 128-byte swizzle, 32: 64-byte)
+// x `rows`.
+bool ffn_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int rows, int cols = 64) {
   const TensorMapEncoder enc = ffn_tensor_map_encoder();
   const cuuint64_t dim[2] = {(cuuint64_t)inner, (cuuint64_t)outer}, str[1] = {(cuuint64_t)inner * 2};
-  const cuuint32_t box[2] = {64u, (cuuint32_t)rows}, est[2] = {1u, 1u};
+  const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)rows}, est[2] = {1u, 1u};
   return enc != nullptr &&
          enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dim, str, box, est,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_INTERLEAVE_NONE,
+             cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int ceil_div(int64_t a, int b) { return (int)((a + b - 1) / b); }
 
-template <bool AMN, bool BMN, int EPI, int BN>
+template <bool AMN, bool BMN, int EPI, int ACT, int BN>
 cudaError_t launch_product(const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  ffn_product_kernel<AMN, BMN, EPI, BN><<<2 * pairs, kFfnThreads, ffn_smem(EPI, BN), s>>>(maps, a);
+  ffn_product_kernel<AMN, BMN, EPI, ACT, BN><<<2 * pairs, kFfnThreads, ffn_smem(EPI, BN), s>>>(maps, a);
   return cudaGetLastError();
 }
 
-template <bool AMN, bool BMN, int EPI, int BN>
+template <bool AMN, bool BMN, int EPI, int ACT, int BN>
 cudaError_t prepare_product() {
-  return cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  return cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, ACT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               (int)ffn_smem(EPI, BN));
 }
 
@@ -504,11 +540,13 @@ srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg) {
   if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dup, bytes);
   if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
-  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, false, kPlain, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kPlain, 256>();
-  if (e == cudaSuccess) e = prepare_product<true, true, kPlain, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_SILU, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_GELU, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kPlain, 0, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_SILU, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_GELU, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kPlain, 0, 256>();
+  if (e == cudaSuccess) e = prepare_product<true, true, kPlain, 0, 256>();
   if (e == cudaSuccess && ffn_tensor_map_encoder() == nullptr) e = cudaErrorNotSupported;
   if (e != cudaSuccess) {
     const srnl_status st = ffn_cuda_fail(nullptr, e, "feed-forward create");
@@ -543,12 +581,13 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   FfnArgs a{};
   a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
   a.tiles_m = ceil_div(M, kTileM); a.tiles_n = ceil_div(F, 128);
-  a.act = c.activation; a.save = gate != nullptr; a.err = h->dev_err;
+  a.save = gate != nullptr; a.err = h->dev_err;
   bool ok = ffn_map(&m.a[0], x, D, M, 128) && ffn_map(&m.b[0], p->W_gate, D, F, 128) &&
             ffn_map(&m.b[1], p->W_up, D, F, 128) && ffn_map(&m.o[0], h->hid, F, M, 32) &&
             (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32) && ffn_map(&m.o[2], up, F, M, 32)));
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  cudaError_t e = launch_product<false, false, kGlu, 256>(m, a, h->sms, s);
+  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, false, kGlu, SRNL_ACT_SILU, 256>(m, a, h->sms, s)
+                                                : launch_product<false, false, kGlu, SRNL_ACT_GELU, 256>(m, a, h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward projections launch");
   FfnArgs b{};
   b.M = rows; b.N = (int)D; b.k0 = ceil_div(F, kTileK);
@@ -556,7 +595,7 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   b.res = static_cast<const bf16*>(res); b.err = h->dev_err;
   ok = ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, 128) && ffn_map(&m.o[0], y, D, M, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  e = launch_product<false, false, kPlain, 256>(m, b, h->sms, s);
+  e = launch_product<false, false, kPlain, 0, 256>(m, b, h->sms, s);
   return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward output launch");
 }
 
@@ -598,12 +637,13 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
   FfnArgs a{};
   a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
   a.tiles_m = ceil_div(M, kTileM); a.tiles_n = ceil_div(F, 256);
-  a.act = c.activation; a.err = h->dev_err;
-  a.gate = static_cast<const bf16*>(gate); a.up = static_cast<const bf16*>(up);
+  a.err = h->dev_err;
   bool ok = ffn_map(&m.a[0], dy, D, M, 128) && ffn_map(&m.b[0], w.W_down, F, D, 64) &&
-            ffn_map(&m.o[0], h->dgate, F, M, 32) && ffn_map(&m.o[1], h->dup, F, M, 32) && ffn_map(&m.o[2], h->hid, F, M, 32);
+            ffn_map(&m.o[0], h->dgate, F, M, 32, 32) && ffn_map(&m.o[1], h->dup, F, M, 32, 32) &&
+            ffn_map(&m.o[2], h->hid, F, M, 32, 32) && ffn_map(&m.in[0], gate, F, M, 32, 32) && ffn_map(&m.in[1], up, F, M, 32, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  cudaError_t e = launch_product<false, true, kGluBack, 256>(m, a, h->sms, s);
+  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, true, kGluBack, SRNL_ACT_SILU, 256>(m, a, h->sms, s)
+                                                : launch_product<false, true, kGluBack, SRNL_ACT_GELU, 256>(m, a, h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward backward launch");
   if (dx != nullptr) {
     FfnArgs b{};
@@ -612,7 +652,7 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
     ok = ffn_map(&m.a[0], h->dgate, F, M, 128) && ffn_map(&m.a[1], h->dup, F, M, 128) &&
          ffn_map(&m.b[0], w.W_gate, D, F, 64) && ffn_map(&m.b[1], w.W_up, D, F, 64) && ffn_map(&m.o[0], dx, D, M, 32);
     if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<false, true, kPlain, 256>(m, b, h->sms, s);
+    e = launch_product<false, true, kPlain, 0, 256>(m, b, h->sms, s);
     if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward input gradient launch");
   }
   if (g.W_gate != nullptr || g.W_up != nullptr) {
@@ -627,7 +667,7 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
     ok = ffn_map(&m.a[0], d0, F, M, 64) && ffn_map(&m.b[0], x, D, M, 64) && ffn_map(&m.o[0], o0, D, F, 32) &&
          (!both || (ffn_map(&m.a[1], h->dup, F, M, 64) && ffn_map(&m.o[1], g.W_up, D, F, 32)));
     if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<true, true, kPlain, 256>(m, b, h->sms, s);
+    e = launch_product<true, true, kPlain, 0, 256>(m, b, h->sms, s);
     if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
   }
   if (g.W_down != nullptr) {
@@ -636,7 +676,7 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
     b.tiles_m = ceil_div(D, kTileM); b.tiles_n = ceil_div(F, 256); b.err = h->dev_err;
     ok = ffn_map(&m.a[0], dy, D, M, 64) && ffn_map(&m.b[0], h->hid, F, M, 64) && ffn_map(&m.o[0], g.W_down, F, D, 32);
     if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<true, true, kPlain, 256>(m, b, h->sms, s);
+    e = launch_product<true, true, kPlain, 0, 256>(m, b, h->sms, s);
     if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
   }
   return SRNL_OK;
