@@ -56,6 +56,8 @@ TensorMapEncoder ffn_tensor_map_encoder() {
 
 namespace {
 
+using bf16_t = __nv_bfloat16;
+
 constexpr int kTileM = 256;        // rows of a pair's tile (128 per CTA)
 constexpr int kTileK = 64;         // K per stage
 constexpr int kEpiWarps = 8;
@@ -172,6 +174,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
   cluster_sync();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *tmem_slot;
+  // Launched while the kernel before may still run: everything above touches only this CTA.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
 
   if (warp == 0) {
     if (lane == 0) {
@@ -241,11 +246,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     const uint32_t done = map_rank(smem_u32(tempty), 0);
     int buf = 0, turn = 0;
     uint32_t ph = 0u;
-    // bf16 pairs of 32 columns into a staging tile's columns 32 c .. : 16-byte units, swizzled
+    // bf16 pairs of 32 columns into a staging tile's columns 32 c .. : 16-byte units, swizzled as
+    // its map has it (rows of 128 bytes, or of 64 where a half has only 32 columns)
+    constexpr bool kNarrow = EPI == kGlu && BN == 128;
     auto stage32 = [&](unsigned char* b, int c, const uint32_t (&w)[16]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint4*>(b + lane * 128 + (((4 * c + j) ^ (lane & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(kNarrow ? b + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)
+                                          : b + lane * 128 + (((4 * c + j) ^ (lane & 7)) << 4)) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     };
     // hand a staging tile to the TMA; tiles wholly past an edge are not sent
@@ -285,17 +293,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       mbar_pass(&tfull[buf], ph, failed);
       tmem_fence_after();
       if constexpr (EPI == kGlu) {
-        // this half's 64 hidden channels: gate in columns 64 half .., up 128 further
-        const int c0 = tn * (BN / 2) + half * 64;
+        // this half's BN / 4 hidden channels: gate in its columns, up BN / 2 further
+        constexpr int kHid = BN / 4;
+        const int c0 = tn * (BN / 2) + half * kHid;
         for (int o = 0; o < (args.save ? 3 : 1); ++o) {
           unsigned char* b = box + (turn & 1) * kBox;
           reuse();
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < kHid / 32; ++c) {
             float g[32], u[32];
             uint32_t w[16];
-            if (o != 2) tmem_ld32(g, acc + half * 64 + 32 * c);
-            if (o != 1) tmem_ld32(u, acc + kHalf + half * 64 + 32 * c);
+            if (o != 2) tmem_ld32(g, acc + half * kHid + 32 * c);
+            if (o != 1) tmem_ld32(u, acc + kHalf + half * kHid + 32 * c);
             tmem_wait_ld();
             if (o == 0) {
 #pragma unroll
@@ -410,6 +419,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
   }
 }
 
+// ------------------------------------------------------------------ few rows
+// A handful of rows, as in serving one token of each sequence: the time is the weights' bytes,
+// so the kernels are built to stream them.  Weights' rows are the left operand of m16n8k16, the
+// tokens its columns: 8 rows of Wg and the same 8 of Wu in the first kernel, 16 of Wd in the
+// second; a block's warps split K.  A sum over K may run in any order, so a lane takes 8
+// consecutive values of K in one 16-byte load of each row and the two products of a 32-wide piece
+// use them as they lie; the tokens are loaded by the same rule, and nothing passes through shared
+// memory but the warps' sums.  Small blocks (8 channels; 5 to an SM) come out even over the SMs:
+// 5632 channels are 704 of them.
+constexpr int kFewRows = 32;
+
+__device__ __forceinline__ uint4 load_once(const bf16_t* p) {   // weights are met once: not kept in L1
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void mma_rows(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// GLU: out = act(x W^T) * (x W2^T), 8 channels a block, and the two products themselves where
+// asked; else out = x W^T (+ res), 16 channels.  NT: columns of 8 tokens; U: 32-wide pieces of K
+// in flight.
+template <bool GLU> __host__ __device__ constexpr int few_warps() { return GLU ? 8 : 16; }
+
+template <bool GLU, int ACT, int NT>
+__global__ void __launch_bounds__(few_warps<GLU>() * 32, GLU && NT == 1 ? 5 : 2)
+    ffn_few_rows_kernel(const bf16_t* __restrict__ x, const bf16_t* __restrict__ W, const bf16_t* __restrict__ W2,
+                        const bf16_t* __restrict__ res, bf16_t* __restrict__ out, bf16_t* __restrict__ gate,
+                        bf16_t* __restrict__ up, int rows, int N, int K) {
+  constexpr int kWarps = few_warps<GLU>(), U = GLU ? 2 : NT == 4 ? 2 : 4;
+  __shared__ float part[kWarps][16][8 * NT + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, kk = (lane & 3) * 8;
+  const int n0 = blockIdx.x * (GLU ? 8 : 16);
+  // the lane's two rows of the left operand
+  const bool on0 = n0 + g < N, on1 = GLU ? on0 : n0 + g + 8 < N;
+  const bf16_t *w0 = W + (int64_t)(n0 + g) * K, *w1 = GLU ? W2 + (int64_t)(n0 + g) * K : W + (int64_t)(n0 + g + 8) * K;
+  float acc[NT][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int k0 = warp * 32; k0 < K; k0 += kWarps * 32 * U) {   // the same passes in every lane: the products are the warp's
+    uint4 a[U][2], b[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kWarps * 32 + kk;
+      a[u][0] = k < K && on0 ? load_once(w0 + k) : zero;
+      a[u][1] = k < K && on1 ? load_once(w1 + k) : zero;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        const int r = t * 8 + g;
+        b[u][t] = k < K && r < rows ? *reinterpret_cast<const uint4*>(x + (int64_t)r * K + k) : zero;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        mma_rows(acc[t], a[u][0].x, a[u][1].x, a[u][0].y, a[u][1].y, b[u][t].x, b[u][t].y);
+        mma_rows(acc[t], a[u][0].z, a[u][1].z, a[u][0].w, a[u][1].w, b[u][t].z, b[u][t].w);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[warp][g + (e >> 1) * 8][t * 8 + (lane & 3) * 2 + (e & 1)] = acc[t][e];
+  __syncthreads();
+  constexpr int kChan = GLU ? 8 : 16;
+  for (int i = threadIdx.x; i < kChan * rows; i += kWarps * 32) {
+    const int c = i % kChan, r = i / kChan, n = n0 + c;
+    if (n >= N) continue;
+    float v = 0.f, u = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      v += part[w][c][r];
+      if (GLU) u += part[w][c + 8][r];
+    }
+    const int64_t at = (int64_t)r * N + n;
+    if constexpr (GLU) {
+      float f, d;
+      activation<ACT>(v, f, d);
+      out[at] = __float2bfloat16_rn(f * u);
+      if (gate != nullptr) {
+        gate[at] = __float2bfloat16_rn(v);
+        up[at] = __float2bfloat16_rn(u);
+      }
+    } else {
+      out[at] = __float2bfloat16_rn(res != nullptr ? v + __bfloat162float(res[at]) : v);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ host side
 // bf16 [outer][inner] row-major, boxes of `cols` inner values (64: 128-byte swizzle, 32: 64-byte)
 // x `rows`.
@@ -426,18 +533,63 @@ bool ffn_map(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int
 
 int ceil_div(int64_t a, int b) { return (int)((a + b - 1) / b); }
 
+// Launch that may begin while the kernel before on the stream runs out; the kernel itself waits
+// for that one's results (griddepcontrol.wait) before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...);
+}
+
 template <bool AMN, bool BMN, int EPI, int ACT, int BN>
 cudaError_t launch_product(const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
   const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  ffn_product_kernel<AMN, BMN, EPI, ACT, BN><<<2 * pairs, kFfnThreads, ffn_smem(EPI, BN), s>>>(maps, a);
-  return cudaGetLastError();
+  return launch_after(ffn_product_kernel<AMN, BMN, EPI, ACT, BN>, dim3(2 * pairs), kFfnThreads, ffn_smem(EPI, BN), s, maps, a);
 }
 
-template <bool AMN, bool BMN, int EPI, int ACT, int BN>
+template <bool AMN, bool BMN, int EPI, int ACT>
+cudaError_t launch_product(int bn, const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
+  return bn == 256 ? launch_product<AMN, BMN, EPI, ACT, 256>(maps, a, sms, s) : launch_product<AMN, BMN, EPI, ACT, 128>(maps, a, sms, s);
+}
+
+template <bool AMN, bool BMN, int EPI, int ACT>
 cudaError_t prepare_product() {
-  return cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, ACT, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)ffn_smem(EPI, BN));
+  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, ACT, 256>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 256));
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, ACT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)ffn_smem(EPI, 128));
+  return e;
+}
+
+template <bool GLU, int ACT>
+cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, const bf16_t* res, bf16_t* out, bf16_t* gate,
+                            bf16_t* up, int rows, int N, int K, cudaStream_t s) {
+  const dim3 grid((unsigned)(GLU ? (N + 7) / 8 : (N + 15) / 16));
+  const int t = few_warps<GLU>() * 32;
+  if (rows <= 8) return launch_after(ffn_few_rows_kernel<GLU, ACT, 1>, grid, t, 0, s, x, W, W2, res, out, gate, up, rows, N, K);
+  if (rows <= 16) return launch_after(ffn_few_rows_kernel<GLU, ACT, 2>, grid, t, 0, s, x, W, W2, res, out, gate, up, rows, N, K);
+  return launch_after(ffn_few_rows_kernel<GLU, ACT, 4>, grid, t, 0, s, x, W, W2, res, out, gate, up, rows, N, K);
+}
+
+// Columns of a pair's tile for a product of tiles_m x n: 256, or 128 where that fills the SMs
+// better.  A 128-column tile reads as much of A for half the work and takes about 0.8 of a
+// 256-column one (8192 x 2048 x 11264: 409 us in 7 waves of them, 259 us in 4; 1531 x 1384 x 520
+// in one wave each: 16 us against 20).
+int pick_bn(int64_t tiles_m, int64_t n, int sms) {
+  const int64_t pairs = sms / 2;
+  const int64_t w256 = (tiles_m * ((n + 255) / 256) + pairs - 1) / pairs, w128 = (tiles_m * ((n + 127) / 128) + pairs - 1) / pairs;
+  return 10 * w128 < 12 * w256 ? 128 : 256;
 }
 
 }  // namespace
@@ -540,13 +692,13 @@ srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg) {
   if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dup, bytes);
   if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
-  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_SILU, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_GELU, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, false, kPlain, 0, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_SILU, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_GELU, 256>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kPlain, 0, 256>();
-  if (e == cudaSuccess) e = prepare_product<true, true, kPlain, 0, 256>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_SILU>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_GELU>();
+  if (e == cudaSuccess) e = prepare_product<false, false, kPlain, 0>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_SILU>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_GELU>();
+  if (e == cudaSuccess) e = prepare_product<false, true, kPlain, 0>();
+  if (e == cudaSuccess) e = prepare_product<true, true, kPlain, 0>();
   if (e == cudaSuccess && ffn_tensor_map_encoder() == nullptr) e = cudaErrorNotSupported;
   if (e != cudaSuccess) {
     const srnl_status st = ffn_cuda_fail(nullptr, e, "feed-forward create");
@@ -576,26 +728,41 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   const srnl_status st = ffn_check(h, in, 5, out, 3);
   if (st != SRNL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows <= kFewRows) {
+    const auto w = [](const void* q) { return static_cast<const bf16*>(q); };
+    bf16 *gk = static_cast<bf16*>(gate), *uk = static_cast<bf16*>(up);
+    cudaError_t e = c.activation == SRNL_ACT_SILU
+        ? launch_few_rows<true, SRNL_ACT_SILU>(w(x), w(p->W_gate), w(p->W_up), nullptr, h->hid, gk, uk, rows, (int)F, (int)D, s)
+        : launch_few_rows<true, SRNL_ACT_GELU>(w(x), w(p->W_gate), w(p->W_up), nullptr, h->hid, gk, uk, rows, (int)F, (int)D, s);
+    if (e == cudaSuccess)
+      e = launch_few_rows<false, 0>(h->hid, w(p->W_down), nullptr, w(res), static_cast<bf16*>(y), nullptr, nullptr, rows, (int)D, (int)F, s);
+    return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward few-row launch");
+  }
   FfnMaps m;
   memset(&m, 0, sizeof m);
   FfnArgs a{};
   a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
-  a.tiles_m = ceil_div(M, kTileM); a.tiles_n = ceil_div(F, 128);
+  a.tiles_m = ceil_div(M, kTileM);
+  int bn = pick_bn(a.tiles_m, 2 * F, h->sms);
+  a.tiles_n = ceil_div(F, bn / 2);
   a.save = gate != nullptr; a.err = h->dev_err;
-  bool ok = ffn_map(&m.a[0], x, D, M, 128) && ffn_map(&m.b[0], p->W_gate, D, F, 128) &&
-            ffn_map(&m.b[1], p->W_up, D, F, 128) && ffn_map(&m.o[0], h->hid, F, M, 32) &&
-            (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32) && ffn_map(&m.o[2], up, F, M, 32)));
+  const int cols = bn / 4;   // of a staging tile
+  bool ok = ffn_map(&m.a[0], x, D, M, 128) && ffn_map(&m.b[0], p->W_gate, D, F, bn / 2) &&
+            ffn_map(&m.b[1], p->W_up, D, F, bn / 2) && ffn_map(&m.o[0], h->hid, F, M, 32, cols) &&
+            (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32, cols) && ffn_map(&m.o[2], up, F, M, 32, cols)));
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, false, kGlu, SRNL_ACT_SILU, 256>(m, a, h->sms, s)
-                                                : launch_product<false, false, kGlu, SRNL_ACT_GELU, 256>(m, a, h->sms, s);
+  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, false, kGlu, SRNL_ACT_SILU>(bn, m, a, h->sms, s)
+                                                : launch_product<false, false, kGlu, SRNL_ACT_GELU>(bn, m, a, h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward projections launch");
   FfnArgs b{};
   b.M = rows; b.N = (int)D; b.k0 = ceil_div(F, kTileK);
-  b.tiles_m = a.tiles_m; b.tiles_n = ceil_div(D, 256);
+  b.tiles_m = a.tiles_m;
+  bn = pick_bn(b.tiles_m, D, h->sms);
+  b.tiles_n = ceil_div(D, bn);
   b.res = static_cast<const bf16*>(res); b.err = h->dev_err;
-  ok = ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, 128) && ffn_map(&m.o[0], y, D, M, 32);
+  ok = ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, bn / 2) && ffn_map(&m.o[0], y, D, M, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  e = launch_product<false, false, kPlain, 0, 256>(m, b, h->sms, s);
+  e = launch_product<false, false, kPlain, 0>(bn, m, b, h->sms, s);
   return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward output launch");
 }
 
@@ -636,23 +803,27 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
   // dgate, dup and h from dh = dy Wd
   FfnArgs a{};
   a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
-  a.tiles_m = ceil_div(M, kTileM); a.tiles_n = ceil_div(F, 256);
+  a.tiles_m = ceil_div(M, kTileM);
+  int bn = pick_bn(a.tiles_m, F, h->sms);
+  a.tiles_n = ceil_div(F, bn);
   a.err = h->dev_err;
   bool ok = ffn_map(&m.a[0], dy, D, M, 128) && ffn_map(&m.b[0], w.W_down, F, D, 64) &&
             ffn_map(&m.o[0], h->dgate, F, M, 32, 32) && ffn_map(&m.o[1], h->dup, F, M, 32, 32) &&
             ffn_map(&m.o[2], h->hid, F, M, 32, 32) && ffn_map(&m.in[0], gate, F, M, 32, 32) && ffn_map(&m.in[1], up, F, M, 32, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, true, kGluBack, SRNL_ACT_SILU, 256>(m, a, h->sms, s)
-                                                : launch_product<false, true, kGluBack, SRNL_ACT_GELU, 256>(m, a, h->sms, s);
+  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, true, kGluBack, SRNL_ACT_SILU>(bn, m, a, h->sms, s)
+                                                : launch_product<false, true, kGluBack, SRNL_ACT_GELU>(bn, m, a, h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward backward launch");
   if (dx != nullptr) {
     FfnArgs b{};
     b.M = rows; b.N = (int)D; b.k0 = b.k1 = ceil_div(F, kTileK);
-    b.tiles_m = a.tiles_m; b.tiles_n = ceil_div(D, 256); b.err = h->dev_err;
+    b.tiles_m = a.tiles_m;
+    bn = pick_bn(b.tiles_m, D, h->sms);
+    b.tiles_n = ceil_div(D, bn); b.err = h->dev_err;
     ok = ffn_map(&m.a[0], h->dgate, F, M, 128) && ffn_map(&m.a[1], h->dup, F, M, 128) &&
          ffn_map(&m.b[0], w.W_gate, D, F, 64) && ffn_map(&m.b[1], w.W_up, D, F, 64) && ffn_map(&m.o[0], dx, D, M, 32);
     if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<false, true, kPlain, 0, 256>(m, b, h->sms, s);
+    e = launch_product<false, true, kPlain, 0>(bn, m, b, h->sms, s);
     if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward input gradient launch");
   }
   if (g.W_gate != nullptr || g.W_up != nullptr) {
@@ -663,20 +834,24 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
     FfnArgs b{};
     b.M = (int)F; b.N = (int)D; b.k0 = ceil_div(M, kTileK);
     b.stack = both ? ceil_div(F, kTileM) : 0;
-    b.tiles_m = ceil_div(F, kTileM) * (both ? 2 : 1); b.tiles_n = ceil_div(D, 256); b.err = h->dev_err;
+    b.tiles_m = ceil_div(F, kTileM) * (both ? 2 : 1);
+    bn = pick_bn(b.tiles_m, D, h->sms);
+    b.tiles_n = ceil_div(D, bn); b.err = h->dev_err;
     ok = ffn_map(&m.a[0], d0, F, M, 64) && ffn_map(&m.b[0], x, D, M, 64) && ffn_map(&m.o[0], o0, D, F, 32) &&
          (!both || (ffn_map(&m.a[1], h->dup, F, M, 64) && ffn_map(&m.o[1], g.W_up, D, F, 32)));
     if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<true, true, kPlain, 0, 256>(m, b, h->sms, s);
+    e = launch_product<true, true, kPlain, 0>(bn, m, b, h->sms, s);
     if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
   }
   if (g.W_down != nullptr) {
     FfnArgs b{};
     b.M = (int)D; b.N = (int)F; b.k0 = ceil_div(M, kTileK);
-    b.tiles_m = ceil_div(D, kTileM); b.tiles_n = ceil_div(F, 256); b.err = h->dev_err;
+    b.tiles_m = ceil_div(D, kTileM);
+    bn = pick_bn(b.tiles_m, F, h->sms);
+    b.tiles_n = ceil_div(F, bn); b.err = h->dev_err;
     ok = ffn_map(&m.a[0], dy, D, M, 64) && ffn_map(&m.b[0], h->hid, F, M, 64) && ffn_map(&m.o[0], g.W_down, F, D, 32);
     if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<true, true, kPlain, 0, 256>(m, b, h->sms, s);
+    e = launch_product<true, true, kPlain, 0>(bn, m, b, h->sms, s);
     if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
   }
   return SRNL_OK;
