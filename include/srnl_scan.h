@@ -592,6 +592,10 @@ SRNL_API srnl_status srnl_lattn_backward(srnl_lattn* h, const void* q, const voi
 SRNL_API srnl_status srnl_lattn_step(srnl_lattn* h, const void* q, const void* k, const void* v, void* o, float* state,
                                      void* stream);
 
+/* Synchronously reads the status word of the handle's kernels: SRNL_OK, or SRNL_E_TIMEOUT once
+ * a bounded in-kernel wait gave up. */
+SRNL_API srnl_status srnl_lattn_device_status(srnl_lattn* h);
+
 /* Message for the last failure on this handle (h == NULL: the calling thread's last
  * srnl_lattn_create failure).  Never NULL. */
 SRNL_API const char* srnl_lattn_last_error(const srnl_lattn* h);

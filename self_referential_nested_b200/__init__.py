@@ -44,7 +44,7 @@ EXPORTED = ("srnl_scan_create", "srnl_scan_forward", "srnl_scan_forward_host",
             "srnl_ffn_create", "srnl_ffn_forward", "srnl_ffn_backward", "srnl_ffn_device_status",
             "srnl_ffn_last_error", "srnl_ffn_destroy",
             "srnl_lattn_create", "srnl_lattn_forward", "srnl_lattn_backward", "srnl_lattn_step",
-            "srnl_lattn_last_error", "srnl_lattn_destroy")
+            "srnl_lattn_device_status", "srnl_lattn_last_error", "srnl_lattn_destroy")
 
 
 class SrnlError(RuntimeError):
@@ -202,6 +202,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.srnl_lattn_forward.argtypes = [vp] * 9
     lib.srnl_lattn_backward.argtypes = [vp] * 13
     lib.srnl_lattn_step.argtypes = [vp] * 7
+    lib.srnl_lattn_device_status.argtypes = [vp]
     lib.srnl_lattn_last_error.argtypes = [vp]
     lib.srnl_lattn_last_error.restype = ctypes.c_char_p
     lib.srnl_lattn_destroy.argtypes = [vp]
@@ -216,7 +217,7 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
                  "srnl_block_forward", "srnl_block_device_status", "srnl_ln_create", "srnl_ln_forward",
                  "srnl_ln_backward", "srnl_ffn_create", "srnl_ffn_forward", "srnl_ffn_backward",
                  "srnl_ffn_device_status", "srnl_lattn_create", "srnl_lattn_forward", "srnl_lattn_backward",
-                 "srnl_lattn_step"):
+                 "srnl_lattn_step", "srnl_lattn_device_status"):
         getattr(lib, name).restype = ctypes.c_int
     if path is None:
         _lib = lib
@@ -815,3 +816,8 @@ def srnl_lattn_step(h: SrnlLattn, q, k, v, o, state, stream=None) -> None:
         hd, h._rows(q, w, "q", 0), h._rows(k, w, "k", 0), h._rows(v, w, "v", 0),
         _dense(h, o, w, "o", h._dtype, c.B * c.heads * c.d),
         _dense(h, state, w, "state", h._f32, c.B * c.heads * c.d * c.d), _stream(stream)), w)
+
+
+def srnl_lattn_device_status(h: SrnlLattn) -> None:
+    """Raise SrnlError if a bounded in-kernel wait of this handle ever gave up."""
+    h._check(load_library().srnl_lattn_device_status(h.handle), "srnl_lattn_device_status")

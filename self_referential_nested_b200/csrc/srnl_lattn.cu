@@ -16,8 +16,11 @@
 // so all powers are of g <= 1 with exponents >= 0 and nothing overflows.
 //
 // Roundings: the state is fp32 throughout.  As an operand of a Z it is split into two bf16
-// parts (16 bits), as are the decayed rows of the state's update; the masked a b^T is rounded
-// to bf16 once; out is rounded once.
+// parts (16 bits), and so are the decayed rows of the state's update, into three where the state
+// itself is asked for; the masked a b^T is rounded to bf16 once; out is rounded once.
+//
+// Heads of 64 and 128 channels run on tcgen05 (srnl_lattn_tc.cu), 32-wide ones here: their
+// products are too narrow for its 128 rows and go by mma.sync.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,30 +32,13 @@
 
 #include "srnl_common.cuh"
 #include "srnl_internal.h"
+#include "srnl_lattn.h"
 #include "srnl_scan.h"
 
 namespace srnl {
 namespace {
 
 using bf16 = __nv_bfloat16;
-
-struct LaPass {
-  const bf16 *a, *b, *c;
-  bf16* out;
-  int64_t lda, ldb, ldc, ldo;   // elements between tokens
-  const float* z0;              // [B][heads][D][D] or nullptr
-  float* zn;                    // final state or nullptr
-  int z0_t;                     // z0 is the transpose of Z
-  int reverse;                  // tokens from the last to the first; z0 enters undecayed, zn leaves decayed once more
-};
-
-struct LaArgs {
-  LaPass pass[3];
-  int passes, B, T, heads, segs, seg_len;   // segments of seg_len tokens per sequence
-  const float* log2g;                       // [heads]
-  const int* lengths;                       // [B] or nullptr
-  float* seg_state;                         // [pass][B][heads][segs][D][D]: what each segment adds
-};
 
 __device__ __forceinline__ uint32_t s_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
@@ -73,15 +59,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-template <int D>
-struct LaShape {
-  static constexpr int kWarps = D == 128 ? 8 : 4;
-  static constexpr int C = 16 * kWarps;         // tokens per chunk: a warp takes 16 of its rows
-  static constexpr int kPitch = D * 2 + 16;     // bytes of a shared row: ldmatrix rows in distinct banks
-  static constexpr int kColGroups = D == 32 ? 2 : 1;   // the state's columns over warps (D = 32: 2 x 2 warps)
-  static constexpr int kCols = D / kColGroups;
-  static constexpr size_t kSmem = (size_t)(3 * C + 2 * D) * kPitch + C * 4;
-};
+constexpr int kD32 = 32, kWarps32 = 4;
+constexpr int kC32 = 16 * kWarps32;        // tokens per chunk: a warp takes 16 of its rows
+constexpr int kPitch32 = kD32 * 2 + 16;    // bytes of a shared row: ldmatrix rows in distinct banks
+constexpr int kCols32 = 16;                // the state over 2 x 2 warps: 16 rows x 16 columns each
+constexpr size_t kSmem32 = (size_t)(3 * kC32 + 2 * kD32) * kPitch32 + kC32 * 4;
 
 // z <- g^m z.  A factor near one is applied as z + (g^m - 1) z: rounded to fp32 it would be off
 // by the same half step in every chunk, which thousands of chunks add up.
@@ -98,14 +80,13 @@ __device__ __forceinline__ void decay_state(float (&z)[NB][4], float lg, int m) 
 
 // One CTA per (segment, sequence and head, pass).  kStateOnly: the state that the segment adds,
 // from zero, to seg_state; otherwise the outputs, from the state at the segment's start.
-template <int D, bool kStateOnly>
-__global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(const __grid_constant__ LaArgs args) {
-  using L = LaShape<D>;
-  constexpr int C = L::C, NB = L::kCols / 8;
+template <bool kStateOnly>
+__global__ void __launch_bounds__(kWarps32 * 32) decay_pass_kernel(const __grid_constant__ LaArgs args) {
+  constexpr int D = kD32, C = kC32, NB = kCols32 / 8;
   extern __shared__ __align__(16) unsigned char sm[];
-  unsigned char *sa = sm, *sb = sa + C * L::kPitch, *sc = sb + C * L::kPitch, *zh = sc + C * L::kPitch,
-                *zl = zh + D * L::kPitch;
-  float* w = reinterpret_cast<float*>(zl + D * L::kPitch);   // g^(count - 1 - j)
+  unsigned char *sa = sm, *sb = sa + C * kPitch32, *sc = sb + C * kPitch32, *zh = sc + C * kPitch32,
+                *zl = zh + D * kPitch32;
+  float* w = reinterpret_cast<float*>(zl + D * kPitch32);   // g^(count - 1 - j)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const LaPass& P = args.pass[blockIdx.z];
   const int seg = blockIdx.x, head = blockIdx.y % args.heads, batch = blockIdx.y / args.heads;
@@ -116,8 +97,8 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
   const int64_t zbase = ((int64_t)batch * args.heads + head) * D * D;
   const int64_t sbase = (((int64_t)blockIdx.z * args.B + batch) * args.heads + head) * args.segs * D * D;
 
-  // the warp's part of the state: rows zr .. zr + 15, columns zc .. zc + kCols - 1
-  const int zr = (warp / L::kColGroups) * 16, zc = (warp % L::kColGroups) * L::kCols;
+  // the warp's part of the state: rows zr .. zr + 15, columns zc .. zc + 15
+  const int zr = (warp >> 1) * 16, zc = (warp & 1) * kCols32;
   const int r0 = lane >> 2, c0 = (lane & 3) * 2;
   float z[NB][4];
 #pragma unroll
@@ -149,7 +130,7 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
     const int lead = (P.reverse && t0 == 0) ? 0 : 1;
     __syncthreads();   // the previous chunk's readers are done
     constexpr int V = D / 8;
-    for (int idx = tid; idx < C * V; idx += L::kWarps * 32) {
+    for (int idx = tid; idx < C * V; idx += kWarps32 * 32) {
       const int i = idx / V, v = idx - i * V;
       const bool on = i < cnt;
       const int t = P.reverse ? n - 1 - (t0 + i) : t0 + i;
@@ -157,11 +138,11 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
       const int col = head * D + v * 8;
       const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
       if constexpr (!kStateOnly)
-        *reinterpret_cast<uint4*>(sa + i * L::kPitch + v * 16) = on ? *reinterpret_cast<const uint4*>(P.a + row * P.lda + col) : zero;
-      *reinterpret_cast<uint4*>(sb + i * L::kPitch + v * 16) = on ? *reinterpret_cast<const uint4*>(P.b + row * P.ldb + col) : zero;
-      *reinterpret_cast<uint4*>(sc + i * L::kPitch + v * 16) = on ? *reinterpret_cast<const uint4*>(P.c + row * P.ldc + col) : zero;
+        *reinterpret_cast<uint4*>(sa + i * kPitch32 + v * 16) = on ? *reinterpret_cast<const uint4*>(P.a + row * P.lda + col) : zero;
+      *reinterpret_cast<uint4*>(sb + i * kPitch32 + v * 16) = on ? *reinterpret_cast<const uint4*>(P.b + row * P.ldb + col) : zero;
+      *reinterpret_cast<uint4*>(sc + i * kPitch32 + v * 16) = on ? *reinterpret_cast<const uint4*>(P.c + row * P.ldc + col) : zero;
     }
-    for (int j = tid; j < C; j += L::kWarps * 32) w[j] = j < cnt ? exp2f(lg * (float)(cnt - 1 - j)) : 0.f;
+    for (int j = tid; j < C; j += kWarps32 * 32) w[j] = j < cnt ? exp2f(lg * (float)(cnt - 1 - j)) : 0.f;
     if constexpr (!kStateOnly) {
 #pragma unroll
       for (int i = 0; i < NB; ++i)
@@ -169,7 +150,7 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
         for (int h = 0; h < 2; ++h) {
           const float x = z[i][2 * h], y = z[i][2 * h + 1];
           const uint32_t hw = pack2(x, y);
-          const uint32_t off = (uint32_t)(zr + r0 + 8 * h) * L::kPitch + (zc + i * 8 + c0) * 2;
+          const uint32_t off = (uint32_t)(zr + r0 + 8 * h) * kPitch32 + (zc + i * 8 + c0) * 2;
           *reinterpret_cast<uint32_t*>(zh + off) = hw;
           *reinterpret_cast<uint32_t*>(zl + off) = pack2(x - lo_f(hw), y - hi_f(hw));
         }
@@ -179,7 +160,7 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
     if constexpr (!kStateOnly) {
       const int row = warp * 16;
       // a's rows as the left operand: lanes 0-15 rows, the upper half 8 columns on
-      const uint32_t a_at = s_u32(sa) + (row + (lane & 15)) * L::kPitch + (lane >> 4) * 16;
+      const uint32_t a_at = s_u32(sa) + (row + (lane & 15)) * kPitch32 + (lane >> 4) * 16;
       float o[D / 8][4];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
@@ -193,7 +174,7 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t bh[4], bl[4];
-          const uint32_t off = (k * 16 + t_row) * L::kPitch + (i * 16 + t_col) * 2;
+          const uint32_t off = (k * 16 + t_row) * kPitch32 + (i * 16 + t_col) * 2;
           ldm4t(bh, s_u32(zh) + off);
           ldm4t(bl, s_u32(zl) + off);
           mma16816(o[2 * i], af, bh[0], bh[1]);
@@ -213,7 +194,7 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
 #pragma unroll 1
       for (int jb = 0; jb <= warp; ++jb) {
         float p[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const uint32_t b_at = s_u32(sb) + (jb * 16 + (lane & 7) + (lane >> 4) * 8) * L::kPitch + ((lane >> 3) & 1) * 16;
+        const uint32_t b_at = s_u32(sb) + (jb * 16 + (lane & 7) + (lane >> 4) * 8) * kPitch32 + ((lane >> 3) & 1) * 16;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t af[4], bf[4];
@@ -233,7 +214,7 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           uint32_t cf[4];
-          ldm4t(cf, s_u32(sc) + (jb * 16 + t_row) * L::kPitch + (i * 16 + t_col) * 2);
+          ldm4t(cf, s_u32(sc) + (jb * 16 + t_row) * kPitch32 + (i * 16 + t_col) * 2);
           mma16816(o[2 * i], pf, cf[0], cf[1]);
           mma16816(o[2 * i + 1], pf, cf[2], cf[3]);
         }
@@ -255,23 +236,29 @@ __global__ void __launch_bounds__(LaShape<D>::kWarps * 32) decay_pass_kernel(con
 #pragma unroll 2
     for (int k = 0; k < C / 16; ++k) {
       // b^T as the left operand: blocks (rows of Z, tokens) in the order of the fragment
-      uint32_t bt[4], ah[4], al[4];
-      ldm4t(bt, s_u32(sb) + (k * 16 + (lane & 7) + (lane >> 4) * 8) * L::kPitch + (zr + ((lane >> 3) & 1) * 8) * 2);
+      uint32_t bt[4], ah[4], al[4], ar[4];
+      ldm4t(bt, s_u32(sb) + (k * 16 + (lane & 7) + (lane >> 4) * 8) * kPitch32 + (zr + ((lane >> 3) & 1) * 8) * 2);
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int j = k * 16 + (h >> 1) * 8 + c0;
         const float x = lo_f(bt[h]) * w[j], y = hi_f(bt[h]) * w[j + 1];
         ah[h] = pack2(x, y);
-        al[h] = pack2(x - lo_f(ah[h]), y - hi_f(ah[h]));
+        const float xr = x - lo_f(ah[h]), yr = y - hi_f(ah[h]);
+        al[h] = pack2(xr, yr);
+        ar[h] = pack2(xr - lo_f(al[h]), yr - hi_f(al[h]));
       }
 #pragma unroll
-      for (int i = 0; i < L::kCols / 16; ++i) {
+      for (int i = 0; i < kCols32 / 16; ++i) {
         uint32_t cf[4];
-        ldm4t(cf, s_u32(sc) + (k * 16 + t_row) * L::kPitch + (zc + i * 16 + t_col) * 2);
+        ldm4t(cf, s_u32(sc) + (k * 16 + t_row) * kPitch32 + (zc + i * 16 + t_col) * 2);
         mma16816(z[2 * i], ah, cf[0], cf[1]);
         mma16816(z[2 * i + 1], ah, cf[2], cf[3]);
         mma16816(z[2 * i], al, cf[0], cf[1]);
         mma16816(z[2 * i + 1], al, cf[2], cf[3]);
+        if (P.zn != nullptr) {
+          mma16816(z[2 * i], ar, cf[0], cf[1]);
+          mma16816(z[2 * i + 1], ar, cf[2], cf[3]);
+        }
       }
     }
   }
@@ -348,30 +335,18 @@ int la_segments(int T, int chunk, int seqs, int sms) {
   return want < most ? want : most;
 }
 
-template <int D>
-cudaError_t launch_passes(LaArgs& a, int sms, cudaStream_t s) {
-  using L = LaShape<D>;
-  const int seqs = a.B * a.heads;
-  int segs = la_segments(a.T, L::C, seqs * a.passes, sms);
-  const int chunks = (a.T + L::C - 1) / L::C;
-  a.seg_len = (chunks + segs - 1) / segs * L::C;
+cudaError_t launch_passes32(LaArgs& a, int sms, cudaStream_t s) {
+  const int seqs = a.B * a.heads, chunks = (a.T + kC32 - 1) / kC32;
+  const int segs = la_segments(a.T, kC32, seqs * a.passes, sms);
+  a.seg_len = (chunks + segs - 1) / segs * kC32;
   a.segs = (a.T + a.seg_len - 1) / a.seg_len;
-  const int threads = L::kWarps * 32;
   if (a.segs > 1) {
-    decay_pass_kernel<D, true><<<dim3(a.segs - 1, seqs, a.passes), threads, L::kSmem, s>>>(a);
+    decay_pass_kernel<true><<<dim3(a.segs - 1, seqs, a.passes), kWarps32 * 32, kSmem32, s>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  decay_pass_kernel<D, false><<<dim3(a.segs, seqs, a.passes), threads, L::kSmem, s>>>(a);
+  decay_pass_kernel<false><<<dim3(a.segs, seqs, a.passes), kWarps32 * 32, kSmem32, s>>>(a);
   return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t prepare_passes() {
-  cudaError_t e = cudaFuncSetAttribute(decay_pass_kernel<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LaShape<D>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(decay_pass_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)LaShape<D>::kSmem);
-  return e;
 }
 
 }  // namespace
@@ -384,6 +359,7 @@ struct srnl_lattn {
   int64_t ld = 0;
   float *log2g = nullptr, *g = nullptr;   // [heads]
   float* seg_state = nullptr;             // what the segments of long sequences add
+  int* dev_err = nullptr;
   char err[256] = "";
 };
 
@@ -403,7 +379,7 @@ srnl_status la_cuda_fail(srnl_lattn* h, cudaError_t e, const char* what) {
 }
 
 void la_free(srnl_lattn* h) {
-  void* ptrs[] = {h->log2g, h->g, h->seg_state};
+  void* ptrs[] = {h->log2g, h->g, h->seg_state, h->dev_err};
   for (void* p : ptrs)
     if (p != nullptr) cudaFree(p);
 }
@@ -454,12 +430,8 @@ srnl_status la_check(srnl_lattn* h, const Rows* in, int ni, const Rows* out, int
 
 cudaError_t la_run(srnl_lattn* h, srnl::LaArgs& a, cudaStream_t s) {
   a.B = h->cfg.B; a.T = h->cfg.T; a.heads = h->cfg.heads;
-  a.log2g = h->log2g; a.seg_state = h->seg_state;
-  switch (h->cfg.d) {
-    case 32: return srnl::launch_passes<32>(a, h->sms, s);
-    case 64: return srnl::launch_passes<64>(a, h->sms, s);
-    default: return srnl::launch_passes<128>(a, h->sms, s);
-  }
+  a.log2g = h->log2g; a.seg_state = h->seg_state; a.err = h->dev_err;
+  return h->cfg.d == 32 ? srnl::launch_passes32(a, h->sms, s) : srnl::launch_la_tc(a, h->cfg.d, h->sms, s);
 }
 
 }  // namespace
@@ -503,17 +475,19 @@ srnl_status srnl_lattn_create(srnl_lattn** out, const srnl_lattn_config* cfg, co
   delete[] host;
   if (e == cudaSuccess) {
     // the most any call splits: one pass (the forward) or three (the backward)
-    const int chunk = cfg->d == 128 ? 128 : 64;
     size_t most = 0;
     for (int passes = 1; passes <= 3; passes += 2) {
-      const int64_t seqs = (int64_t)cfg->B * cfg->heads;
-      const int segs = la_segments(cfg->T, chunk, (int)(seqs * passes), h->sms);
-      const size_t n = segs > 1 ? (size_t)passes * seqs * segs * cfg->d * cfg->d * sizeof(float) : 0;
+      const int groups = (D + 127) / 128;
+      const int segs = cfg->d == 32 ? la_segments(cfg->T, kC32, cfg->B * cfg->heads * passes, h->sms)
+                                    : la_tc_segments(cfg->T, cfg->B * groups * passes, h->sms);
+      const size_t n = segs > 1 ? (size_t)passes * cfg->B * cfg->heads * segs * cfg->d * cfg->d * sizeof(float) : 0;
       if (n > most) most = n;
     }
     if (most > 0) e = cudaMalloc(&h->seg_state, most);
   }
-  if (e == cudaSuccess) e = cfg->d == 32 ? prepare_passes<32>() : cfg->d == 64 ? prepare_passes<64>() : prepare_passes<128>();
+  if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
+  if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
+  if (e == cudaSuccess && cfg->d != 32) e = prepare_la_tc(cfg->d);
   if (e != cudaSuccess) {
     const srnl_status st = la_cuda_fail(nullptr, e, "linear attention create");
     la_free(h);
@@ -595,6 +569,14 @@ srnl_status srnl_lattn_step(srnl_lattn* h, const void* q, const void* k, const v
   else decay_step_kernel<128><<<grid, 256, 0, cs>>>(Q, K, V, O, state, h->g, c.heads, ld);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SRNL_OK : la_cuda_fail(h, e, "linear attention step launch");
+}
+
+srnl_status srnl_lattn_device_status(srnl_lattn* h) {
+  if (h == nullptr) return la_fail(nullptr, SRNL_E_INVAL, "handle is NULL");
+  int v = 0;
+  const cudaError_t e = cudaMemcpy(&v, h->dev_err, sizeof(int), cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return la_cuda_fail(h, e, "status read");
+  return v == 0 ? SRNL_OK : la_fail(h, static_cast<srnl_status>(v), "a bounded in-kernel wait gave up");
 }
 
 const char* srnl_lattn_last_error(const srnl_lattn* h) { return h != nullptr ? h->err : g_lattn_create_error; }

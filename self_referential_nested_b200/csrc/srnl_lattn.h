@@ -1,0 +1,36 @@
+// Interface between the linear attention entry points (srnl_lattn.cu) and the tensor-core
+// passes of 64- and 128-wide heads (srnl_lattn_tc.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace srnl {
+
+// A decayed pass over rows a, b, c of every token (see srnl_lattn.cu).
+struct LaPass {
+  const __nv_bfloat16 *a, *b, *c;
+  __nv_bfloat16* out;
+  int64_t lda, ldb, ldc, ldo;   // elements between tokens
+  const float* z0;              // [B][heads][D][D] or nullptr
+  float* zn;                    // final state or nullptr
+  int z0_t;                     // z0 is the transpose of Z
+  int reverse;                  // tokens from the last to the first; z0 enters undecayed, zn leaves decayed once more
+};
+
+struct LaArgs {
+  LaPass pass[3];
+  int passes, B, T, heads, segs, seg_len;   // segments of seg_len tokens per sequence
+  const float* log2g;                       // [heads]
+  const int* lengths;                       // [B] or nullptr
+  float* seg_state;                         // [pass][B][heads][segs][D][D]: what each segment adds, then its start
+  int* err;
+};
+
+// Segments per sequence that the tensor-core passes use: one when the sequences fill the GPU.
+int la_tc_segments(int T, int seqs, int sms);
+cudaError_t launch_la_tc(LaArgs& a, int d, int sms, cudaStream_t s);
+cudaError_t prepare_la_tc(int d);
+
+}  // namespace srnl

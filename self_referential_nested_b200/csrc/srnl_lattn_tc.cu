@@ -1,0 +1,699 @@
+// Tensor-core passes of linear attention for 64- and 128-wide heads (sm_100a).
+//
+// One CTA takes a 128-channel group (a 128-wide head, or two 64-wide ones) of a segment of a
+// sequence, in chunks of 128 tokens, with the formulas of srnl_lattn.cu:
+//   G  = a b^T                          tokens x tokens, per head          (1)
+//   O  = a Z                            tokens x channels                  (4)
+//   dZ = (w b)^T c                      channels of b x channels of c      (5)
+//   O <- g^(i + 1) O + (mask(G) g^(i - j)) c                               (3)
+//   Z <- g^C Z + dZ
+// All five are tcgen05 products with accumulators in TMEM.  a, b and c arrive by TMA as 64-channel
+// boxes, 128-byte rows, and serve as they lie, K-major where channels are summed over and
+// MN-major where tokens are.  The masked G goes back to TMEM over G's own columns as the left
+// operand of (3).  Roles: one thread loads, one issues products, four warps own a token's row
+// each (masking, O), four own a row of the state each, in fp32 registers (the decayed b, Z).
+// Z and w b are split into two bf16 parts (a third of w b where the state itself is asked for).
+//
+// Two 64-wide heads share a CTA so that every product has 128 rows; (5) computes the two
+// heads' cross terms with it and nobody reads them.
+//
+// What bounds it: the chain of a chunk (products, masking and the state's update wait for one
+// another, about 2 us) where few sequences run, memory where many do.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <cstring>
+
+#include "srnl_lattn.h"
+#include "srnl_scan.h"
+#include "srnl_tma.cuh"
+#include "srnl_umma.cuh"
+
+namespace srnl {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int kC = 128;                  // tokens per chunk, and channels per CTA
+constexpr uint32_t kBoxBytes = kC * 128; // 128 tokens x 64 channels
+constexpr uint32_t kTile = 2 * kBoxBytes;
+constexpr int kLaThreads = 384;          // load, product, 2 idle, 4 row and 4 state warps
+
+struct LaMaps {
+  CUtensorMap m[3][3];   // [pass][a, b, c]
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// D (+)= A B^T over K = 16 with A in TMEM (bf16 pairs, 8 columns).
+__device__ __forceinline__ void mma_k16_tmem_a(uint32_t d, uint32_t a, uint64_t bd, uint32_t idesc, bool accumulate) {
+  const uint32_t acc = accumulate ? 1u : 0u;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d),
+      "r"(a), "l"(bd), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]),
+      "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]),
+      "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]));
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// A warp's arrival: every lane's writes are done, one lane signals.
+__device__ __forceinline__ void warp_arrive(unsigned long long* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// Parts of w b for 128 tokens x 128 channels, from tile b into tiles p0, p1 (parts `first` and
+// first + 1; p1 may be skipped): x = b w, part 0 = bf16(x), part 1 = bf16(x - part 0), part 2 the
+// rest.  w: [head][token], zero where a token is none (its b is not read into the product then).
+// `threads` threads, t their index; two rows a warp pass, 16-byte units under the swizzle.
+template <int NH>
+__device__ __forceinline__ void form_parts(const unsigned char* b, unsigned char* p0, unsigned char* p1, unsigned char* p2,
+                                           const float* w, int t, int threads, int first) {
+  const int u = t & 15, box = u >> 3;
+  for (int r = t >> 4; r < kC; r += threads >> 4) {
+    const uint32_t off = (uint32_t)box * kBoxBytes + (uint32_t)r * 128 + (uint32_t)(((u & 7) ^ (r & 7)) << 4);
+    const uint4 raw = *reinterpret_cast<const uint4*>(b + off);
+    const float f = w[(NH == 2 ? box : 0) * kC + r];
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o0[4], o1[4], o2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x = f != 0.f ? bf16_lo(in[i]) * f : 0.f, y = f != 0.f ? bf16_hi(in[i]) * f : 0.f;
+      o0[i] = pack_bf16(x, y);
+      x -= bf16_lo(o0[i]);
+      y -= bf16_hi(o0[i]);
+      o1[i] = pack_bf16(x, y);
+      o2[i] = pack_bf16(x - bf16_lo(o1[i]), y - bf16_hi(o1[i]));
+    }
+    if (first == 0) {
+      *reinterpret_cast<uint4*>(p0 + off) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+      *reinterpret_cast<uint4*>(p1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    }
+    if (p2 != nullptr) *reinterpret_cast<uint4*>(p2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  }
+}
+
+// Rows of tile c from token `from` on become zero (tokens behind a sequence's last one hold
+// anything, and zero times NaN is NaN).
+__device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, int threads) {
+  for (int i = t; i < (kC - from) * 16; i += threads) {
+    const int r = from + (i >> 4), u = i & 15;
+    *reinterpret_cast<uint4*>(c + (u >> 3) * kBoxBytes + r * 128 + (u & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+}
+
+struct Chunk {
+  int cnt, lead, token0;   // tokens, the exponent z0 adds, token of the tile's row 0 (may be negative)
+};
+__device__ __forceinline__ Chunk chunk_of(int t0, int end, int n, int reverse) {
+  Chunk k;
+  k.cnt = min(kC, end - t0);
+  k.lead = reverse && t0 == 0 ? 0 : 1;
+  k.token0 = reverse ? n - t0 - kC : t0;
+  return k;
+}
+
+enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kZ, kDZ, kBars };
+
+template <int D>
+__global__ void __launch_bounds__(kLaThreads, 1)
+    decay_tc_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
+  constexpr int NH = kC / D;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  unsigned char *sa = sm, *sb = sa + kTile, *sc = sb + kTile, *p0 = sc + kTile, *p1 = p0 + kTile, *zh = p1 + kTile, *zl = zh + kTile;
+  float* pw = reinterpret_cast<float*>(zl + kTile);      // [NH][kC]: g^n
+  float* wt = pw + NH * kC;                              // [NH][kC]: weights of the chunk's rows of b
+  unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
+  int* failed = reinterpret_cast<int*>(tmem_slot + 1);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int which = blockIdx.z, seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
+  const int group = blockIdx.y % groups, batch = blockIdx.y / groups;
+  const LaPass& P = args.pass[which];
+  const int rev = P.reverse;
+  const bool exact = P.zn != nullptr;   // the state leaves: a third part of w b
+  if (smem_u32(sm) & 1023u) {           // the swizzled tiles' alignment
+    if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
+    return;
+  }
+
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    *failed = 0;
+    for (int i = 0; i < kBars; ++i) {
+      const int four = i == kRows || i == kOFree || i == kParts || i == kZ;
+      mbar_init(&bar[i], four ? 4 : i == kFreeB ? 5 : i == kFreeC ? 2 : 1);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int i = tid; i < NH * kC; i += kLaThreads) {
+    const int h = group * NH + i / kC;
+    pw[i] = h < args.heads ? exp2f(args.log2g[h] * (float)(i % kC)) : 0.f;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const uint32_t tmem = *tmem_slot, tG = tmem, tO = tmem + 256, tZ = tmem + 384;
+
+  int n = args.T;
+  if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
+  const int begin = seg * args.seg_len, end = min(begin + args.seg_len, n);
+  const int chunks = end > begin ? (end - begin + kC - 1) / kC : 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const int x = group * kC;
+      for (int k = 0; k < chunks; ++k) {
+        const Chunk c = chunk_of(begin + k * kC, end, n, rev);
+        const uint32_t ph = (k & 1) ^ 1;
+        // b is free first (its product and the forming of its parts), c last
+        unsigned char* dst[3] = {sb, sa, sc};
+        const int map[3] = {1, 0, 2}, full[3] = {kFullB, kFullA, kFullC}, free_[3] = {kFreeB, kFreeA, kFreeC};
+        for (int i = 0; i < 3; ++i) {
+          if (!mbar_pass(&bar[free_[i]], ph, failed)) break;
+          mbar_expect(&bar[full[i]], kTile);
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(smem_u32(dst[i]) + h * kBoxBytes, &maps.m[which][map[i]], x + 64 * h, c.token0, batch, &bar[full[i]]);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t iG = idesc_mn(128, 128, false, false);         // a b^T
+      constexpr uint32_t iO = idesc_mn(128, NH == 2 ? 64 : 128, false, true);   // a Z, P c
+      constexpr uint32_t iZ = idesc_mn(128, 128, true, true);           // (w b)^T c
+      const uint64_t da = desc_k_major(smem_u32(sa)), db = desc_k_major(smem_u32(sb)), dc = desc_mn_major(smem_u32(sc), kBoxBytes);
+      const uint64_t dzh = desc_mn_major(smem_u32(zh), kBoxBytes), dzl = desc_mn_major(smem_u32(zl), kBoxBytes);
+      const uint64_t dp0 = desc_mn_major(smem_u32(p0), kBoxBytes), dp1 = desc_mn_major(smem_u32(p1), kBoxBytes);
+      constexpr uint64_t kBox16 = kBoxBytes >> 4;
+      uint32_t parts = 0;
+      for (int k = 0; k < chunks; ++k) {
+        const uint32_t ph = k & 1;
+        // (1) G; its columns hold the previous chunk's left operand until (3) is done
+        if (k > 0) mbar_pass(&bar[kO], ph ^ 1, failed);
+        mbar_pass(&bar[kFullB], ph, failed);
+        mbar_pass(&bar[kFullA], ph, failed);
+        tmem_fence_after();
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {   // 16 channels a step, four to a box
+          const uint64_t at = (uint64_t)(s >> 2) * kBox16 + (uint64_t)(s & 3) * 2;
+          mma_k16_desc(tG + (NH == 2 ? (s >> 2) * 128 : 0), da + at, db + at, iG, NH == 2 ? (s & 3) > 0 : s > 0);
+        }
+        mma_commit(&bar[kG]);
+        mma_commit(&bar[kFreeB]);
+        // (4) O = a Z, once Z is written and the last O read
+        mbar_pass(&bar[kZ], ph, failed);
+        mbar_pass(&bar[kOFree], ph ^ 1, failed);
+        tmem_fence_after();
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int s = 0; s < 8; ++s) {
+            const int h = NH == 2 ? s >> 2 : 0;
+            const uint64_t az = (part == 0 ? dzh : dzl) + (uint64_t)s * 128 + (uint64_t)h * kBox16;   // 16 rows of Z
+            mma_k16_desc(tO + h * 64, da + (uint64_t)(s >> 2) * kBox16 + (uint64_t)(s & 3) * 2, az, iO,
+                         part > 0 || (NH == 2 ? (s & 3) > 0 : s > 0));
+          }
+        mma_commit(&bar[kO2]);
+        mma_commit(&bar[kFreeA]);
+        // (5) dZ from the parts of w b
+        mbar_pass(&bar[kFullC], ph, failed);
+        for (int round = 0; round < (exact ? 2 : 1); ++round, parts ^= 1) {
+          mbar_pass(&bar[kParts], parts, failed);
+          tmem_fence_after();
+#pragma unroll
+          for (int s = 0; s < 8; ++s) mma_k16_desc(tZ, dp0 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, round > 0 || s > 0);
+          if (round == 0)
+#pragma unroll
+            for (int s = 0; s < 8; ++s) mma_k16_desc(tZ, dp1 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, true);
+          mma_commit(&bar[kDZ]);
+        }
+        mma_commit(&bar[kFreeC]);
+        // (3) O += P c
+        mbar_pass(&bar[kRows], ph, failed);
+        tmem_fence_after();
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int s = 0; s < 8; ++s)
+            mma_k16_tmem_a(tO + h * 64, tG + h * 128 + s * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
+        mma_commit(&bar[kO]);
+        mma_commit(&bar[kFreeC]);
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ---- token rows
+    const int q = warp & 3, r = 32 * q + lane;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const int ord = rev ? kC - 1 - r : r;   // the token's place in the chunk's order
+    for (int k = 0; k < chunks; ++k) {
+      const uint32_t ph = k & 1;
+      const Chunk c = chunk_of(begin + k * kC, end, n, rev);
+      mbar_pass(&bar[kG], ph, failed);
+      tmem_fence_after();
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+#pragma unroll 1
+        for (int jb = 0; jb < 4; ++jb) {   // 32 columns; the result goes over columns already read
+          uint32_t w[16];
+          if (rev ? jb < q : jb > q) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = 0u;
+          } else {
+            float v[32];
+            tmem_ld32(v, tG + lanes + h * 128 + jb * 32);
+            // g^distance; the distance falls (rises, in reverse) along the columns
+            const float* p = pw + h * kC + (rev ? 0 : r - jb * 32);
+            const int d0 = rev ? jb * 32 - r : 0;
+            tmem_wait_ld();
+            if (jb == q) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const bool on = rev ? j >= lane : j <= lane;
+                v[j] = on ? v[j] * (rev ? p[j - lane] : p[-j]) : 0.f;
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= rev ? p[d0 + j] : p[-j];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+          }
+          tmem_st16(tG + lanes + h * 128 + jb * 16, w);
+        }
+      }
+      // the state's share of O, decayed to the row
+      float f[NH];
+#pragma unroll
+      for (int h = 0; h < NH; ++h) f[h] = ord + c.lead < kC ? pw[h * kC + ord + c.lead] : pw[h * kC + kC - 1] * pw[h * kC + 1];
+      mbar_pass(&bar[kO2], ph, failed);
+      tmem_fence_after();
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        float v[32];
+        tmem_ld32(v, tO + lanes + cb * 32);
+        tmem_wait_ld();
+        const float s = f[NH == 2 ? cb >> 1 : 0];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= s;
+        tmem_st32(tO + lanes + cb * 32, v);
+      }
+      tmem_wait_st();
+      warp_arrive(&bar[kRows], lane);
+      mbar_pass(&bar[kO], ph, failed);
+      tmem_fence_after();
+      const int token = c.token0 + r;
+      bf16* dst = P.out + ((int64_t)batch * args.T + token) * P.ldo + (int64_t)group * kC;
+#pragma unroll 1
+      for (int cb = 0; cb < 4; ++cb) {
+        float v[32];
+        tmem_ld32(v, tO + lanes + cb * 32);
+        tmem_wait_ld();
+        if (cb == 3) warp_arrive(&bar[kOFree], lane);
+        if (ord < c.cnt && (NH == 1 || group * 2 + (cb >> 1) < args.heads)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) =
+                make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+        }
+      }
+    }
+  } else if (warp >= 8) {
+    // ---- rows of the state: channel r of the group's b, all of its head's c channels
+    const int q = warp & 3, t = tid - 256, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D;
+    const int head = group * NH + h;
+    const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const bool live = head < args.heads;
+    const float lg = live ? args.log2g[head] : 0.f;
+    float z[D];
+    {
+      const int64_t sq = (int64_t)batch * args.heads + head;
+      const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * D * D
+                                       : P.z0 != nullptr ? P.z0 + sq * D * D : nullptr;
+      const bool tr = args.segs == 1 && P.z0_t;
+#pragma unroll
+      for (int i = 0; i < D; i += 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && src != nullptr) {
+          if (tr) v = make_float4(src[i * D + br], src[(i + 1) * D + br], src[(i + 2) * D + br], src[(i + 3) * D + br]);
+          else v = *reinterpret_cast<const float4*>(src + br * D + i);
+        }
+        z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
+      }
+    }
+    // the row in two bf16 parts: row r of Z, its head's columns (two boxes of a 128-wide head)
+    auto put_z = [&]() {
+#pragma unroll
+      for (int u = 0; u < D / 8; ++u) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = z[8 * u + 2 * i], y = z[8 * u + 2 * i + 1];
+          hi[i] = pack_bf16(x, y);
+          lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+        }
+        const uint32_t off = (uint32_t)(NH == 2 ? h : u >> 3) * kBoxBytes + (uint32_t)r * 128 + (uint32_t)(((u & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(zh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(zl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_async();
+      warp_arrive(&bar[kZ], lane);
+    };
+    put_z();
+    uint32_t dz = 0;
+    for (int k = 0; k < chunks; ++k) {
+      const uint32_t ph = k & 1;
+      const Chunk c = chunk_of(begin + k * kC, end, n, rev);
+      // weights of this chunk's tokens, g^(tokens behind them); the four warps share them
+      for (int i = t; i < NH * kC; i += 128) {
+        const int row = i % kC, o = rev ? kC - 1 - row : row;
+        wt[i] = o < c.cnt ? pw[i - row + c.cnt - 1 - o] : 0.f;
+      }
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      mbar_pass(&bar[kFullB], ph, failed);
+      form_parts<NH>(sb, p0, p1, nullptr, wt, t, 128, 0);
+      if (!rev && c.cnt < kC) {
+        mbar_pass(&bar[kFullC], ph, failed);
+        clear_rows(sc, c.cnt, t, 128);
+      }
+      fence_async();
+      warp_arrive(&bar[kParts], lane);
+      if (exact) {   // the third part, over the first once its product is done
+        mbar_pass(&bar[kDZ], dz, failed);
+        dz ^= 1;
+        form_parts<NH>(sb, p0, p1, p0, wt, t, 128, 2);
+        fence_async();
+        warp_arrive(&bar[kParts], lane);
+      }
+      warp_arrive(&bar[kFreeB], lane);
+      // z <- g^m z + dZ; a factor near one is applied as z + (g^m - 1) z, whose error does not
+      // add up over thousands of chunks
+      const float e = lg * (float)(c.cnt - 1 + c.lead);
+      const bool near = e > -1.f;
+      const float fm = near ? expm1f(e * 0.69314718055994531f) : exp2f(e);
+      mbar_pass(&bar[kDZ], dz, failed);
+      dz ^= 1;
+      tmem_fence_after();
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
+        float v[32];
+        tmem_ld32(v, tZ + lanes + (NH == 2 ? h * 64 : 0) + cb * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float x = z[cb * 32 + j];
+          z[cb * 32 + j] = fmaf(x, fm, near ? x : 0.f) + v[j];
+        }
+      }
+      if (k + 1 < chunks) {
+        mbar_pass(&bar[kO2], ph, failed);   // (4) has read the old Z
+        put_z();
+      }
+      asm volatile("bar.sync 2, 128;" ::: "memory");   // the weights may change
+    }
+    // the segment that holds the last token (the first one of an empty sequence)
+    const int last = n > 0 ? (n - 1) / args.seg_len : 0;
+    if (P.zn != nullptr && seg == last && live) {
+      const float f = rev && n > 0 ? exp2f(lg) : 1.f;
+      float* dst = P.zn + ((int64_t)batch * args.heads + head) * D * D + (int64_t)br * D;
+#pragma unroll
+      for (int i = 0; i < D; i += 4)
+        *reinterpret_cast<float4*>(dst + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(failed)) {   // a wait gave up: report, and let the copies in flight land
+    if (tid == 0) atomicExch(args.err, SRNL_E_TIMEOUT);
+    const unsigned long long t0 = global_ns();
+    for (int i = 0; i < (1 << 20) && global_ns() - t0 < 1000000ull; ++i) {}
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
+  }
+}
+
+// ------------------------------------------------------------------ the segments' states
+// What a segment adds to the state, from zero: sum_j g^(tokens behind j) b_j c_j^T.  The weights
+// reach to the segment's end, so the products of all its chunks add up in TMEM.
+enum { sFull = 0, sFree = 2, sParts = 4, sDone = 5, sBars = 6 };
+
+template <int D>
+__global__ void __launch_bounds__(kLaThreads, 1)
+    decay_segment_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
+  constexpr int NH = kC / D;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  unsigned char *ring = sm, *p0 = sm + 4 * kTile, *p1 = p0 + kTile, *p2 = p1 + kTile;   // ring: two stages of b, c
+  float* wt = reinterpret_cast<float*>(p2 + kTile);   // [NH][kC]
+  unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + sBars);
+  int* failed = reinterpret_cast<int*>(tmem_slot + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int which = blockIdx.z, seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
+  const int group = blockIdx.y % groups, batch = blockIdx.y / groups;
+  const int rev = args.pass[which].reverse;
+  const bool exact = args.pass[which].zn != nullptr;
+  if (smem_u32(sm) & 1023u) {
+    if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
+    return;
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(128u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (tid == 0) {
+    *failed = 0;
+    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i == sParts ? 8 : i >= sFree && i < sParts ? 9 : 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const uint32_t tmem = *tmem_slot;
+  int n = args.T;
+  if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
+  const int begin = seg * args.seg_len, end = min(begin + args.seg_len, n);
+  const int chunks = end > begin ? (end - begin + kC - 1) / kC : 0;
+
+  if (warp == 0) {
+    if (lane == 0)
+      for (int k = 0; k < chunks; ++k) {
+        const Chunk c = chunk_of(begin + k * kC, end, n, rev);
+        const int s = k & 1;
+        if (!mbar_pass(&bar[sFree + s], ((k >> 1) & 1) ^ 1, failed)) break;
+        mbar_expect(&bar[sFull + s], 2 * kTile);
+        for (int i = 0; i < 2; ++i)
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(smem_u32(ring + (2 * s + i) * kTile) + h * kBoxBytes, &maps.m[which][1 + i], group * kC + 64 * h, c.token0,
+                        batch, &bar[sFull + s]);
+      }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
+      const uint64_t d0 = desc_mn_major(smem_u32(p0), kBoxBytes), d1 = desc_mn_major(smem_u32(p1), kBoxBytes),
+                     d2 = desc_mn_major(smem_u32(p2), kBoxBytes);
+      for (int k = 0; k < chunks; ++k) {
+        const uint64_t dc = desc_mn_major(smem_u32(ring + (2 * (k & 1) + 1) * kTile), kBoxBytes);
+        mbar_pass(&bar[sFull + (k & 1)], (k >> 1) & 1, failed);
+        if (!mbar_pass(&bar[sParts], k & 1, failed)) break;
+        tmem_fence_after();
+#pragma unroll
+        for (int s = 0; s < 8; ++s) mma_k16_desc(tmem, d0 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, k > 0 || s > 0);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) mma_k16_desc(tmem, d1 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, true);
+        if (exact)
+#pragma unroll
+          for (int s = 0; s < 8; ++s) mma_k16_desc(tmem, d2 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, true);
+        mma_commit(&bar[sDone]);
+        mma_commit(&bar[sFree + (k & 1)]);
+      }
+    }
+  } else if (warp >= 4) {
+    const int t = tid - 128;
+    for (int k = 0; k < chunks; ++k) {
+      const int s = k & 1, t0 = begin + k * kC;
+      const Chunk c = chunk_of(t0, end, n, rev);
+      for (int i = t; i < NH * kC; i += 256) {
+        const int row = i % kC, o = rev ? kC - 1 - row : row, h = group * NH + i / kC;
+        wt[i] = o < c.cnt && h < args.heads ? exp2f(args.log2g[h] * (float)(end - 1 - (t0 + o))) : 0.f;
+      }
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      mbar_pass(&bar[sFull + s], (k >> 1) & 1, failed);
+      if (k > 0) mbar_pass(&bar[sDone], (k - 1) & 1, failed);   // the parts' last products are done
+      unsigned char *b = ring + 2 * s * kTile, *cc = b + kTile;
+      form_parts<NH>(b, p0, p1, exact ? p2 : nullptr, wt, t, 256, 0);
+      if (!rev && c.cnt < kC) clear_rows(cc, c.cnt, t, 256);
+      fence_async();
+      warp_arrive(&bar[sParts], lane);
+      if (lane == 0) mbar_arrive(&bar[sFree + s]);
+      asm volatile("bar.sync 2, 256;" ::: "memory");   // the weights may change
+    }
+    if (warp < 8) {
+      const int q = warp & 3, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, head = group * NH + h;
+      if (chunks > 0) mbar_pass(&bar[sDone], (chunks - 1) & 1, failed);
+      tmem_fence_after();
+      float* dst = args.seg_state +
+                   ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * D * D + (int64_t)(r % D) * D;
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
+        float v[32];
+        if (chunks > 0) {
+          tmem_ld32(v, tmem + ((uint32_t)(32 * q) << 16) + (NH == 2 ? h * 64 : 0) + cb * 32);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0.f;
+        }
+        if (head < args.heads)
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(dst + cb * 32 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(failed)) {
+    if (tid == 0) atomicExch(args.err, SRNL_E_TIMEOUT);
+    const unsigned long long t0 = global_ns();
+    for (int i = 0; i < (1 << 20) && global_ns() - t0 < 1000000ull; ++i) {}
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(128u));
+  }
+}
+
+// What each segment adds -> the state each segment starts from, in place; z0 is the first one's.
+__global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant__ LaArgs args, int D) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int i = blockIdx.x * 256 + threadIdx.x, which = blockIdx.z, head = blockIdx.y % args.heads, batch = blockIdx.y / args.heads;
+  if (i >= D * D) return;
+  const LaPass& P = args.pass[which];
+  const int64_t sq = (int64_t)batch * args.heads + head;
+  int n = args.T;
+  if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
+  float cur = P.z0 != nullptr ? P.z0[sq * D * D + (P.z0_t ? (i % D) * D + i / D : i)] : 0.f;
+  float* at = args.seg_state + ((int64_t)which * args.B * args.heads + sq) * args.segs * D * D + i;
+  const float lg = args.log2g[head];
+  for (int s = 0; s < args.segs; ++s, at += D * D) {
+    const int len = min(max(n - s * args.seg_len, 0), args.seg_len);
+    const float add = s + 1 < args.segs ? *at : 0.f;
+    *at = cur;
+    // z0 of a reversed pass meets its first token undecayed
+    if (len > 0) cur = fmaf(exp2f(lg * (float)(P.reverse && s == 0 ? len - 1 : len)), cur, add);
+  }
+}
+
+constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + 2 * (size_t)(kC / d) * kC * 4 + kBars * 8 + 16; }
+
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3((unsigned)threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &at;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...);
+}
+
+template <int D>
+cudaError_t launch_tc(LaArgs& a, const LaMaps& m, cudaStream_t s) {
+  const int groups = (a.heads * D + kC - 1) / kC;
+  if (a.segs > 1) {
+    cudaError_t e = launch_next(decay_segment_kernel<D>, dim3(a.segs - 1, a.B * groups, a.passes), kLaThreads, la_smem(D), s, m, a);
+    if (e == cudaSuccess)
+      e = launch_next(decay_start_kernel, dim3((D * D + 255) / 256, a.B * a.heads, a.passes), 256, 0, s, a, D);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_next(decay_tc_kernel<D>, dim3(a.segs, a.B * groups, a.passes), kLaThreads, la_smem(D), s, m, a);
+}
+
+}  // namespace
+
+int la_tc_segments(int T, int seqs, int sms) {
+  const int chunks = (T + kC - 1) / kC, want = sms / seqs;
+  const int most = chunks / 2 > 1 ? chunks / 2 : 1;
+  return want < 1 ? 1 : want < most ? want : most;
+}
+
+cudaError_t launch_la_tc(LaArgs& a, int d, int sms, cudaStream_t s) {
+  const int groups = (a.heads * d + kC - 1) / kC, chunks = (a.T + kC - 1) / kC;
+  const int want = la_tc_segments(a.T, a.B * groups * a.passes, sms);
+  a.seg_len = (chunks + want - 1) / want * kC;
+  a.segs = (a.T + a.seg_len - 1) / a.seg_len;
+  const TensorMapEncoder enc = ffn_tensor_map_encoder();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  LaMaps m;
+  memset(&m, 0, sizeof m);
+  for (int i = 0; i < a.passes; ++i) {
+    const LaPass& p = a.pass[i];
+    const bf16* base[3] = {p.a, p.b, p.c};
+    const int64_t ld[3] = {p.lda, p.ldb, p.ldc};
+    for (int j = 0; j < 3; ++j) {
+      const cuuint64_t dim[3] = {(cuuint64_t)a.heads * d, (cuuint64_t)a.T, (cuuint64_t)a.B};
+      const cuuint64_t str[2] = {(cuuint64_t)ld[j] * 2, a.B > 1 ? (cuuint64_t)ld[j] * 2 * a.T : (cuuint64_t)ld[j] * 2};
+      const cuuint32_t box[3] = {64u, (cuuint32_t)kC, 1u}, est[3] = {1u, 1u, 1u};
+      if (enc(&m.m[i][j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(base[j]), dim, str, box, est,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    }
+  }
+  return d == 64 ? launch_tc<64>(a, m, s) : launch_tc<128>(a, m, s);
+}
+
+cudaError_t prepare_la_tc(int d) {
+  const int n = (int)la_smem(d);
+  if (d == 64) {
+    cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+    return e == cudaSuccess ? cudaFuncSetAttribute(decay_segment_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, n) : e;
+  }
+  cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
+  return e == cudaSuccess ? cudaFuncSetAttribute(decay_segment_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, n) : e;
+}
+
+}  // namespace srnl

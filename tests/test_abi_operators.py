@@ -98,4 +98,5 @@ def test_lattn_null_arguments_fail_cleanly(lib):
     assert lib.srnl_lattn_forward(*[None] * 9) == S.SRNL_E_INVAL
     assert lib.srnl_lattn_backward(*[None] * 13) == S.SRNL_E_INVAL
     assert lib.srnl_lattn_step(*[None] * 7) == S.SRNL_E_INVAL
+    assert lib.srnl_lattn_device_status(None) == S.SRNL_E_INVAL
     lib.srnl_lattn_destroy(None)

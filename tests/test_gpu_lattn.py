@@ -125,6 +125,7 @@ def test_forward_and_backward(B, T, H, d, lens, packed, state):
                               state_in=t["s0"] if state else None, dstate_out=t["ds"] if state else None,
                               dstate_in=dsi if state else None)
         torch.cuda.synchronize()
+        S.srnl_lattn_device_status(h)
     finally:
         h.close()
     ln = lens or [T] * B
