@@ -10,8 +10,9 @@
 // All five are tcgen05 products with accumulators in TMEM.  a, b and c arrive by TMA as 64-channel
 // boxes, 128-byte rows, and serve as they lie, K-major where channels are summed over and
 // MN-major where tokens are.  The masked G goes back to TMEM over G's own columns as the left
-// operand of (3).  Roles: one thread loads, one issues products, four warps own a token's row
-// each (masking, O), four own a row of the state each, in fp32 registers (the decayed b, Z).
+// operand of (3).  Roles: one thread loads, two issue products (those of the rows, and (5), whose
+// chain of decayed b, dZ and Z goes on beside them), four warps own a token's row per thread
+// (masking, O), eight half a row of the state per thread, in fp32 registers (the decayed b, Z).
 // Z and w b are split into two bf16 parts (a third of w b where the state itself is asked for).
 //
 // Two 64-wide heads share a CTA so that every product has 128 rows; (5) computes the two
@@ -39,7 +40,9 @@ using bf16 = __nv_bfloat16;
 constexpr int kC = 128;                  // tokens per chunk, and channels per CTA
 constexpr uint32_t kBoxBytes = kC * 128; // 128 tokens x 64 channels
 constexpr uint32_t kTile = 2 * kBoxBytes;
-constexpr int kLaThreads = 384;          // load, product, 2 idle, 4 row and 4 state warps
+constexpr int kLaThreads = 512;          // load, two of products, 1 idle, 4 row and 8 state warps
+constexpr int kStateThreads = 256;
+constexpr uint32_t kHalfBytes = kTile / 2;   // 64 tokens of a part of w b: two boxes of 64 x 64
 
 struct LaMaps {
   CUtensorMap m[3][3];   // [pass][a, b, c]
@@ -89,34 +92,48 @@ __device__ __forceinline__ void warp_arrive(unsigned long long* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Parts of w b for 128 tokens x 128 channels, from tile b into tiles p0, p1 (parts `first` and
-// first + 1; p1 may be skipped): x = b w, part 0 = bf16(x), part 1 = bf16(x - part 0), part 2 the
-// rest.  w: [head][token], zero where a token is none (its b is not read into the product then).
-// `threads` threads, t their index; two rows a warp pass, 16-byte units under the swizzle.
+// Parts of w b for tokens 64 half .. + 63 of tile b, into that half of part tiles p0 and p1:
+// x = w b, part 0 = bf16(x), part 1 = bf16(x - part 0); the rest, as bf16, stays in `rest`.
+// A thread takes 4 16-byte units; f: its rows' weights.  A row without weight (no token of
+// this sequence: it may hold anything) becomes zero.
 template <int NH>
-__device__ __forceinline__ void form_parts(const unsigned char* b, unsigned char* p0, unsigned char* p1, unsigned char* p2,
-                                           const float* w, int t, int threads, int first) {
+__device__ __forceinline__ void form_half(const unsigned char* b, unsigned char* p0, unsigned char* p1, const float* w, float scale0,
+                                          float scale1, int t, int half, bool third, uint4 (&rest)[4]) {
   const int u = t & 15, box = u >> 3;
-  for (int r = t >> 4; r < kC; r += threads >> 4) {
-    const uint32_t off = (uint32_t)box * kBoxBytes + (uint32_t)r * 128 + (uint32_t)(((u & 7) ^ (r & 7)) << 4);
-    const uint4 raw = *reinterpret_cast<const uint4*>(b + off);
-    const float f = w[(NH == 2 ? box : 0) * kC + r];
-    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t o0[4], o1[4], o2[4];
+  const float* wr = w + (NH == 2 ? box : 0) * kC + 64 * half;
+  const float scale = NH == 2 && box ? scale1 : scale0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x = f != 0.f ? bf16_lo(in[i]) * f : 0.f, y = f != 0.f ? bf16_hi(in[i]) * f : 0.f;
-      o0[i] = pack_bf16(x, y);
-      x -= bf16_lo(o0[i]);
-      y -= bf16_hi(o0[i]);
-      o1[i] = pack_bf16(x, y);
-      o2[i] = pack_bf16(x - bf16_lo(o1[i]), y - bf16_hi(o1[i]));
+  for (int i = 0; i < 4; ++i) {
+    const int r = (t >> 4) + 16 * i;
+    const uint32_t sw = (uint32_t)(((u & 7) ^ (r & 7)) << 4);
+    const uint4 raw = *reinterpret_cast<const uint4*>(b + box * kBoxBytes + (64 * half + r) * 128 + sw);
+    const float f = wr[r] * scale;
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o0[4] = {0u, 0u, 0u, 0u}, o1[4] = {0u, 0u, 0u, 0u}, o2[4] = {0u, 0u, 0u, 0u};
+    if (f != 0.f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 x = __fmul2_rn(make_float2(bf16_lo(in[k]), bf16_hi(in[k])), make_float2(f, f));
+        o0[k] = pack_bf16(x.x, x.y);
+        x = __fadd2_rn(x, make_float2(-bf16_lo(o0[k]), -bf16_hi(o0[k])));
+        o1[k] = pack_bf16(x.x, x.y);
+        if (third) o2[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
+      }
     }
-    if (first == 0) {
-      *reinterpret_cast<uint4*>(p0 + off) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-      *reinterpret_cast<uint4*>(p1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    }
-    if (p2 != nullptr) *reinterpret_cast<uint4*>(p2 + off) = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    const uint32_t off = (uint32_t)half * kHalfBytes + (uint32_t)box * (kBoxBytes / 2) + (uint32_t)r * 128 + sw;
+    *reinterpret_cast<uint4*>(p0 + off) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    *reinterpret_cast<uint4*>(p1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  }
+}
+// The rest of a half into part tile p.
+__device__ __forceinline__ void put_rest(unsigned char* p, int t, int half, const uint4 (&rest)[4]) {
+  const int u = t & 15;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = (t >> 4) + 16 * i;
+    *reinterpret_cast<uint4*>(p + (uint32_t)half * kHalfBytes + (uint32_t)(u >> 3) * (kBoxBytes / 2) + (uint32_t)r * 128 +
+                              (uint32_t)(((u & 7) ^ (r & 7)) << 4)) = rest[i];
   }
 }
 
@@ -140,7 +157,7 @@ __device__ __forceinline__ Chunk chunk_of(int t0, int end, int n, int reverse) {
   return k;
 }
 
-enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kZ, kDZ, kBars };
+enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kZ = kParts + 3, kDZ, kClear, kBars };   // kParts: halves 0 and 1, and the rest
 
 template <int D>
 __global__ void __launch_bounds__(kLaThreads, 1)
@@ -172,14 +189,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   if (tid == 0) {
     *failed = 0;
     for (int i = 0; i < kBars; ++i) {
-      const int four = i == kRows || i == kOFree || i == kParts || i == kZ;
-      mbar_init(&bar[i], four ? 4 : i == kFreeB ? 5 : i == kFreeC ? 2 : 1);
+      mbar_init(&bar[i], i == kRows || i == kOFree ? 4 : (i >= kParts && i < kParts + 3) || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : i == kFreeC ? 2 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = tid; i < NH * kC; i += kLaThreads) {
-    const int h = group * NH + i / kC;
-    pw[i] = h < args.heads ? exp2f(args.log2g[h] * (float)(i % kC)) : 0.f;
+    const int h = group * NH + i / kC, m = i % kC;
+    pw[i] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
+    wt[i - m + (rev ? m : kC - 1 - m)] = pw[i];   // of a whole chunk; m tokens behind the row's
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -212,14 +229,11 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t iG = idesc_mn(128, 128, false, false);         // a b^T
+      constexpr uint32_t iG = idesc_mn(128, 128, false, false);                 // a b^T
       constexpr uint32_t iO = idesc_mn(128, NH == 2 ? 64 : 128, false, true);   // a Z, P c
-      constexpr uint32_t iZ = idesc_mn(128, 128, true, true);           // (w b)^T c
       const uint64_t da = desc_k_major(smem_u32(sa)), db = desc_k_major(smem_u32(sb)), dc = desc_mn_major(smem_u32(sc), kBoxBytes);
       const uint64_t dzh = desc_mn_major(smem_u32(zh), kBoxBytes), dzl = desc_mn_major(smem_u32(zl), kBoxBytes);
-      const uint64_t dp0 = desc_mn_major(smem_u32(p0), kBoxBytes), dp1 = desc_mn_major(smem_u32(p1), kBoxBytes);
       constexpr uint64_t kBox16 = kBoxBytes >> 4;
-      uint32_t parts = 0;
       for (int k = 0; k < chunks; ++k) {
         const uint32_t ph = k & 1;
         // (1) G; its columns hold the previous chunk's left operand until (3) is done
@@ -249,21 +263,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           }
         mma_commit(&bar[kO2]);
         mma_commit(&bar[kFreeA]);
-        // (5) dZ from the parts of w b
-        mbar_pass(&bar[kFullC], ph, failed);
-        for (int round = 0; round < (exact ? 2 : 1); ++round, parts ^= 1) {
-          mbar_pass(&bar[kParts], parts, failed);
-          tmem_fence_after();
-#pragma unroll
-          for (int s = 0; s < 8; ++s) mma_k16_desc(tZ, dp0 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, round > 0 || s > 0);
-          if (round == 0)
-#pragma unroll
-            for (int s = 0; s < 8; ++s) mma_k16_desc(tZ, dp1 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, true);
-          mma_commit(&bar[kDZ]);
-        }
-        mma_commit(&bar[kFreeC]);
         // (3) O += P c
         mbar_pass(&bar[kRows], ph, failed);
+        mbar_pass(&bar[kFullC], ph, failed);
+        if (!rev && k == chunks - 1 && (end - begin) % kC != 0) mbar_pass(&bar[kClear], 0, failed);   // c's spare rows are zeros
         tmem_fence_after();
 #pragma unroll
         for (int h = 0; h < NH; ++h)
@@ -271,6 +274,34 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           for (int s = 0; s < 8; ++s)
             mma_k16_tmem_a(tO + h * 64, tG + h * 128 + s * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
         mma_commit(&bar[kO]);
+        mma_commit(&bar[kFreeC]);
+      }
+    }
+  } else if (warp == 2) {
+    if (lane == 0) {
+      // (5) dZ from the parts of w b, half a chunk at a time, then from the rest of both
+      constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
+      const uint64_t dc = desc_mn_major(smem_u32(sc), kBoxBytes);
+      const uint64_t dp0 = desc_mn_major(smem_u32(p0), kBoxBytes / 2), dp1 = desc_mn_major(smem_u32(p1), kBoxBytes / 2);
+      for (int k = 0; k < chunks; ++k) {
+        mbar_pass(&bar[kFullC], k & 1, failed);
+        for (int half = 0; half < (exact ? 3 : 2); ++half) {
+          mbar_pass(&bar[kParts + half], k & 1, failed);
+          tmem_fence_after();
+          if (half < 2) {
+#pragma unroll
+            for (int part = 0; part < 2; ++part)
+#pragma unroll
+              for (int s = 0; s < 4; ++s)
+                mma_k16_desc(tZ, (part == 0 ? dp0 : dp1) + (uint64_t)half * (kHalfBytes >> 4) + (uint64_t)s * 128,
+                             dc + (uint64_t)(half * 4 + s) * 128, iZ, half > 0 || part > 0 || s > 0);
+          } else {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              mma_k16_desc(tZ, dp0 + (uint64_t)(s >> 2) * (kHalfBytes >> 4) + (uint64_t)(s & 3) * 128, dc + (uint64_t)s * 128, iZ, true);
+          }
+          if (half > 0) mma_commit(&bar[kDZ]);
+        }
         mma_commit(&bar[kFreeC]);
       }
     }
@@ -353,32 +384,35 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
     }
   } else if (warp >= 8) {
-    // ---- rows of the state: channel r of the group's b, all of its head's c channels
-    const int q = warp & 3, t = tid - 256, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D;
+    // ---- rows of the state: channel r of the group's b, half of its head's c channels
+    constexpr int Z = D / 2;
+    const int q = warp & 3, t = tid - 256, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D, hf = (warp - 8) >> 2;
     const int head = group * NH + h;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const bool live = head < args.heads;
     const float lg = live ? args.log2g[head] : 0.f;
-    float z[D];
+    float z[Z];
     {
       const int64_t sq = (int64_t)batch * args.heads + head;
       const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * D * D
                                        : P.z0 != nullptr ? P.z0 + sq * D * D : nullptr;
       const bool tr = args.segs == 1 && P.z0_t;
 #pragma unroll
-      for (int i = 0; i < D; i += 4) {
+      for (int i = 0; i < Z; i += 4) {
+        const int c = hf * Z + i;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         if (live && src != nullptr) {
-          if (tr) v = make_float4(src[i * D + br], src[(i + 1) * D + br], src[(i + 2) * D + br], src[(i + 3) * D + br]);
-          else v = *reinterpret_cast<const float4*>(src + br * D + i);
+          if (tr) v = make_float4(src[c * D + br], src[(c + 1) * D + br], src[(c + 2) * D + br], src[(c + 3) * D + br]);
+          else v = *reinterpret_cast<const float4*>(src + br * D + c);
         }
         z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
       }
     }
-    // the row in two bf16 parts: row r of Z, its head's columns (two boxes of a 128-wide head)
+    // the half row in two bf16 parts: row r of Z, its head's columns (a box for each half of a
+    // 128-wide head)
     auto put_z = [&]() {
 #pragma unroll
-      for (int u = 0; u < D / 8; ++u) {
+      for (int u = 0; u < Z / 8; ++u) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -386,7 +420,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           hi[i] = pack_bf16(x, y);
           lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
         }
-        const uint32_t off = (uint32_t)(NH == 2 ? h : u >> 3) * kBoxBytes + (uint32_t)r * 128 + (uint32_t)(((u & 7) ^ (r & 7)) << 4);
+        const int box = NH == 2 ? h : hf, unit = NH == 2 ? hf * 4 + u : u;
+        const uint32_t off = (uint32_t)box * kBoxBytes + (uint32_t)r * 128 + (uint32_t)((unit ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(zh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(zl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
@@ -398,28 +433,37 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     for (int k = 0; k < chunks; ++k) {
       const uint32_t ph = k & 1;
       const Chunk c = chunk_of(begin + k * kC, end, n, rev);
-      // weights of this chunk's tokens, g^(tokens behind them); the four warps share them
-      for (int i = t; i < NH * kC; i += 128) {
-        const int row = i % kC, o = rev ? kC - 1 - row : row;
-        wt[i] = o < c.cnt ? pw[i - row + c.cnt - 1 - o] : 0.f;
+      if (c.cnt < kC) {   // the last chunk: its own weights, g^(tokens behind the row's)
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        for (int i = t; i < NH * kC; i += kStateThreads) {
+          const int row = i % kC, o = rev ? kC - 1 - row : row;
+          wt[i] = o < c.cnt ? pw[i - row + c.cnt - 1 - o] : 0.f;
+        }
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        if (!rev) {
+          mbar_pass(&bar[kFullC], ph, failed);
+          clear_rows(sc, c.cnt, t, kStateThreads);
+          fence_async();
+          warp_arrive(&bar[kClear], lane);
+        }
       }
-      asm volatile("bar.sync 2, 128;" ::: "memory");
       mbar_pass(&bar[kFullB], ph, failed);
-      form_parts<NH>(sb, p0, p1, nullptr, wt, t, 128, 0);
-      if (!rev && c.cnt < kC) {
-        mbar_pass(&bar[kFullC], ph, failed);
-        clear_rows(sc, c.cnt, t, 128);
-      }
+      uint4 rest[2][4];
+      form_half<NH>(sb, p0, p1, wt, 1.f, 1.f, t, 0, exact, rest[0]);
       fence_async();
       warp_arrive(&bar[kParts], lane);
-      if (exact) {   // the third part, over the first once its product is done
+      form_half<NH>(sb, p0, p1, wt, 1.f, 1.f, t, 1, exact, rest[1]);
+      fence_async();
+      warp_arrive(&bar[kParts + 1], lane);
+      warp_arrive(&bar[kFreeB], lane);
+      if (exact) {   // the rest, over the first parts once their products are done
         mbar_pass(&bar[kDZ], dz, failed);
         dz ^= 1;
-        form_parts<NH>(sb, p0, p1, p0, wt, t, 128, 2);
+        put_rest(p0, t, 0, rest[0]);
+        put_rest(p0, t, 1, rest[1]);
         fence_async();
-        warp_arrive(&bar[kParts], lane);
+        warp_arrive(&bar[kParts + 2], lane);
       }
-      warp_arrive(&bar[kFreeB], lane);
       // z <- g^m z + dZ; a factor near one is applied as z + (g^m - 1) z, whose error does not
       // add up over thousands of chunks
       const float e = lg * (float)(c.cnt - 1 + c.lead);
@@ -429,9 +473,9 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       dz ^= 1;
       tmem_fence_after();
 #pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
+      for (int cb = 0; cb < Z / 32; ++cb) {
         float v[32];
-        tmem_ld32(v, tZ + lanes + (NH == 2 ? h * 64 : 0) + cb * 32);
+        tmem_ld32(v, tZ + lanes + (NH == 2 ? h * 64 : 0) + hf * Z + cb * 32);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
@@ -443,15 +487,14 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         mbar_pass(&bar[kO2], ph, failed);   // (4) has read the old Z
         put_z();
       }
-      asm volatile("bar.sync 2, 128;" ::: "memory");   // the weights may change
     }
     // the segment that holds the last token (the first one of an empty sequence)
     const int last = n > 0 ? (n - 1) / args.seg_len : 0;
     if (P.zn != nullptr && seg == last && live) {
       const float f = rev && n > 0 ? exp2f(lg) : 1.f;
-      float* dst = P.zn + ((int64_t)batch * args.heads + head) * D * D + (int64_t)br * D;
+      float* dst = P.zn + ((int64_t)batch * args.heads + head) * D * D + (int64_t)br * D + hf * Z;
 #pragma unroll
-      for (int i = 0; i < D; i += 4)
+      for (int i = 0; i < Z; i += 4)
         *reinterpret_cast<float4*>(dst + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
     }
   }
@@ -471,7 +514,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 // ------------------------------------------------------------------ the segments' states
 // What a segment adds to the state, from zero: sum_j g^(tokens behind j) b_j c_j^T.  The weights
 // reach to the segment's end, so the products of all its chunks add up in TMEM.
-enum { sFull = 0, sFree = 2, sParts = 4, sDone = 5, sBars = 6 };
+enum { sFull = 0, sFree = 2, sParts = 4, sDone = 6, sBars = 8 };   // parts and done: one for each half
 
 template <int D>
 __global__ void __launch_bounds__(kLaThreads, 1)
@@ -498,8 +541,12 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   }
   if (tid == 0) {
     *failed = 0;
-    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i == sParts ? 8 : i >= sFree && i < sParts ? 9 : 1);
+    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i >= sParts && i < sDone ? 12 : i >= sFree && i < sParts ? 13 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  for (int i = tid; i < NH * kC; i += kLaThreads) {   // weights of a whole chunk
+    const int h = group * NH + i / kC, m = i % kC;
+    wt[i - m + (rev ? m : kC - 1 - m)] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -527,47 +574,63 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
-      const uint64_t d0 = desc_mn_major(smem_u32(p0), kBoxBytes), d1 = desc_mn_major(smem_u32(p1), kBoxBytes),
-                     d2 = desc_mn_major(smem_u32(p2), kBoxBytes);
+      const uint64_t d0 = desc_mn_major(smem_u32(p0), kBoxBytes / 2);
       for (int k = 0; k < chunks; ++k) {
         const uint64_t dc = desc_mn_major(smem_u32(ring + (2 * (k & 1) + 1) * kTile), kBoxBytes);
         mbar_pass(&bar[sFull + (k & 1)], (k >> 1) & 1, failed);
-        if (!mbar_pass(&bar[sParts], k & 1, failed)) break;
-        tmem_fence_after();
+        for (int half = 0; half < 2; ++half) {
+          mbar_pass(&bar[sParts + half], k & 1, failed);
+          tmem_fence_after();
+          for (int part = 0; part < (exact ? 3 : 2); ++part)
 #pragma unroll
-        for (int s = 0; s < 8; ++s) mma_k16_desc(tmem, d0 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, k > 0 || s > 0);
-#pragma unroll
-        for (int s = 0; s < 8; ++s) mma_k16_desc(tmem, d1 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, true);
-        if (exact)
-#pragma unroll
-          for (int s = 0; s < 8; ++s) mma_k16_desc(tmem, d2 + (uint64_t)s * 128, dc + (uint64_t)s * 128, iZ, true);
-        mma_commit(&bar[sDone]);
+            for (int s = 0; s < 4; ++s)
+              mma_k16_desc(tmem, d0 + (uint64_t)part * (kTile >> 4) + (uint64_t)half * (kHalfBytes >> 4) + (uint64_t)s * 128,
+                           dc + (uint64_t)(half * 4 + s) * 128, iZ, k > 0 || half > 0 || part > 0 || s > 0);
+          mma_commit(&bar[sDone + half]);
+        }
         mma_commit(&bar[sFree + (k & 1)]);
       }
     }
   } else if (warp >= 4) {
-    const int t = tid - 128;
+    // 12 warps: a half's rows go to the 256 threads of the last eight, half 0 and half 1 in turn
+    const int t = tid - 256;
+    const int h0 = group * NH;
+    const float lg0 = h0 < args.heads ? args.log2g[h0] : 0.f, lg1 = NH == 2 && h0 + 1 < args.heads ? args.log2g[h0 + 1] : 0.f;
     for (int k = 0; k < chunks; ++k) {
       const int s = k & 1, t0 = begin + k * kC;
       const Chunk c = chunk_of(t0, end, n, rev);
-      for (int i = t; i < NH * kC; i += 256) {
-        const int row = i % kC, o = rev ? kC - 1 - row : row, h = group * NH + i / kC;
-        wt[i] = o < c.cnt && h < args.heads ? exp2f(args.log2g[h] * (float)(end - 1 - (t0 + o))) : 0.f;
-      }
-      asm volatile("bar.sync 2, 256;" ::: "memory");
-      mbar_pass(&bar[sFull + s], (k >> 1) & 1, failed);
-      if (k > 0) mbar_pass(&bar[sDone], (k - 1) & 1, failed);   // the parts' last products are done
       unsigned char *b = ring + 2 * s * kTile, *cc = b + kTile;
-      form_parts<NH>(b, p0, p1, exact ? p2 : nullptr, wt, t, 256, 0);
-      if (!rev && c.cnt < kC) clear_rows(cc, c.cnt, t, 256);
-      fence_async();
-      warp_arrive(&bar[sParts], lane);
-      if (lane == 0) mbar_arrive(&bar[sFree + s]);
-      asm volatile("bar.sync 2, 256;" ::: "memory");   // the weights may change
+      float f0 = 1.f, f1 = 1.f;
+      if (c.cnt < kC) {
+        asm volatile("bar.sync 2, 384;" ::: "memory");
+        for (int i = tid - 128; i < NH * kC; i += 384) {
+          const int row = i % kC, o = rev ? kC - 1 - row : row;
+          const float lg = i >= kC ? lg1 : lg0;
+          wt[i] = o < c.cnt && h0 + i / kC < args.heads ? exp2f(lg * (float)(c.cnt - 1 - o)) : 0.f;
+        }
+        asm volatile("bar.sync 2, 384;" ::: "memory");
+      } else {   // a whole chunk's weights, decayed over the tokens behind it
+        f0 = exp2f(lg0 * (float)(end - t0 - kC));
+        f1 = exp2f(lg1 * (float)(end - t0 - kC));
+      }
+      mbar_pass(&bar[sFull + s], (k >> 1) & 1, failed);
+      for (int half = 0; half < 2; ++half) {
+        if (k > 0) mbar_pass(&bar[sDone + half], (k - 1) & 1, failed);   // the half's last products are done
+        if (warp >= 8) {
+          uint4 rest[4];
+          form_half<NH>(b, p0, p1, wt, f0, f1, t, half, exact, rest);
+          if (exact) put_rest(p2, t, half, rest);
+        } else if (half == 0 && !rev && c.cnt < kC) {
+          clear_rows(cc, c.cnt, tid - 128, 128);
+        }
+        fence_async();
+        warp_arrive(&bar[sParts + half], lane);
+      }
+      warp_arrive(&bar[sFree + s], lane);
     }
     if (warp < 8) {
       const int q = warp & 3, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, head = group * NH + h;
-      if (chunks > 0) mbar_pass(&bar[sDone], (chunks - 1) & 1, failed);
+      if (chunks > 0) mbar_pass(&bar[sDone + 1], (chunks - 1) & 1, failed);
       tmem_fence_after();
       float* dst = args.seg_state +
                    ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * D * D + (int64_t)(r % D) * D;
@@ -614,12 +677,20 @@ __global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant_
   float cur = P.z0 != nullptr ? P.z0[sq * D * D + (P.z0_t ? (i % D) * D + i / D : i)] : 0.f;
   float* at = args.seg_state + ((int64_t)which * args.B * args.heads + sq) * args.segs * D * D + i;
   const float lg = args.log2g[head];
-  for (int s = 0; s < args.segs; ++s, at += D * D) {
-    const int len = min(max(n - s * args.seg_len, 0), args.seg_len);
-    const float add = s + 1 < args.segs ? *at : 0.f;
-    *at = cur;
-    // z0 of a reversed pass meets its first token undecayed
-    if (len > 0) cur = fmaf(exp2f(lg * (float)(P.reverse && s == 0 ? len - 1 : len)), cur, add);
+  constexpr int kAhead = 8;   // loads in flight
+  for (int s0 = 0; s0 < args.segs; s0 += kAhead) {
+    float add[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) add[j] = s0 + j + 1 < args.segs ? at[(int64_t)(s0 + j) * D * D] : 0.f;
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int s = s0 + j;
+      if (s >= args.segs) break;
+      const int len = min(max(n - s * args.seg_len, 0), args.seg_len);
+      at[(int64_t)s * D * D] = cur;
+      // z0 of a reversed pass meets its first token undecayed
+      if (len > 0) cur = fmaf(exp2f(lg * (float)(P.reverse && s == 0 ? len - 1 : len)), cur, add[j]);
+    }
   }
 }
 
