@@ -54,6 +54,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
+               "r"(y), "r"(z)
+               : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -146,6 +151,54 @@ __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, in
   }
 }
 
+// A warp's 32 rows of G, masked and decayed, over G's own columns as bf16 (column block jb's
+// result goes to columns already read).  The distance falls along a row's columns (rises, in
+// reverse).  Away from the diagonal the powers are one product after another from the nearest
+// token on, two columns an instruction; on it, where powers below zero would overflow, they are
+// read from the table.
+template <int NH, bool REV>
+__device__ __forceinline__ void mask_rows(uint32_t tG, const float* pw, int q, int lane) {
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    const float* p = pw + h * kC;
+    const float g1 = p[1];
+    const float2 g2 = make_float2(g1 * g1, g1 * g1);
+#pragma unroll 1
+    for (int jb = 0; jb < 4; ++jb) {
+      uint32_t w[16];
+      if (REV ? jb < q : jb > q) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = 0u;
+      } else {
+        float v[32];
+        tmem_ld32(v, tG + h * 128 + jb * 32);
+        if (jb == q) {
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            const float f = REV ? p[max(j - lane, 0)] : p[max(lane - j, 0)];
+            v[j] = (REV ? j >= lane : j <= lane) ? v[j] * f : 0.f;
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+        } else {
+          const float near = REV ? p[(jb - q) * 32 - lane] : p[(q - jb) * 32 + lane - 31];
+          float2 f = REV ? make_float2(near, near * g1) : make_float2(near * g1, near);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int i = REV ? k : 15 - k;
+            const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f);
+            w[i] = pack_bf16(x.x, x.y);
+            f = __fmul2_rn(f, g2);
+          }
+        }
+      }
+      tmem_st16(tG + h * 128 + jb * 16, w);
+    }
+  }
+}
+
 struct Chunk {
   int cnt, lead, token0;   // tokens, the exponent z0 adds, token of the tile's row 0 (may be negative)
 };
@@ -219,6 +272,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         // b is free first (its product and the forming of its parts), c last
         unsigned char* dst[3] = {sb, sa, sc};
         const int map[3] = {1, 0, 2}, full[3] = {kFullB, kFullA, kFullC}, free_[3] = {kFreeB, kFreeA, kFreeC};
+        if (k + 1 < chunks) {   // the next chunk into L2: its tiles have one buffer each and load late
+          const Chunk d = chunk_of(begin + (k + 1) * kC, end, n, rev);
+          for (int i = 0; i < 6; ++i) tma_prefetch_3d(&maps.m[which][map[i >> 1]], x + 64 * (i & 1), d.token0, batch);
+        }
         for (int i = 0; i < 3; ++i) {
           if (!mbar_pass(&bar[free_[i]], ph, failed)) break;
           mbar_expect(&bar[full[i]], kTile);
@@ -315,51 +372,26 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const Chunk c = chunk_of(begin + k * kC, end, n, rev);
       mbar_pass(&bar[kG], ph, failed);
       tmem_fence_after();
-#pragma unroll
-      for (int h = 0; h < NH; ++h) {
-#pragma unroll 1
-        for (int jb = 0; jb < 4; ++jb) {   // 32 columns; the result goes over columns already read
-          uint32_t w[16];
-          if (rev ? jb < q : jb > q) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = 0u;
-          } else {
-            float v[32];
-            tmem_ld32(v, tG + lanes + h * 128 + jb * 32);
-            // g^distance; the distance falls (rises, in reverse) along the columns
-            const float* p = pw + h * kC + (rev ? 0 : r - jb * 32);
-            const int d0 = rev ? jb * 32 - r : 0;
-            tmem_wait_ld();
-            if (jb == q) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const bool on = rev ? j >= lane : j <= lane;
-                v[j] = on ? v[j] * (rev ? p[j - lane] : p[-j]) : 0.f;
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= rev ? p[d0 + j] : p[-j];
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-          }
-          tmem_st16(tG + lanes + h * 128 + jb * 16, w);
-        }
-      }
+      if (rev) mask_rows<NH, true>(tG + lanes, pw, q, lane);
+      else mask_rows<NH, false>(tG + lanes, pw, q, lane);
       // the state's share of O, decayed to the row
       float f[NH];
 #pragma unroll
       for (int h = 0; h < NH; ++h) f[h] = ord + c.lead < kC ? pw[h * kC + ord + c.lead] : pw[h * kC + kC - 1] * pw[h * kC + 1];
       mbar_pass(&bar[kO2], ph, failed);
       tmem_fence_after();
-#pragma unroll 1
+#pragma unroll
       for (int cb = 0; cb < 4; ++cb) {
         float v[32];
         tmem_ld32(v, tO + lanes + cb * 32);
         tmem_wait_ld();
-        const float s = f[NH == 2 ? cb >> 1 : 0];
+        const float2 s = make_float2(f[NH == 2 ? cb >> 1 : 0], f[NH == 2 ? cb >> 1 : 0]);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] *= s;
+        for (int j = 0; j < 32; j += 2) {
+          const float2 x = __fmul2_rn(make_float2(v[j], v[j + 1]), s);
+          v[j] = x.x;
+          v[j + 1] = x.y;
+        }
         tmem_st32(tO + lanes + cb * 32, v);
       }
       tmem_wait_st();
@@ -368,7 +400,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       tmem_fence_after();
       const int token = c.token0 + r;
       bf16* dst = P.out + ((int64_t)batch * args.T + token) * P.ldo + (int64_t)group * kC;
-#pragma unroll 1
+#pragma unroll
       for (int cb = 0; cb < 4; ++cb) {
         float v[32];
         tmem_ld32(v, tO + lanes + cb * 32);
