@@ -45,8 +45,15 @@ constexpr int kStateThreads = 256;
 constexpr uint32_t kHalfBytes = kTile / 2;   // 64 tokens of a part of w b: two boxes of 64 x 64
 
 struct LaMaps {
-  CUtensorMap m[3][3];   // [pass][a, b, c]
+  CUtensorMap m[3][4];   // [pass][a, b, c, out]
 };
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
 
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, unsigned long long* bar) {
   asm volatile(
@@ -210,7 +217,16 @@ __device__ __forceinline__ Chunk chunk_of(int t0, int end, int n, int reverse) {
   return k;
 }
 
-enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kZ = kParts + 3, kDZ, kClear, kBars };   // kParts: halves 0 and 1, and the rest
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, int x, int token, int batch, unsigned long long* bar) {
+  mbar_expect(bar, kTile);
+  for (int h = 0; h < 2; ++h) tma_load_3d(smem_u32(dst) + h * kBoxBytes, map, x + 64 * h, token, batch, bar);
+}
+// A tile into L2: the tiles have one buffer each and are loaded late.
+__device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int x, int token, int batch) {
+  for (int h = 0; h < 2; ++h) tma_prefetch_3d(map, x + 64 * h, token, batch);
+}
+
+enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kZ = kParts + 3, kDZ, kClear, kOut, kBars };   // kParts: halves 0 and 1, and the rest
 
 template <int D>
 __global__ void __launch_bounds__(kLaThreads, 1)
@@ -242,7 +258,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   if (tid == 0) {
     *failed = 0;
     for (int i = 0; i < kBars; ++i) {
-      mbar_init(&bar[i], i == kRows || i == kOFree ? 4 : (i >= kParts && i < kParts + 3) || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : i == kFreeC ? 2 : 1);
+      mbar_init(&bar[i], i == kRows || i == kOFree || i == kOut ? 4 : (i >= kParts && i < kParts + 3) || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -267,22 +283,41 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     if (lane == 0) {
       const int x = group * kC;
       for (int k = 0; k < chunks; ++k) {
-        const Chunk c = chunk_of(begin + k * kC, end, n, rev);
-        const uint32_t ph = (k & 1) ^ 1;
-        // b is free first (its product and the forming of its parts), c last
-        unsigned char* dst[3] = {sb, sa, sc};
-        const int map[3] = {1, 0, 2}, full[3] = {kFullB, kFullA, kFullC}, free_[3] = {kFreeB, kFreeA, kFreeC};
-        if (k + 1 < chunks) {   // the next chunk into L2: its tiles have one buffer each and load late
-          const Chunk d = chunk_of(begin + (k + 1) * kC, end, n, rev);
-          for (int i = 0; i < 6; ++i) tma_prefetch_3d(&maps.m[which][map[i >> 1]], x + 64 * (i & 1), d.token0, batch);
+        if (k + 1 < chunks) prefetch_chunk(&maps.m[which][1], x, chunk_of(begin + (k + 1) * kC, end, n, rev).token0, batch);
+        if (!mbar_pass(&bar[kFreeB], (k & 1) ^ 1, failed)) break;
+        load_tile(sb, &maps.m[which][1], x, chunk_of(begin + k * kC, end, n, rev).token0, batch, &bar[kFullB]);
+      }
+    }
+  } else if (warp == 3) {
+    // a, and c, in whose tile a whole chunk's O leaves once its products are done
+    if (lane == 0) {
+      const int x = group * kC;
+      for (int k = 0; k <= chunks; ++k) {
+        const Chunk c = chunk_of(begin + k * kC, end, n, rev), d = chunk_of(begin + (k + 1) * kC, end, n, rev);
+        if (k < chunks) {
+          if (k + 1 < chunks) {
+            prefetch_chunk(&maps.m[which][0], x, d.token0, batch);
+            prefetch_chunk(&maps.m[which][2], x, d.token0, batch);
+          }
+          if (!mbar_pass(&bar[kFreeA], (k & 1) ^ 1, failed)) break;
+          load_tile(sa, &maps.m[which][0], x, c.token0, batch, &bar[kFullA]);
         }
-        for (int i = 0; i < 3; ++i) {
-          if (!mbar_pass(&bar[free_[i]], ph, failed)) break;
-          mbar_expect(&bar[full[i]], kTile);
-          for (int h = 0; h < 2; ++h)
-            tma_load_3d(smem_u32(dst[i]) + h * kBoxBytes, &maps.m[which][map[i]], x + 64 * h, c.token0, batch, &bar[full[i]]);
+        if (k > 0) {
+          const Chunk o = chunk_of(begin + (k - 1) * kC, end, n, rev);
+          if (!mbar_pass(&bar[kOut], (k - 1) & 1, failed)) break;
+          if (o.cnt == kC) {
+            for (int h = 0; h < 2; ++h)
+              if (x + 64 * h < args.heads * D) tma_store_3d(&maps.m[which][3], smem_u32(sc) + h * kBoxBytes, x + 64 * h, o.token0, batch);
+            bulk_commit();
+            bulk_wait_read<0>();
+          }
+        }
+        if (k < chunks) {
+          if (!mbar_pass(&bar[kFreeC], (k & 1) ^ 1, failed)) break;
+          load_tile(sc, &maps.m[which][2], x, c.token0, batch, &bar[kFullC]);
         }
       }
+      bulk_wait_all();
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -291,6 +326,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const uint64_t da = desc_k_major(smem_u32(sa)), db = desc_k_major(smem_u32(sb)), dc = desc_mn_major(smem_u32(sc), kBoxBytes);
       const uint64_t dzh = desc_mn_major(smem_u32(zh), kBoxBytes), dzl = desc_mn_major(smem_u32(zl), kBoxBytes);
       constexpr uint64_t kBox16 = kBoxBytes >> 4;
+#pragma unroll 1
       for (int k = 0; k < chunks; ++k) {
         const uint32_t ph = k & 1;
         // (1) G; its columns hold the previous chunk's left operand until (3) is done
@@ -331,7 +367,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           for (int s = 0; s < 8; ++s)
             mma_k16_tmem_a(tO + h * 64, tG + h * 128 + s * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
         mma_commit(&bar[kO]);
-        mma_commit(&bar[kFreeC]);
       }
     }
   } else if (warp == 2) {
@@ -367,6 +402,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int q = warp & 3, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const int ord = rev ? kC - 1 - r : r;   // the token's place in the chunk's order
+#pragma unroll 1
     for (int k = 0; k < chunks; ++k) {
       const uint32_t ph = k & 1;
       const Chunk c = chunk_of(begin + k * kC, end, n, rev);
@@ -375,17 +411,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       if (rev) mask_rows<NH, true>(tG + lanes, pw, q, lane);
       else mask_rows<NH, false>(tG + lanes, pw, q, lane);
       // the state's share of O, decayed to the row
-      float f[NH];
-#pragma unroll
-      for (int h = 0; h < NH; ++h) f[h] = ord + c.lead < kC ? pw[h * kC + ord + c.lead] : pw[h * kC + kC - 1] * pw[h * kC + 1];
       mbar_pass(&bar[kO2], ph, failed);
       tmem_fence_after();
-#pragma unroll
+#pragma unroll 2
       for (int cb = 0; cb < 4; ++cb) {
         float v[32];
         tmem_ld32(v, tO + lanes + cb * 32);
+        const float* p = pw + (NH == 2 ? cb >> 1 : 0) * kC;
+        const float f = ord + c.lead < kC ? p[ord + c.lead] : p[kC - 1] * p[1];
+        const float2 s = make_float2(f, f);
         tmem_wait_ld();
-        const float2 s = make_float2(f[NH == 2 ? cb >> 1 : 0], f[NH == 2 ? cb >> 1 : 0]);
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
           const float2 x = __fmul2_rn(make_float2(v[j], v[j + 1]), s);
@@ -396,72 +431,91 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       tmem_wait_st();
       warp_arrive(&bar[kRows], lane);
+      // O: a whole chunk's through c's tile (free once (3) and (5) are done), the last, shorter
+      // one's straight to its rows
       mbar_pass(&bar[kO], ph, failed);
+      if (c.cnt == kC) mbar_pass(&bar[kFreeC], ph, failed);
       tmem_fence_after();
       const int token = c.token0 + r;
       bf16* dst = P.out + ((int64_t)batch * args.T + token) * P.ldo + (int64_t)group * kC;
-#pragma unroll
+#pragma unroll 2
       for (int cb = 0; cb < 4; ++cb) {
         float v[32];
         tmem_ld32(v, tO + lanes + cb * 32);
         tmem_wait_ld();
-        if (cb == 3) warp_arrive(&bar[kOFree], lane);
-        if (ord < c.cnt && (NH == 1 || group * 2 + (cb >> 1) < args.heads)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) =
-                make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
-                           pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
+                                     pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+          if (c.cnt == kC)
+            *reinterpret_cast<uint4*>(sc + (cb >> 1) * kBoxBytes + r * 128 + ((((cb & 1) * 4 + j) ^ (r & 7)) << 4)) = w;
+          else if (ord < c.cnt && (NH == 1 || group * 2 + (cb >> 1) < args.heads))
+            *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) = w;
         }
       }
+      fence_async();
+      warp_arrive(&bar[kOFree], lane);
+      if (lane == 0) mbar_arrive(&bar[kOut]);
     }
   } else if (warp >= 8) {
-    // ---- rows of the state: channel r of the group's b, half of its head's c channels
-    constexpr int Z = D / 2;
+    // ---- rows of the state: channel r of the group's b, half of its head's c channels, fp32, in
+    // 32-column blocks: one in registers (64-wide heads) or two in TMEM, where G leaves room.  The
+    // sums are taken here, not in the products' accumulator: their rounding there is not to
+    // nearest and would add up over a long memory.
+    constexpr int Z = D / 2, kBlocks = Z / 32;
     const int q = warp & 3, t = tid - 256, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D, hf = (warp - 8) >> 2;
     const int head = group * NH + h;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
+    const uint32_t tS = tmem + 128 + lanes + hf * Z;                              // 128-wide heads: the state
+    const uint32_t tD = tZ + lanes + (NH == 2 ? h * 64 : 0) + hf * Z;             // dZ
     const bool live = head < args.heads;
     const float lg = live ? args.log2g[head] : 0.f;
-    float z[Z];
-    {
-      const int64_t sq = (int64_t)batch * args.heads + head;
-      const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * D * D
-                                       : P.z0 != nullptr ? P.z0 + sq * D * D : nullptr;
-      const bool tr = args.segs == 1 && P.z0_t;
-#pragma unroll
-      for (int i = 0; i < Z; i += 4) {
-        const int c = hf * Z + i;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (live && src != nullptr) {
-          if (tr) v = make_float4(src[c * D + br], src[(c + 1) * D + br], src[(c + 2) * D + br], src[(c + 3) * D + br]);
-          else v = *reinterpret_cast<const float4*>(src + br * D + c);
-        }
-        z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
-      }
-    }
-    // the half row in two bf16 parts: row r of Z, its head's columns (a box for each half of a
+    float z[32];
+    // block cb in two bf16 parts: row r of Z, its head's columns (a box for each half of a
     // 128-wide head)
-    auto put_z = [&]() {
+    auto put_z = [&](int cb) {
 #pragma unroll
-      for (int u = 0; u < Z / 8; ++u) {
+      for (int u = 0; u < 4; ++u) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float x = z[8 * u + 2 * i], y = z[8 * u + 2 * i + 1];
           hi[i] = pack_bf16(x, y);
-          lo[i] = pack_bf16(x - bf16_lo(hi[i]), y - bf16_hi(hi[i]));
+          const float2 e = __fadd2_rn(make_float2(x, y), make_float2(-bf16_lo(hi[i]), -bf16_hi(hi[i])));
+          lo[i] = pack_bf16(e.x, e.y);
         }
-        const int box = NH == 2 ? h : hf, unit = NH == 2 ? hf * 4 + u : u;
+        const int box = NH == 2 ? h : hf, unit = (NH == 2 ? hf : cb) * 4 + u;
         const uint32_t off = (uint32_t)box * kBoxBytes + (uint32_t)r * 128 + (uint32_t)((unit ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(zh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(zl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+    };
+    {
+      const int64_t sq = (int64_t)batch * args.heads + head;
+      const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * D * D
+                                       : P.z0 != nullptr ? P.z0 + sq * D * D : nullptr;
+      const bool tr = args.segs == 1 && P.z0_t;
+#pragma unroll 1
+      for (int cb = 0; cb < kBlocks; ++cb) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+          const int c = hf * Z + cb * 32 + i;
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (live && src != nullptr) {
+            if (tr) v = make_float4(src[c * D + br], src[(c + 1) * D + br], src[(c + 2) * D + br], src[(c + 3) * D + br]);
+            else v = *reinterpret_cast<const float4*>(src + br * D + c);
+          }
+          z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
+        }
+        if (kBlocks > 1) tmem_st32(tS + cb * 32, z);
+        put_z(cb);
+      }
+      if (kBlocks > 1) tmem_wait_st();
       fence_async();
       warp_arrive(&bar[kZ], lane);
-    };
-    put_z();
+    }
     uint32_t dz = 0;
+#pragma unroll 1
     for (int k = 0; k < chunks; ++k) {
       const uint32_t ph = k & 1;
       const Chunk c = chunk_of(begin + k * kC, end, n, rev);
@@ -480,19 +534,22 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       mbar_pass(&bar[kFullB], ph, failed);
-      uint4 rest[2][4];
-      form_half<NH>(sb, p0, p1, wt, 1.f, 1.f, t, 0, exact, rest[0]);
-      fence_async();
-      warp_arrive(&bar[kParts], lane);
-      form_half<NH>(sb, p0, p1, wt, 1.f, 1.f, t, 1, exact, rest[1]);
-      fence_async();
-      warp_arrive(&bar[kParts + 1], lane);
+      uint4 rest[4], rest0[4];
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        form_half<NH>(sb, p0, p1, wt, 1.f, 1.f, t, half, exact, rest);
+        fence_async();
+        warp_arrive(&bar[kParts + half], lane);
+        if (half == 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) rest0[i] = rest[i];
+      }
       warp_arrive(&bar[kFreeB], lane);
       if (exact) {   // the rest, over the first parts once their products are done
         mbar_pass(&bar[kDZ], dz, failed);
         dz ^= 1;
-        put_rest(p0, t, 0, rest[0]);
-        put_rest(p0, t, 1, rest[1]);
+        put_rest(p0, t, 0, rest0);
+        put_rest(p0, t, 1, rest);
         fence_async();
         warp_arrive(&bar[kParts + 2], lane);
       }
@@ -501,33 +558,49 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const float e = lg * (float)(c.cnt - 1 + c.lead);
       const bool near = e > -1.f;
       const float fm = near ? expm1f(e * 0.69314718055994531f) : exp2f(e);
+      const float2 f2 = make_float2(fm, fm);
       mbar_pass(&bar[kDZ], dz, failed);
       dz ^= 1;
+      if (k + 1 < chunks) mbar_pass(&bar[kO2], ph, failed);   // (4) has read the old Z
       tmem_fence_after();
-#pragma unroll
-      for (int cb = 0; cb < Z / 32; ++cb) {
+#pragma unroll 1
+      for (int cb = 0; cb < kBlocks; ++cb) {
         float v[32];
-        tmem_ld32(v, tZ + lanes + (NH == 2 ? h * 64 : 0) + hf * Z + cb * 32);
+        tmem_ld32(v, tD + cb * 32);
+        if (kBlocks > 1) tmem_ld32(z, tS + cb * 32);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float x = z[cb * 32 + j];
-          z[cb * 32 + j] = fmaf(x, fm, near ? x : 0.f) + v[j];
+        for (int j = 0; j < 32; j += 2) {
+          const float2 x = make_float2(z[j], z[j + 1]);
+          const float2 y = __fadd2_rn(__ffma2_rn(x, f2, near ? x : make_float2(0.f, 0.f)), make_float2(v[j], v[j + 1]));
+          z[j] = y.x;
+          z[j + 1] = y.y;
         }
+        if (kBlocks > 1) tmem_st32(tS + cb * 32, z);
+        if (k + 1 < chunks) put_z(cb);
       }
+      if (kBlocks > 1) tmem_wait_st();
       if (k + 1 < chunks) {
-        mbar_pass(&bar[kO2], ph, failed);   // (4) has read the old Z
-        put_z();
+        fence_async();
+        warp_arrive(&bar[kZ], lane);
       }
     }
     // the segment that holds the last token (the first one of an empty sequence)
     const int last = n > 0 ? (n - 1) / args.seg_len : 0;
-    if (P.zn != nullptr && seg == last && live) {
+    if (P.zn != nullptr && seg == last) {
       const float f = rev && n > 0 ? exp2f(lg) : 1.f;
       float* dst = P.zn + ((int64_t)batch * args.heads + head) * D * D + (int64_t)br * D + hf * Z;
+#pragma unroll 1
+      for (int cb = 0; cb < kBlocks; ++cb) {
+        if (kBlocks > 1) {
+          tmem_ld32(z, tS + cb * 32);
+          tmem_wait_ld();
+        }
+        if (live)
 #pragma unroll
-      for (int i = 0; i < Z; i += 4)
-        *reinterpret_cast<float4*>(dst + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<float4*>(dst + cb * 32 + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
+      }
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -774,9 +847,9 @@ cudaError_t launch_la_tc(LaArgs& a, int d, int sms, cudaStream_t s) {
   memset(&m, 0, sizeof m);
   for (int i = 0; i < a.passes; ++i) {
     const LaPass& p = a.pass[i];
-    const bf16* base[3] = {p.a, p.b, p.c};
-    const int64_t ld[3] = {p.lda, p.ldb, p.ldc};
-    for (int j = 0; j < 3; ++j) {
+    const bf16* base[4] = {p.a, p.b, p.c, p.out};
+    const int64_t ld[4] = {p.lda, p.ldb, p.ldc, p.ldo};
+    for (int j = 0; j < 4; ++j) {
       const cuuint64_t dim[3] = {(cuuint64_t)a.heads * d, (cuuint64_t)a.T, (cuuint64_t)a.B};
       const cuuint64_t str[2] = {(cuuint64_t)ld[j] * 2, a.B > 1 ? (cuuint64_t)ld[j] * 2 * a.T : (cuuint64_t)ld[j] * 2};
       const cuuint32_t box[3] = {64u, (cuuint32_t)kC, 1u}, est[3] = {1u, 1u, 1u};

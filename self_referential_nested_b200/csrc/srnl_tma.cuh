@@ -52,6 +52,12 @@ __device__ __forceinline__ void mbar_init(unsigned long long* bar, uint32_t coun
 __device__ __forceinline__ void mbar_expect(unsigned long long* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
+// The slow path of a wait, out of line: kernels of many roles run each wait's code a few times
+// a tile, and their instruction fetches count.
+__device__ __noinline__ bool mbar_wait_slow(unsigned long long* bar, uint32_t phase, int* failed) {
+  mbar_wait(bar, phase, failed);
+  return *reinterpret_cast<volatile int*>(failed) == 0;
+}
 // mbar_wait with a first look that reads nothing but the barrier; false once a wait has given up.
 __device__ __forceinline__ bool mbar_pass(unsigned long long* bar, uint32_t phase, int* failed) {
   uint32_t done;
@@ -61,9 +67,7 @@ __device__ __forceinline__ bool mbar_pass(unsigned long long* bar, uint32_t phas
       : "=r"(done)
       : "r"(smem_u32(bar)), "r"(phase)
       : "memory");
-  if (done) return true;
-  mbar_wait(bar, phase, failed);
-  return *reinterpret_cast<volatile int*>(failed) == 0;
+  return done || mbar_wait_slow(bar, phase, failed);
 }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
