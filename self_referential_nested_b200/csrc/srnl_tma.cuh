@@ -52,22 +52,36 @@ __device__ __forceinline__ void mbar_init(unsigned long long* bar, uint32_t coun
 __device__ __forceinline__ void mbar_expect(unsigned long long* bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
-// The slow path of a wait, out of line: kernels of many roles run each wait's code a few times
-// a tile, and their instruction fetches count.
-__device__ __noinline__ bool mbar_wait_slow(unsigned long long* bar, uint32_t phase, int* failed) {
-  mbar_wait(bar, phase, failed);
-  return *reinterpret_cast<volatile int*>(failed) == 0;
-}
-// mbar_wait with a first look that reads nothing but the barrier; false once a wait has given up.
-__device__ __forceinline__ bool mbar_pass(unsigned long long* bar, uint32_t phase, int* failed) {
+// One look at a barrier, which may suspend the thread for up to kNapNs until the phase completes:
+// a warp that polls takes issue slots from those that work.
+constexpr uint32_t kNapNs = 100000;
+__device__ __forceinline__ bool mbar_try(unsigned long long* bar, uint32_t phase) {
   uint32_t done;
   asm volatile(
-      "{\n\t.reg .pred P1;\n\tmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2;\n\t"
+      "{\n\t.reg .pred P1;\n\tmbarrier.try_wait.parity.shared::cta.b64 P1, [%1], %2, %3;\n\t"
       "selp.b32 %0, 1, 0, P1;\n\t}\n"
       : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(phase)
+      : "r"(smem_u32(bar)), "r"(phase), "r"(kNapNs)
       : "memory");
-  return done || mbar_wait_slow(bar, phase, failed);
+  return done != 0;
+}
+// The rest of a wait, out of line (kernels of many roles run each wait's code a few times a tile,
+// and their instruction fetches count): bounded by kWaitLimit looks or kWaitNs of wall time, after
+// which *failed is set and every later wait returns at once.
+__device__ __noinline__ bool mbar_wait_slow(unsigned long long* bar, uint32_t phase, int* failed) {
+  if (*reinterpret_cast<volatile int*>(failed)) return false;
+  const unsigned long long t0 = global_ns();
+  for (long long looks = 0; looks < kWaitLimit; ++looks) {
+    if (mbar_try(bar, phase)) return true;
+    if (*reinterpret_cast<volatile int*>(failed)) return false;
+    if (global_ns() - t0 > kWaitNs) break;
+  }
+  *failed = 1;
+  return false;
+}
+// Waits for a phase of a barrier; false once a wait of the block has given up.
+__device__ __forceinline__ bool mbar_pass(unsigned long long* bar, uint32_t phase, int* failed) {
+  return mbar_try(bar, phase) || mbar_wait_slow(bar, phase, failed);
 }
 __device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
