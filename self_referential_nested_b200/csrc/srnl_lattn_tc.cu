@@ -149,6 +149,48 @@ __device__ __forceinline__ void put_rest(unsigned char* p, int t, int half, cons
   }
 }
 
+// The same for a quarter (32 tokens) into a slot of the main kernel's ring: part 0, then 8 KB on
+// part 1, each two boxes of 32 x 64.  A thread takes 2 units.
+constexpr uint32_t kSlot = 16384, kSlotPart = 8192, kSlotBox = 4096;
+template <int NH>
+__device__ __forceinline__ void form_quarter(const unsigned char* b, unsigned char* slot, const float* w, int t, int quarter, bool third,
+                                             uint4 (&rest)[2]) {
+  const int u = t & 15, box = u >> 3;
+  const float* wr = w + (NH == 2 ? box : 0) * kC + 32 * quarter;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (t >> 4) + 16 * i;
+    const uint32_t sw = (uint32_t)(((u & 7) ^ (r & 7)) << 4);
+    const uint4 raw = *reinterpret_cast<const uint4*>(b + box * kBoxBytes + (32 * quarter + r) * 128 + sw);
+    const float f = wr[r];
+    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+    uint32_t o0[4] = {0u, 0u, 0u, 0u}, o1[4] = {0u, 0u, 0u, 0u}, o2[4] = {0u, 0u, 0u, 0u};
+    if (f != 0.f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float2 x = __fmul2_rn(make_float2(bf16_lo(in[k]), bf16_hi(in[k])), make_float2(f, f));
+        o0[k] = pack_bf16(x.x, x.y);
+        x = __fadd2_rn(x, make_float2(-bf16_lo(o0[k]), -bf16_hi(o0[k])));
+        o1[k] = pack_bf16(x.x, x.y);
+        if (third) o2[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
+      }
+    }
+    unsigned char* at = slot + box * kSlotBox + r * 128 + sw;
+    *reinterpret_cast<uint4*>(at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    *reinterpret_cast<uint4*>(at + kSlotPart) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  }
+}
+// The rest of a quarter into one part of a slot.
+__device__ __forceinline__ void put_quarter(unsigned char* part, int t, const uint4 (&rest)[2]) {
+  const int u = t & 15;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (t >> 4) + 16 * i;
+    *reinterpret_cast<uint4*>(part + (u >> 3) * kSlotBox + r * 128 + (uint32_t)(((u & 7) ^ (r & 7)) << 4)) = rest[i];
+  }
+}
+
 // Rows of tile c from token `from` on become zero (tokens behind a sequence's last one hold
 // anything, and zero times NaN is NaN).
 __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, int threads) {
@@ -226,14 +268,14 @@ __device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int x, in
   for (int h = 0; h < 2; ++h) tma_prefetch_3d(map, x + 64 * h, token, batch);
 }
 
-enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kZ = kParts + 3, kDZ, kClear, kOut, kBars };   // kParts: halves 0 and 1, and the rest
+enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars };   // kParts, kPDone: the ring's slots
 
 template <int D>
 __global__ void __launch_bounds__(kLaThreads, 1)
     decay_tc_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
   constexpr int NH = kC / D;
   extern __shared__ __align__(1024) unsigned char sm[];
-  unsigned char *sa = sm, *sb = sa + kTile, *sc = sb + kTile, *p0 = sc + kTile, *p1 = p0 + kTile, *zh = p1 + kTile, *zl = zh + kTile;
+  unsigned char *sa = sm, *sb = sa + kTile, *sc = sb + kTile, *ps = sc + kTile, *so = ps + kTile, *zh = so + kTile, *zl = zh + kTile;
   float* pw = reinterpret_cast<float*>(zl + kTile);      // [NH][kC]: g^n
   float* wt = pw + NH * kC;                              // [NH][kC]: weights of the chunk's rows of b
   unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
@@ -258,7 +300,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   if (tid == 0) {
     *failed = 0;
     for (int i = 0; i < kBars; ++i) {
-      mbar_init(&bar[i], i == kRows || i == kOFree || i == kOut ? 4 : (i >= kParts && i < kParts + 3) || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : 1);
+      mbar_init(&bar[i], i == kRows || i == kOFree ? 4 : i == kParts || i == kParts + 1 || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : i == kFreeC ? 2 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -289,35 +331,19 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
     }
   } else if (warp == 3) {
-    // a, and c, in whose tile a whole chunk's O leaves once its products are done
     if (lane == 0) {
       const int x = group * kC;
-      for (int k = 0; k <= chunks; ++k) {
-        const Chunk c = chunk_of(begin + k * kC, end, n, rev), d = chunk_of(begin + (k + 1) * kC, end, n, rev);
-        if (k < chunks) {
-          if (k + 1 < chunks) {
-            prefetch_chunk(&maps.m[which][0], x, d.token0, batch);
-            prefetch_chunk(&maps.m[which][2], x, d.token0, batch);
-          }
-          if (!mbar_pass(&bar[kFreeA], (k & 1) ^ 1, failed)) break;
-          load_tile(sa, &maps.m[which][0], x, c.token0, batch, &bar[kFullA]);
+      for (int k = 0; k < chunks; ++k) {
+        const int token0 = chunk_of(begin + k * kC, end, n, rev).token0, next = chunk_of(begin + (k + 1) * kC, end, n, rev).token0;
+        if (k + 1 < chunks) {
+          prefetch_chunk(&maps.m[which][0], x, next, batch);
+          prefetch_chunk(&maps.m[which][2], x, next, batch);
         }
-        if (k > 0) {
-          const Chunk o = chunk_of(begin + (k - 1) * kC, end, n, rev);
-          if (!mbar_pass(&bar[kOut], (k - 1) & 1, failed)) break;
-          if (o.cnt == kC) {
-            for (int h = 0; h < 2; ++h)
-              if (x + 64 * h < args.heads * D) tma_store_3d(&maps.m[which][3], smem_u32(sc) + h * kBoxBytes, x + 64 * h, o.token0, batch);
-            bulk_commit();
-            bulk_wait_read<0>();
-          }
-        }
-        if (k < chunks) {
-          if (!mbar_pass(&bar[kFreeC], (k & 1) ^ 1, failed)) break;
-          load_tile(sc, &maps.m[which][2], x, c.token0, batch, &bar[kFullC]);
-        }
+        if (!mbar_pass(&bar[kFreeA], (k & 1) ^ 1, failed)) break;
+        load_tile(sa, &maps.m[which][0], x, token0, batch, &bar[kFullA]);
+        if (!mbar_pass(&bar[kFreeC], (k & 1) ^ 1, failed)) break;
+        load_tile(sc, &maps.m[which][2], x, token0, batch, &bar[kFullC]);
       }
-      bulk_wait_all();
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -367,33 +393,39 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           for (int s = 0; s < 8; ++s)
             mma_k16_tmem_a(tO + h * 64, tG + h * 128 + s * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
         mma_commit(&bar[kO]);
+        mma_commit(&bar[kFreeC]);
       }
     }
   } else if (warp == 2) {
     if (lane == 0) {
-      // (5) dZ from the parts of w b, half a chunk at a time, then from the rest of both
+      // (5) dZ from the parts of w b, a quarter of the tokens a step, then from the rest, two
+      // quarters a step; steps alternate between the ring's slots
       constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
-      const uint64_t dc = desc_mn_major(smem_u32(sc), kBoxBytes);
-      const uint64_t dp0 = desc_mn_major(smem_u32(p0), kBoxBytes / 2), dp1 = desc_mn_major(smem_u32(p1), kBoxBytes / 2);
+      const uint64_t dc = desc_mn_major(smem_u32(sc), kBoxBytes), dp = desc_mn_major(smem_u32(ps), kSlotBox);
+      const int uses = exact ? 3 : 2;   // of a slot in a chunk
+#pragma unroll 1
       for (int k = 0; k < chunks; ++k) {
         mbar_pass(&bar[kFullC], k & 1, failed);
-        for (int half = 0; half < (exact ? 3 : 2); ++half) {
-          mbar_pass(&bar[kParts + half], k & 1, failed);
+#pragma unroll 1
+        for (int st = 0; st < 2 * uses; ++st) {
+          const int slot = st & 1;
+          mbar_pass(&bar[kParts + slot], (k * uses + (st >> 1)) & 1, failed);
           tmem_fence_after();
-          if (half < 2) {
+          const uint64_t pa = dp + (uint64_t)slot * (kSlot >> 4);
+          if (st < 4) {
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
-#pragma unroll
-              for (int s = 0; s < 4; ++s)
-                mma_k16_desc(tZ, (part == 0 ? dp0 : dp1) + (uint64_t)half * (kHalfBytes >> 4) + (uint64_t)s * 128,
-                             dc + (uint64_t)(half * 4 + s) * 128, iZ, half > 0 || part > 0 || s > 0);
+            for (int i = 0; i < 4; ++i)   // part i >> 1, 16 tokens i & 1
+              mma_k16_desc(tZ, pa + (uint64_t)(i >> 1) * (kSlotPart >> 4) + (uint64_t)(i & 1) * 128, dc + (uint64_t)(st * 2 + (i & 1)) * 128,
+                           iZ, st > 0 || i > 0);
           } else {
 #pragma unroll
-            for (int s = 0; s < 8; ++s)
-              mma_k16_desc(tZ, dp0 + (uint64_t)(s >> 2) * (kHalfBytes >> 4) + (uint64_t)(s & 3) * 128, dc + (uint64_t)s * 128, iZ, true);
+            for (int i = 0; i < 4; ++i)   // quarter i >> 1 of two, 16 tokens i & 1
+              mma_k16_desc(tZ, pa + (uint64_t)(i >> 1) * (kSlotPart >> 4) + (uint64_t)(i & 1) * 128, dc + (uint64_t)((st - 4) * 4 + i) * 128,
+                           iZ, true);
           }
-          if (half > 0) mma_commit(&bar[kDZ]);
+          mma_commit(&bar[kPDone + slot]);
         }
+        mma_commit(&bar[kDZ]);
         mma_commit(&bar[kFreeC]);
       }
     }
@@ -431,10 +463,10 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       }
       tmem_wait_st();
       warp_arrive(&bar[kRows], lane);
-      // O: a whole chunk's through c's tile (free once (3) and (5) are done), the last, shorter
-      // one's straight to its rows
+      // O: a whole chunk's leaves by TMA, the last, shorter one's goes straight to its rows
+      if (lane == 0) bulk_wait_read<0>();   // the last chunk's has left the staging tile
       mbar_pass(&bar[kO], ph, failed);
-      if (c.cnt == kC) mbar_pass(&bar[kFreeC], ph, failed);
+      __syncwarp();
       tmem_fence_after();
       const int token = c.token0 + r;
       bf16* dst = P.out + ((int64_t)batch * args.T + token) * P.ldo + (int64_t)group * kC;
@@ -443,20 +475,29 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         float v[32];
         tmem_ld32(v, tO + lanes + cb * 32);
         tmem_wait_ld();
+        if (cb == 3) warp_arrive(&bar[kOFree], lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 w = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
                                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
           if (c.cnt == kC)
-            *reinterpret_cast<uint4*>(sc + (cb >> 1) * kBoxBytes + r * 128 + ((((cb & 1) * 4 + j) ^ (r & 7)) << 4)) = w;
+            *reinterpret_cast<uint4*>(so + (cb >> 1) * kBoxBytes + r * 128 + ((((cb & 1) * 4 + j) ^ (r & 7)) << 4)) = w;
           else if (ord < c.cnt && (NH == 1 || group * 2 + (cb >> 1) < args.heads))
             *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) = w;
         }
       }
-      fence_async();
-      warp_arrive(&bar[kOFree], lane);
-      if (lane == 0) mbar_arrive(&bar[kOut]);
+      if (c.cnt == kC) {
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          for (int h = 0; h < 2; ++h)
+            if (NH == 1 || group * 2 + h < args.heads)
+              tma_store_3d(&maps.m[which][3], smem_u32(so) + h * kBoxBytes + q * 4096, group * kC + 64 * h, c.token0 + 32 * q, batch);
+          bulk_commit();
+        }
+      }
     }
+    if (lane == 0) bulk_wait_all();
   } else if (warp >= 8) {
     // ---- rows of the state: channel r of the group's b, half of its head's c channels, fp32, in
     // 32-column blocks: one in registers (64-wide heads) or two in TMEM, where G leaves room.  The
@@ -514,7 +555,6 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       fence_async();
       warp_arrive(&bar[kZ], lane);
     }
-    uint32_t dz = 0;
 #pragma unroll 1
     for (int k = 0; k < chunks; ++k) {
       const uint32_t ph = k & 1;
@@ -534,24 +574,26 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         }
       }
       mbar_pass(&bar[kFullB], ph, failed);
-      uint4 rest[4], rest0[4];
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        form_half<NH>(sb, p0, p1, wt, 1.f, 1.f, t, half, exact, rest);
-        fence_async();
-        warp_arrive(&bar[kParts + half], lane);
-        if (half == 0)
+      uint4 rest[4][2];
+      const int uses = exact ? 3 : 2;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) rest0[i] = rest[i];
+      for (int st = 0; st < 4; ++st) {
+        const int use = k * uses + (st >> 1);
+        if (use > 0) mbar_pass(&bar[kPDone + (st & 1)], (use - 1) & 1, failed);   // the slot's last products are done
+        form_quarter<NH>(sb, ps + (st & 1) * kSlot, wt, t, st, exact, rest[st]);
+        fence_async();
+        warp_arrive(&bar[kParts + (st & 1)], lane);
       }
       warp_arrive(&bar[kFreeB], lane);
-      if (exact) {   // the rest, over the first parts once their products are done
-        mbar_pass(&bar[kDZ], dz, failed);
-        dz ^= 1;
-        put_rest(p0, t, 0, rest0);
-        put_rest(p0, t, 1, rest);
-        fence_async();
-        warp_arrive(&bar[kParts + 2], lane);
+      if (exact) {
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          mbar_pass(&bar[kPDone + st], (k * uses + 1) & 1, failed);
+          put_quarter(ps + st * kSlot, t, rest[2 * st]);
+          put_quarter(ps + st * kSlot + kSlotPart, t, rest[2 * st + 1]);
+          fence_async();
+          warp_arrive(&bar[kParts + st], lane);
+        }
       }
       // z <- g^m z + dZ; a factor near one is applied as z + (g^m - 1) z, whose error does not
       // add up over thousands of chunks
@@ -559,8 +601,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       const bool near = e > -1.f;
       const float fm = near ? expm1f(e * 0.69314718055994531f) : exp2f(e);
       const float2 f2 = make_float2(fm, fm);
-      mbar_pass(&bar[kDZ], dz, failed);
-      dz ^= 1;
+      mbar_pass(&bar[kDZ], ph, failed);
       if (k + 1 < chunks) mbar_pass(&bar[kO2], ph, failed);   // (4) has read the old Z
       tmem_fence_after();
 #pragma unroll 1
@@ -852,7 +893,7 @@ cudaError_t launch_la_tc(LaArgs& a, int d, int sms, cudaStream_t s) {
     for (int j = 0; j < 4; ++j) {
       const cuuint64_t dim[3] = {(cuuint64_t)a.heads * d, (cuuint64_t)a.T, (cuuint64_t)a.B};
       const cuuint64_t str[2] = {(cuuint64_t)ld[j] * 2, a.B > 1 ? (cuuint64_t)ld[j] * 2 * a.T : (cuuint64_t)ld[j] * 2};
-      const cuuint32_t box[3] = {64u, (cuuint32_t)kC, 1u}, est[3] = {1u, 1u, 1u};
+      const cuuint32_t box[3] = {64u, j == 3 ? 32u : (cuuint32_t)kC, 1u}, est[3] = {1u, 1u, 1u};   // out: a warp's rows
       if (enc(&m.m[i][j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(base[j]), dim, str, box, est,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
