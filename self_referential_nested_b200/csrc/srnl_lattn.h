@@ -1,5 +1,5 @@
 // Interface between the linear attention entry points (srnl_lattn.cu) and the tensor-core
-// passes of 64- and 128-wide heads (srnl_lattn_tc.cu).
+// passes (srnl_lattn_tc.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -21,16 +21,18 @@ struct LaPass {
 
 struct LaArgs {
   LaPass pass[3];
-  int passes, B, T, heads, segs, seg_len;   // segments of seg_len tokens per sequence
+  int passes, B, T, heads, d, segs, seg_len;   // segments of seg_len tokens per sequence
   const float* log2g;                       // [heads]
   const int* lengths;                       // [B] or nullptr
   float* seg_state;                         // [pass][B][heads][segs][D][D]: what each segment adds, then its start
   int* err;
 };
 
-// Segments per sequence that the tensor-core passes use: one when the sequences fill the GPU.
+// CTAs that a sequence's heads take (two heads of up to 64 channels share one).
+int la_groups(int heads, int d);
+// Segments per sequence for that many sequences x groups: one when they fill the GPU by themselves.
 int la_tc_segments(int T, int seqs, int sms);
-cudaError_t launch_la_tc(LaArgs& a, int d, int sms, cudaStream_t s);
+cudaError_t launch_la_tc(LaArgs& a, int sms, cudaStream_t s);
 cudaError_t prepare_la_tc(int d);
 
 }  // namespace srnl

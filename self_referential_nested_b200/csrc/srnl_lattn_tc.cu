@@ -1,6 +1,6 @@
-// Tensor-core passes of linear attention for 64- and 128-wide heads (sm_100a).
+// Tensor-core passes of linear attention (sm_100a).
 //
-// One CTA takes a 128-channel group (a 128-wide head, or two 64-wide ones) of a segment of a
+// One CTA takes a 128-channel group (a 128-wide head, or two narrower ones) of a segment of a
 // sequence, in chunks of 128 tokens, with the formulas of srnl_lattn.cu:
 //   G  = a b^T                          tokens x tokens, per head          (1)
 //   O  = a Z                            tokens x channels                  (4)
@@ -15,8 +15,9 @@
 // (masking, O), eight half a row of the state per thread, in fp32 registers (the decayed b, Z).
 // Z and w b are split into two bf16 parts (a third of w b where the state itself is asked for).
 //
-// Two 64-wide heads share a CTA so that every product has 128 rows; (5) computes the two
-// heads' cross terms with it and nobody reads them.
+// Two heads of up to 64 channels share a CTA so that every product has 128 rows; (5) computes
+// the two heads' cross terms with it and nobody reads them.  A 32-wide head runs as a 64-wide one
+// whose upper half the loads fill with zeros and the stores leave out.
 //
 // What bounds it: the chain of a chunk (products, masking and the state's update wait for one
 // another, about 2 us) where few sequences run, memory where many do.
@@ -40,30 +41,31 @@ using bf16 = __nv_bfloat16;
 constexpr int kC = 128;                  // tokens per chunk, and channels per CTA
 constexpr uint32_t kBoxBytes = kC * 128; // 128 tokens x 64 channels
 constexpr uint32_t kTile = 2 * kBoxBytes;
-constexpr int kLaThreads = 512;          // load, two of products, 1 idle, 4 row and 8 state warps
+__host__ __device__ constexpr int la_threads(int nh) { return 128 * (3 + nh); }   // loads and products, 4 row warps a head, 8 state warps
+constexpr int kSegThreads = 512;         // of the segments' kernel
 constexpr int kStateThreads = 256;
 constexpr uint32_t kHalfBytes = kTile / 2;   // 64 tokens of a part of w b: two boxes of 64 x 64
 
 struct LaMaps {
-  CUtensorMap m[3][4];   // [pass][a, b, c, out]
+  CUtensorMap m[3][4];   // [pass][a, b, c, out]: (channel of 64 or fewer, 64-channel piece, token, batch)
 };
 
-__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap* map, uint32_t src, int piece, int token, int batch) {
+  asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(x), "r"(y), "r"(z), "r"(src)
+               "r"(0), "r"(piece), "r"(token), "r"(batch), "r"(src)
                : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, unsigned long long* bar) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int piece, int token, int batch, unsigned long long* bar) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(piece), "r"(token), "r"(batch), "r"(smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(x),
-               "r"(y), "r"(z)
+__device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap* map, int piece, int token, int batch) {
+  asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(reinterpret_cast<uint64_t>(map)), "r"(0),
+               "r"(piece), "r"(token), "r"(batch)
                : "memory");
 }
 __device__ __forceinline__ void mbar_arrive(unsigned long long* bar) {
@@ -200,51 +202,54 @@ __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, in
   }
 }
 
-// A warp's 32 rows of G, masked and decayed, over G's own columns as bf16 (column block jb's
-// result goes to columns already read).  The distance falls along a row's columns (rises, in
-// reverse).  Away from the diagonal the powers are one product after another from the nearest
-// token on, two columns an instruction; on it, where powers below zero would overflow, they are
-// read from the table.
-template <int NH, bool REV>
-__device__ __forceinline__ void mask_rows(uint32_t tG, const float* pw, int q, int lane) {
+// One 32-column block of a warp's 32 rows of G, masked and decayed, as bf16 pairs; `diff`: blocks
+// between it and the diagonal one.  The distance falls along a row's columns (rises, in reverse).
+// Away from the diagonal the powers are one product after another from the nearest token on, two
+// columns an instruction; on it, where powers below zero would overflow, they are read from the
+// table (zeros lie before its start).
+template <bool REV>
+__device__ __forceinline__ void mask_block(const float (&v)[32], uint32_t (&w)[16], const float* p, int diff, int lane) {
+  if (diff < 0) {
 #pragma unroll
-  for (int h = 0; h < NH; ++h) {
-    const float* p = pw + h * kC;
-    const float g1 = p[1];
-    const float2 g2 = make_float2(g1 * g1, g1 * g1);
-#pragma unroll 1
-    for (int jb = 0; jb < 4; ++jb) {
-      uint32_t w[16];
-      if (REV ? jb < q : jb > q) {
+    for (int i = 0; i < 16; ++i) w[i] = 0u;
+  } else if (diff == 0) {
+    const float* at = p + (REV ? -lane : lane);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = 0u;
-      } else {
-        float v[32];
-        tmem_ld32(v, tG + h * 128 + jb * 32);
-        if (jb == q) {
-          tmem_wait_ld();
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            const float f = REV ? p[max(j - lane, 0)] : p[max(lane - j, 0)];
-            v[j] = (REV ? j >= lane : j <= lane) ? v[j] * f : 0.f;
-          }
-#pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-        } else {
-          const float near = REV ? p[(jb - q) * 32 - lane] : p[(q - jb) * 32 + lane - 31];
-          float2 f = REV ? make_float2(near, near * g1) : make_float2(near * g1, near);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int i = REV ? k : 15 - k;
-            const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f);
-            w[i] = pack_bf16(x.x, x.y);
-            f = __fmul2_rn(f, g2);
-          }
-        }
-      }
-      tmem_st16(tG + h * 128 + jb * 16, w);
+    for (int i = 0; i < 16; ++i) {
+      const int j = 2 * i;
+      const float x = (REV ? j >= lane : j <= lane) ? v[j] * at[REV ? j : -j] : 0.f;
+      const float y = (REV ? j + 1 >= lane : j + 1 <= lane) ? v[j + 1] * at[REV ? j + 1 : -j - 1] : 0.f;
+      w[i] = pack_bf16(x, y);
     }
+  } else {
+    const float g1 = p[1], near = REV ? p[diff * 32 - lane] : p[diff * 32 + lane - 31];
+    const float2 g2 = make_float2(g1 * g1, g1 * g1);
+    float2 f = REV ? make_float2(near, near * g1) : make_float2(near * g1, near);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int i = REV ? k : 15 - k;
+      const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), f);
+      w[i] = pack_bf16(x.x, x.y);
+      f = __fmul2_rn(f, g2);
+    }
+  }
+}
+
+// A warp's rows of a head's G, over G's own columns: block jb's result goes to columns
+// 16 jb .. + 15, which lie on blocks already read.
+template <bool REV>
+__device__ __forceinline__ void mask_rows(uint32_t tG, const float* pw, int q, int lane) {
+#pragma unroll 1
+  for (int j = 0; j < 4; j += 2) {
+    float v0[32], v1[32];
+    uint32_t w[16];
+    tmem_ld32(v0, tG + j * 32);
+    tmem_ld32(v1, tG + j * 32 + 32);
+    tmem_wait_ld();
+    mask_block<REV>(v0, w, pw, REV ? j - q : q - j, lane);
+    tmem_st16(tG + j * 16, w);
+    mask_block<REV>(v1, w, pw, REV ? j + 1 - q : q - j - 1, lane);
+    tmem_st16(tG + j * 16 + 16, w);
   }
 }
 
@@ -259,25 +264,28 @@ __device__ __forceinline__ Chunk chunk_of(int t0, int end, int n, int reverse) {
   return k;
 }
 
-__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, int x, int token, int batch, unsigned long long* bar) {
+// A tile: pieces 2 group and 2 group + 1 of 128 tokens.  A piece past the last head, a token
+// outside the sequence and the upper half of a 32-wide head's piece read as zeros.
+__device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap* map, int group, int token, int batch, unsigned long long* bar) {
   mbar_expect(bar, kTile);
-  for (int h = 0; h < 2; ++h) tma_load_3d(smem_u32(dst) + h * kBoxBytes, map, x + 64 * h, token, batch, bar);
+  for (int h = 0; h < 2; ++h) tma_load_4d(smem_u32(dst) + h * kBoxBytes, map, 2 * group + h, token, batch, bar);
 }
 // A tile into L2: the tiles have one buffer each and are loaded late.
-__device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int x, int token, int batch) {
-  for (int h = 0; h < 2; ++h) tma_prefetch_3d(map, x + 64 * h, token, batch);
+__device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int group, int token, int batch) {
+  for (int h = 0; h < 2; ++h) tma_prefetch_4d(map, 2 * group + h, token, batch);
 }
 
 enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars };   // kParts, kPDone: the ring's slots
 
 template <int D>
-__global__ void __launch_bounds__(kLaThreads, 1)
+__global__ void __launch_bounds__(la_threads(kC / D), 1)
     decay_tc_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
   constexpr int NH = kC / D;
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char *sa = sm, *sb = sa + kTile, *sc = sb + kTile, *ps = sc + kTile, *so = ps + kTile, *zh = so + kTile, *zl = zh + kTile;
-  float* pw = reinterpret_cast<float*>(zl + kTile);      // [NH][kC]: g^n
-  float* wt = pw + NH * kC;                              // [NH][kC]: weights of the chunk's rows of b
+  constexpr int kPw = 32 + kC;
+  float* pw = reinterpret_cast<float*>(zl + kTile) + 32; // [NH][kPw]: g^n, after 32 zeros each
+  float* wt = pw - 32 + NH * kPw;                        // [NH][kC]: weights of the chunk's rows of b
   unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
   int* failed = reinterpret_cast<int*>(tmem_slot + 1);
@@ -286,7 +294,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const int which = blockIdx.z, seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
   const int group = blockIdx.y % groups, batch = blockIdx.y / groups;
   const LaPass& P = args.pass[which];
-  const int rev = P.reverse;
+  const int rev = P.reverse, dr = args.d;   // dr: a head's channels, D or 32 of a 64-wide piece
   const bool exact = P.zn != nullptr;   // the state leaves: a third part of w b
   if (smem_u32(sm) & 1023u) {           // the swizzled tiles' alignment
     if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
@@ -300,14 +308,16 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   if (tid == 0) {
     *failed = 0;
     for (int i = 0; i < kBars; ++i) {
-      mbar_init(&bar[i], i == kRows || i == kOFree ? 4 : i == kParts || i == kParts + 1 || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : i == kFreeC ? 2 : 1);
+      mbar_init(&bar[i], i == kRows || i == kOFree ? 4 * NH : i == kParts || i == kParts + 1 || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : i == kFreeC ? 2 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < NH * kC; i += kLaThreads) {
+  for (int i = tid; i < NH * kC; i += la_threads(NH)) {
     const int h = group * NH + i / kC, m = i % kC;
-    pw[i] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
-    wt[i - m + (rev ? m : kC - 1 - m)] = pw[i];   // of a whole chunk; m tokens behind the row's
+    const float f = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
+    pw[i / kC * kPw + m] = f;
+    if (m < 32) pw[i / kC * kPw + m - 32] = 0.f;
+    wt[i - m + (rev ? m : kC - 1 - m)] = f;   // of a whole chunk; m tokens behind the row's
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -323,26 +333,24 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      const int x = group * kC;
       for (int k = 0; k < chunks; ++k) {
-        if (k + 1 < chunks) prefetch_chunk(&maps.m[which][1], x, chunk_of(begin + (k + 1) * kC, end, n, rev).token0, batch);
+        if (k + 1 < chunks) prefetch_chunk(&maps.m[which][1], group, chunk_of(begin + (k + 1) * kC, end, n, rev).token0, batch);
         if (!mbar_pass(&bar[kFreeB], (k & 1) ^ 1, failed)) break;
-        load_tile(sb, &maps.m[which][1], x, chunk_of(begin + k * kC, end, n, rev).token0, batch, &bar[kFullB]);
+        load_tile(sb, &maps.m[which][1], group, chunk_of(begin + k * kC, end, n, rev).token0, batch, &bar[kFullB]);
       }
     }
   } else if (warp == 3) {
     if (lane == 0) {
-      const int x = group * kC;
       for (int k = 0; k < chunks; ++k) {
         const int token0 = chunk_of(begin + k * kC, end, n, rev).token0, next = chunk_of(begin + (k + 1) * kC, end, n, rev).token0;
         if (k + 1 < chunks) {
-          prefetch_chunk(&maps.m[which][0], x, next, batch);
-          prefetch_chunk(&maps.m[which][2], x, next, batch);
+          prefetch_chunk(&maps.m[which][0], group, next, batch);
+          prefetch_chunk(&maps.m[which][2], group, next, batch);
         }
         if (!mbar_pass(&bar[kFreeA], (k & 1) ^ 1, failed)) break;
-        load_tile(sa, &maps.m[which][0], x, token0, batch, &bar[kFullA]);
+        load_tile(sa, &maps.m[which][0], group, token0, batch, &bar[kFullA]);
         if (!mbar_pass(&bar[kFreeC], (k & 1) ^ 1, failed)) break;
-        load_tile(sc, &maps.m[which][2], x, token0, batch, &bar[kFullC]);
+        load_tile(sc, &maps.m[which][2], group, token0, batch, &bar[kFullC]);
       }
     }
   } else if (warp == 1) {
@@ -429,37 +437,38 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         mma_commit(&bar[kFreeC]);
       }
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- token rows
-    const int q = warp & 3, r = 32 * q + lane;
+  } else if (warp >= 4 && warp < 4 + 4 * NH) {
+    // ---- token rows: a warp has 32 of them, of one head
+    const int q = warp & 3, head = NH == 2 ? (warp - 4) >> 2 : 0, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const int ord = rev ? kC - 1 - r : r;   // the token's place in the chunk's order
+    const float* p = pw + head * kPw;
+    const uint32_t tH = tG + lanes + head * 128, tR = tO + lanes + head * 64;
+    const bool live = group * NH + head < args.heads;
 #pragma unroll 1
     for (int k = 0; k < chunks; ++k) {
       const uint32_t ph = k & 1;
       const Chunk c = chunk_of(begin + k * kC, end, n, rev);
       mbar_pass(&bar[kG], ph, failed);
       tmem_fence_after();
-      if (rev) mask_rows<NH, true>(tG + lanes, pw, q, lane);
-      else mask_rows<NH, false>(tG + lanes, pw, q, lane);
+      if (rev) mask_rows<true>(tH, p, q, lane);
+      else mask_rows<false>(tH, p, q, lane);
       // the state's share of O, decayed to the row
+      const float f = ord + c.lead < kC ? p[ord + c.lead] : p[kC - 1] * p[1];
       mbar_pass(&bar[kO2], ph, failed);
       tmem_fence_after();
-#pragma unroll 2
-      for (int cb = 0; cb < 4; ++cb) {
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
         float v[32];
-        tmem_ld32(v, tO + lanes + cb * 32);
-        const float* p = pw + (NH == 2 ? cb >> 1 : 0) * kC;
-        const float f = ord + c.lead < kC ? p[ord + c.lead] : p[kC - 1] * p[1];
-        const float2 s = make_float2(f, f);
+        tmem_ld32(v, tR + cb * 32);
         tmem_wait_ld();
 #pragma unroll
         for (int j = 0; j < 32; j += 2) {
-          const float2 x = __fmul2_rn(make_float2(v[j], v[j + 1]), s);
+          const float2 x = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(f, f));
           v[j] = x.x;
           v[j + 1] = x.y;
         }
-        tmem_st32(tO + lanes + cb * 32, v);
+        tmem_st32(tR + cb * 32, v);
       }
       tmem_wait_st();
       warp_arrive(&bar[kRows], lane);
@@ -468,22 +477,20 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       mbar_pass(&bar[kO], ph, failed);
       __syncwarp();
       tmem_fence_after();
-      const int token = c.token0 + r;
-      bf16* dst = P.out + ((int64_t)batch * args.T + token) * P.ldo + (int64_t)group * kC;
-#pragma unroll 2
-      for (int cb = 0; cb < 4; ++cb) {
+      bf16* dst = P.out + ((int64_t)batch * args.T + c.token0 + r) * P.ldo + (int64_t)(group * NH + head) * dr;
+#pragma unroll
+      for (int cb = 0; cb < D / 32; ++cb) {
         float v[32];
-        tmem_ld32(v, tO + lanes + cb * 32);
+        tmem_ld32(v, tR + cb * 32);
         tmem_wait_ld();
-        if (cb == 3) warp_arrive(&bar[kOFree], lane);
+        if (cb == D / 32 - 1) warp_arrive(&bar[kOFree], lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint4 w = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
                                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
-          if (c.cnt == kC)
-            *reinterpret_cast<uint4*>(so + (cb >> 1) * kBoxBytes + r * 128 + ((((cb & 1) * 4 + j) ^ (r & 7)) << 4)) = w;
-          else if (ord < c.cnt && (NH == 1 || group * 2 + (cb >> 1) < args.heads))
-            *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) = w;
+          const int box = NH == 2 ? head : cb >> 1, unit = (cb & 1) * 4 + j;
+          if (c.cnt == kC) *reinterpret_cast<uint4*>(so + box * kBoxBytes + r * 128 + ((unit ^ (r & 7)) << 4)) = w;
+          else if (ord < c.cnt && live && cb * 32 < dr) *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) = w;
         }
       }
       if (c.cnt == kC) {
@@ -491,26 +498,27 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         __syncwarp();
         if (lane == 0) {
           for (int h = 0; h < 2; ++h)
-            if (NH == 1 || group * 2 + h < args.heads)
-              tma_store_3d(&maps.m[which][3], smem_u32(so) + h * kBoxBytes + q * 4096, group * kC + 64 * h, c.token0 + 32 * q, batch);
+            if (live && (NH == 1 || h == head))
+              tma_store_4d(&maps.m[which][3], smem_u32(so) + h * kBoxBytes + q * 4096, 2 * group + h, c.token0 + 32 * q, batch);
           bulk_commit();
         }
       }
     }
     if (lane == 0) bulk_wait_all();
-  } else if (warp >= 8) {
+  } else if (warp >= 4 + 4 * NH) {
     // ---- rows of the state: channel r of the group's b, half of its head's c channels, fp32, in
     // 32-column blocks: one in registers (64-wide heads) or two in TMEM, where G leaves room.  The
     // sums are taken here, not in the products' accumulator: their rounding there is not to
     // nearest and would add up over a long memory.
     constexpr int Z = D / 2, kBlocks = Z / 32;
-    const int q = warp & 3, t = tid - 256, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D, hf = (warp - 8) >> 2;
+    const int q = warp & 3, t = tid - 128 * (1 + NH), r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D,
+              hf = (warp - 4 - 4 * NH) >> 2;
     const int head = group * NH + h;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const uint32_t tS = tmem + 128 + lanes + hf * Z;                              // 128-wide heads: the state
     const uint32_t tD = tZ + lanes + (NH == 2 ? h * 64 : 0) + hf * Z;             // dZ
-    const bool live = head < args.heads;
-    const float lg = live ? args.log2g[head] : 0.f;
+    const bool live = head < args.heads && br < dr && hf * Z < dr;
+    const float lg = head < args.heads ? args.log2g[head] : 0.f;
     float z[32];
     // block cb in two bf16 parts: row r of Z, its head's columns (a box for each half of a
     // 128-wide head)
@@ -533,8 +541,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     };
     {
       const int64_t sq = (int64_t)batch * args.heads + head;
-      const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * D * D
-                                       : P.z0 != nullptr ? P.z0 + sq * D * D : nullptr;
+      const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * dr * dr
+                                       : P.z0 != nullptr ? P.z0 + sq * dr * dr : nullptr;
       const bool tr = args.segs == 1 && P.z0_t;
 #pragma unroll 1
       for (int cb = 0; cb < kBlocks; ++cb) {
@@ -543,8 +551,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
           const int c = hf * Z + cb * 32 + i;
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
           if (live && src != nullptr) {
-            if (tr) v = make_float4(src[c * D + br], src[(c + 1) * D + br], src[(c + 2) * D + br], src[(c + 3) * D + br]);
-            else v = *reinterpret_cast<const float4*>(src + br * D + c);
+            if (tr) v = make_float4(src[c * dr + br], src[(c + 1) * dr + br], src[(c + 2) * dr + br], src[(c + 3) * dr + br]);
+            else v = *reinterpret_cast<const float4*>(src + br * dr + c);
           }
           z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
         }
@@ -563,7 +571,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         asm volatile("bar.sync 2, 256;" ::: "memory");
         for (int i = t; i < NH * kC; i += kStateThreads) {
           const int row = i % kC, o = rev ? kC - 1 - row : row;
-          wt[i] = o < c.cnt ? pw[i - row + c.cnt - 1 - o] : 0.f;
+          wt[i] = o < c.cnt ? pw[i / kC * kPw + c.cnt - 1 - o] : 0.f;
         }
         asm volatile("bar.sync 2, 256;" ::: "memory");
         if (!rev) {
@@ -630,7 +638,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     const int last = n > 0 ? (n - 1) / args.seg_len : 0;
     if (P.zn != nullptr && seg == last) {
       const float f = rev && n > 0 ? exp2f(lg) : 1.f;
-      float* dst = P.zn + ((int64_t)batch * args.heads + head) * D * D + (int64_t)br * D + hf * Z;
+      float* dst = P.zn + ((int64_t)batch * args.heads + head) * dr * dr + (int64_t)br * dr + hf * Z;
 #pragma unroll 1
       for (int cb = 0; cb < kBlocks; ++cb) {
         if (kBlocks > 1) {
@@ -663,7 +671,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 enum { sFull = 0, sFree = 2, sParts = 4, sDone = 6, sBars = 8 };   // parts and done: one for each half
 
 template <int D>
-__global__ void __launch_bounds__(kLaThreads, 1)
+__global__ void __launch_bounds__(kSegThreads, 1)
     decay_segment_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
   constexpr int NH = kC / D;
   extern __shared__ __align__(1024) unsigned char sm[];
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int which = blockIdx.z, seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
   const int group = blockIdx.y % groups, batch = blockIdx.y / groups;
-  const int rev = args.pass[which].reverse;
+  const int rev = args.pass[which].reverse, dr = args.d;
   const bool exact = args.pass[which].zn != nullptr;
   if (smem_u32(sm) & 1023u) {
     if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
@@ -690,7 +698,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
     for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i >= sParts && i < sDone ? 12 : i >= sFree && i < sParts ? 13 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  for (int i = tid; i < NH * kC; i += kLaThreads) {   // weights of a whole chunk
+  for (int i = tid; i < NH * kC; i += kSegThreads) {   // weights of a whole chunk
     const int h = group * NH + i / kC, m = i % kC;
     wt[i - m + (rev ? m : kC - 1 - m)] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
   }
@@ -714,8 +722,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
         mbar_expect(&bar[sFull + s], 2 * kTile);
         for (int i = 0; i < 2; ++i)
           for (int h = 0; h < 2; ++h)
-            tma_load_3d(smem_u32(ring + (2 * s + i) * kTile) + h * kBoxBytes, &maps.m[which][1 + i], group * kC + 64 * h, c.token0,
-                        batch, &bar[sFull + s]);
+            tma_load_4d(smem_u32(ring + (2 * s + i) * kTile) + h * kBoxBytes, &maps.m[which][1 + i], 2 * group + h, c.token0, batch,
+                        &bar[sFull + s]);
       }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -779,7 +787,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
       if (chunks > 0) mbar_pass(&bar[sDone + 1], (chunks - 1) & 1, failed);
       tmem_fence_after();
       float* dst = args.seg_state +
-                   ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * D * D + (int64_t)(r % D) * D;
+                   ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * dr * dr + (int64_t)(r % D) * dr;
 #pragma unroll
       for (int cb = 0; cb < D / 32; ++cb) {
         float v[32];
@@ -790,7 +798,7 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0.f;
         }
-        if (head < args.heads)
+        if (head < args.heads && r % D < dr && cb * 32 < dr)
 #pragma unroll
           for (int j = 0; j < 32; j += 4)
             *reinterpret_cast<float4*>(dst + cb * 32 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
@@ -811,7 +819,8 @@ __global__ void __launch_bounds__(kLaThreads, 1)
 }
 
 // What each segment adds -> the state each segment starts from, in place; z0 is the first one's.
-__global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant__ LaArgs args, int D) {
+__global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant__ LaArgs args) {
+  const int D = args.d;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int i = blockIdx.x * 256 + threadIdx.x, which = blockIdx.z, head = blockIdx.y % args.heads, batch = blockIdx.y / args.heads;
@@ -840,7 +849,7 @@ __global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant_
   }
 }
 
-constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + 2 * (size_t)(kC / d) * kC * 4 + kBars * 8 + 16; }
+constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + (size_t)(kC / d) * (2 * kC + 32) * 4 + kBars * 8 + 16; }
 
 template <typename... P, typename... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
@@ -859,17 +868,20 @@ cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t sme
 
 template <int D>
 cudaError_t launch_tc(LaArgs& a, const LaMaps& m, cudaStream_t s) {
-  const int groups = (a.heads * D + kC - 1) / kC;
+  constexpr int NH = kC / D;
+  const int groups = (a.heads + NH - 1) / NH;
   if (a.segs > 1) {
-    cudaError_t e = launch_next(decay_segment_kernel<D>, dim3(a.segs - 1, a.B * groups, a.passes), kLaThreads, la_smem(D), s, m, a);
+    cudaError_t e = launch_next(decay_segment_kernel<D>, dim3(a.segs - 1, a.B * groups, a.passes), kSegThreads, la_smem(D), s, m, a);
     if (e == cudaSuccess)
-      e = launch_next(decay_start_kernel, dim3((D * D + 255) / 256, a.B * a.heads, a.passes), 256, 0, s, a, D);
+      e = launch_next(decay_start_kernel, dim3((a.d * a.d + 255) / 256, a.B * a.heads, a.passes), 256, 0, s, a);
     if (e != cudaSuccess) return e;
   }
-  return launch_next(decay_tc_kernel<D>, dim3(a.segs, a.B * groups, a.passes), kLaThreads, la_smem(D), s, m, a);
+  return launch_next(decay_tc_kernel<D>, dim3(a.segs, a.B * groups, a.passes), la_threads(NH), la_smem(D), s, m, a);
 }
 
 }  // namespace
+
+int la_groups(int heads, int d) { return d == 128 ? heads : (heads + 1) / 2; }
 
 int la_tc_segments(int T, int seqs, int sms) {
   const int chunks = (T + kC - 1) / kC, want = sms / seqs;
@@ -877,35 +889,37 @@ int la_tc_segments(int T, int seqs, int sms) {
   return want < 1 ? 1 : want < most ? want : most;
 }
 
-cudaError_t launch_la_tc(LaArgs& a, int d, int sms, cudaStream_t s) {
-  const int groups = (a.heads * d + kC - 1) / kC, chunks = (a.T + kC - 1) / kC;
-  const int want = la_tc_segments(a.T, a.B * groups * a.passes, sms);
+cudaError_t launch_la_tc(LaArgs& a, int sms, cudaStream_t s) {
+  const int chunks = (a.T + kC - 1) / kC;
+  const int want = la_tc_segments(a.T, a.B * la_groups(a.heads, a.d) * a.passes, sms);
   a.seg_len = (chunks + want - 1) / want * kC;
   a.segs = (a.T + a.seg_len - 1) / a.seg_len;
   const TensorMapEncoder enc = ffn_tensor_map_encoder();
   if (enc == nullptr) return cudaErrorNotSupported;
   LaMaps m;
   memset(&m, 0, sizeof m);
+  const int piece = a.d < 64 ? a.d : 64;   // channels of a piece; a 32-wide head's is half of its box
   for (int i = 0; i < a.passes; ++i) {
     const LaPass& p = a.pass[i];
     const bf16* base[4] = {p.a, p.b, p.c, p.out};
     const int64_t ld[4] = {p.lda, p.ldb, p.ldc, p.ldo};
     for (int j = 0; j < 4; ++j) {
-      const cuuint64_t dim[3] = {(cuuint64_t)a.heads * d, (cuuint64_t)a.T, (cuuint64_t)a.B};
-      const cuuint64_t str[2] = {(cuuint64_t)ld[j] * 2, a.B > 1 ? (cuuint64_t)ld[j] * 2 * a.T : (cuuint64_t)ld[j] * 2};
-      const cuuint32_t box[3] = {64u, j == 3 ? 32u : (cuuint32_t)kC, 1u}, est[3] = {1u, 1u, 1u};   // out: a warp's rows
-      if (enc(&m.m[i][j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16*>(base[j]), dim, str, box, est,
+      const cuuint64_t token = (cuuint64_t)ld[j] * 2;
+      const cuuint64_t dim[4] = {(cuuint64_t)piece, (cuuint64_t)a.heads * a.d / piece, (cuuint64_t)a.T, (cuuint64_t)a.B};
+      const cuuint64_t str[3] = {(cuuint64_t)piece * 2, token, a.B > 1 ? token * a.T : token};
+      const cuuint32_t box[4] = {64u, 1u, j == 3 ? 32u : (cuuint32_t)kC, 1u}, est[4] = {1u, 1u, 1u, 1u};   // out: a warp's rows
+      if (enc(&m.m[i][j], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<bf16*>(base[j]), dim, str, box, est,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     }
   }
-  return d == 64 ? launch_tc<64>(a, m, s) : launch_tc<128>(a, m, s);
+  return a.d == 128 ? launch_tc<128>(a, m, s) : launch_tc<64>(a, m, s);
 }
 
 cudaError_t prepare_la_tc(int d) {
-  const int n = (int)la_smem(d);
-  if (d == 64) {
+  const int n = (int)la_smem(d == 128 ? 128 : 64);
+  if (d != 128) {
     cudaError_t e = cudaFuncSetAttribute(decay_tc_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, n);
     return e == cudaSuccess ? cudaFuncSetAttribute(decay_segment_kernel<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, n) : e;
   }
