@@ -106,92 +106,57 @@ __device__ __forceinline__ void warp_arrive(unsigned long long* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Parts of w b for tokens 64 half .. + 63 of tile b, into that half of part tiles p0 and p1:
-// x = w b, part 0 = bf16(x), part 1 = bf16(x - part 0); the rest, as bf16, stays in `rest`.
-// A thread takes 4 16-byte units; f: its rows' weights.  A row without weight (no token of
-// this sequence: it may hold anything) becomes zero.
-template <int NH>
-__device__ __forceinline__ void form_half(const unsigned char* b, unsigned char* p0, unsigned char* p1, const float* w, float scale0,
-                                          float scale1, int t, int half, bool third, uint4 (&rest)[4]) {
+// Parts of w b for U x 16 tokens from row `row0` of tile b: x = w b, part 0 = bf16(x) to p0, part 1 =
+// bf16(x - part 0) to p1, both boxes of 64 channels, `box_stride` apart; the rest, as bf16, stays in
+// `rest`.  256 threads (t), a 16-byte unit of each U-th row.  A row without weight (no token of this
+// sequence: it may hold anything) becomes zero.  All loads come first: the products' operands take
+// most of the shared memory's time, and a load waits long for its turn.
+template <int NH, int U>
+__device__ __forceinline__ void form_parts(const unsigned char* b, int row0, unsigned char* p0, unsigned char* p1, uint32_t box_stride,
+                                           const float* w, float scale0, float scale1, int t, bool third, uint4 (&rest)[U]) {
   const int u = t & 15, box = u >> 3;
-  const float* wr = w + (NH == 2 ? box : 0) * kC + 64 * half;
+  const uint32_t sw = (uint32_t)(((u & 7) ^ ((t >> 4) & 7)) << 4);
+  const float* wr = w + (NH == 2 ? box : 0) * kC + row0 + (t >> 4);
   const float scale = NH == 2 && box ? scale1 : scale0;
+  const unsigned char* src = b + box * kBoxBytes + (row0 + (t >> 4)) * 128 + sw;
+  const uint32_t off = (uint32_t)box * box_stride + (uint32_t)(t >> 4) * 128 + sw;
+  uint4 raw[U];
+  float f[U];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 4) + 16 * i;
-    const uint32_t sw = (uint32_t)(((u & 7) ^ (r & 7)) << 4);
-    const uint4 raw = *reinterpret_cast<const uint4*>(b + box * kBoxBytes + (64 * half + r) * 128 + sw);
-    const float f = wr[r] * scale;
-    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t o0[4] = {0u, 0u, 0u, 0u}, o1[4] = {0u, 0u, 0u, 0u}, o2[4] = {0u, 0u, 0u, 0u};
-    if (f != 0.f) {
+  for (int i = 0; i < U; ++i) {
+    raw[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
+    f[i] = wr[16 * i];
+  }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float2 x = __fmul2_rn(make_float2(bf16_lo(in[k]), bf16_hi(in[k])), make_float2(f, f));
-        o0[k] = pack_bf16(x.x, x.y);
-        x = __fadd2_rn(x, make_float2(-bf16_lo(o0[k]), -bf16_hi(o0[k])));
-        o1[k] = pack_bf16(x.x, x.y);
-        if (third) o2[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
-      }
+  for (int i = 0; i < U; ++i) {
+    const bool on = f[i] != 0.f;
+    const float2 g = make_float2(f[i] * scale, f[i] * scale);
+    const uint32_t in[4] = {on ? raw[i].x : 0u, on ? raw[i].y : 0u, on ? raw[i].z : 0u, on ? raw[i].w : 0u};
+    uint32_t o0[4], o1[4], o2[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float2 x = __fmul2_rn(make_float2(bf16_lo(in[k]), bf16_hi(in[k])), g);
+      o0[k] = pack_bf16(x.x, x.y);
+      x = __fadd2_rn(x, make_float2(-bf16_lo(o0[k]), -bf16_hi(o0[k])));
+      o1[k] = pack_bf16(x.x, x.y);
+      if (third) o2[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
     }
-    const uint32_t off = (uint32_t)half * kHalfBytes + (uint32_t)box * (kBoxBytes / 2) + (uint32_t)r * 128 + sw;
-    *reinterpret_cast<uint4*>(p0 + off) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-    *reinterpret_cast<uint4*>(p1 + off) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+    *reinterpret_cast<uint4*>(p0 + off + i * 2048) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    *reinterpret_cast<uint4*>(p1 + off + i * 2048) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
     rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
   }
 }
-// The rest of a half into part tile p.
-__device__ __forceinline__ void put_rest(unsigned char* p, int t, int half, const uint4 (&rest)[4]) {
+// The rest into a part of its own.
+template <int U>
+__device__ __forceinline__ void put_rest(unsigned char* p, uint32_t box_stride, int t, const uint4 (&rest)[U]) {
   const int u = t & 15;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = (t >> 4) + 16 * i;
-    *reinterpret_cast<uint4*>(p + (uint32_t)half * kHalfBytes + (uint32_t)(u >> 3) * (kBoxBytes / 2) + (uint32_t)r * 128 +
-                              (uint32_t)(((u & 7) ^ (r & 7)) << 4)) = rest[i];
-  }
+  for (int i = 0; i < U; ++i)
+    *reinterpret_cast<uint4*>(p + (uint32_t)(u >> 3) * box_stride + (uint32_t)(t >> 4) * 128 + i * 2048 +
+                              (uint32_t)(((u & 7) ^ ((t >> 4) & 7)) << 4)) = rest[i];
 }
-
-// The same for a quarter (32 tokens) into a slot of the main kernel's ring: part 0, then 8 KB on
-// part 1, each two boxes of 32 x 64.  A thread takes 2 units.
+// The main kernel's ring: a slot holds two parts of 32 tokens.
 constexpr uint32_t kSlot = 16384, kSlotPart = 8192, kSlotBox = 4096;
-template <int NH>
-__device__ __forceinline__ void form_quarter(const unsigned char* b, unsigned char* slot, const float* w, int t, int quarter, bool third,
-                                             uint4 (&rest)[2]) {
-  const int u = t & 15, box = u >> 3;
-  const float* wr = w + (NH == 2 ? box : 0) * kC + 32 * quarter;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (t >> 4) + 16 * i;
-    const uint32_t sw = (uint32_t)(((u & 7) ^ (r & 7)) << 4);
-    const uint4 raw = *reinterpret_cast<const uint4*>(b + box * kBoxBytes + (32 * quarter + r) * 128 + sw);
-    const float f = wr[r];
-    const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
-    uint32_t o0[4] = {0u, 0u, 0u, 0u}, o1[4] = {0u, 0u, 0u, 0u}, o2[4] = {0u, 0u, 0u, 0u};
-    if (f != 0.f) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float2 x = __fmul2_rn(make_float2(bf16_lo(in[k]), bf16_hi(in[k])), make_float2(f, f));
-        o0[k] = pack_bf16(x.x, x.y);
-        x = __fadd2_rn(x, make_float2(-bf16_lo(o0[k]), -bf16_hi(o0[k])));
-        o1[k] = pack_bf16(x.x, x.y);
-        if (third) o2[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
-      }
-    }
-    unsigned char* at = slot + box * kSlotBox + r * 128 + sw;
-    *reinterpret_cast<uint4*>(at) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-    *reinterpret_cast<uint4*>(at + kSlotPart) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
-  }
-}
-// The rest of a quarter into one part of a slot.
-__device__ __forceinline__ void put_quarter(unsigned char* part, int t, const uint4 (&rest)[2]) {
-  const int u = t & 15;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = (t >> 4) + 16 * i;
-    *reinterpret_cast<uint4*>(part + (u >> 3) * kSlotBox + r * 128 + (uint32_t)(((u & 7) ^ (r & 7)) << 4)) = rest[i];
-  }
-}
 
 // Rows of tile c from token `from` on become zero (tokens behind a sequence's last one hold
 // anything, and zero times NaN is NaN).
@@ -588,7 +553,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       for (int st = 0; st < 4; ++st) {
         const int use = k * uses + (st >> 1);
         if (use > 0) mbar_pass(&bar[kPDone + (st & 1)], (use - 1) & 1, failed);   // the slot's last products are done
-        form_quarter<NH>(sb, ps + (st & 1) * kSlot, wt, t, st, exact, rest[st]);
+        unsigned char* slot = ps + (st & 1) * kSlot;
+        form_parts<NH>(sb, 32 * st, slot, slot + kSlotPart, kSlotBox, wt, 1.f, 1.f, t, exact, rest[st]);
         fence_async();
         warp_arrive(&bar[kParts + (st & 1)], lane);
       }
@@ -597,8 +563,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
           mbar_pass(&bar[kPDone + st], (k * uses + 1) & 1, failed);
-          put_quarter(ps + st * kSlot, t, rest[2 * st]);
-          put_quarter(ps + st * kSlot + kSlotPart, t, rest[2 * st + 1]);
+          put_rest(ps + st * kSlot, kSlotBox, t, rest[2 * st]);
+          put_rest(ps + st * kSlot + kSlotPart, kSlotBox, t, rest[2 * st + 1]);
           fence_async();
           warp_arrive(&bar[kParts + st], lane);
         }
@@ -772,8 +738,9 @@ __global__ void __launch_bounds__(kSegThreads, 1)
         if (k > 0) mbar_pass(&bar[sDone + half], (k - 1) & 1, failed);   // the half's last products are done
         if (warp >= 8) {
           uint4 rest[4];
-          form_half<NH>(b, p0, p1, wt, f0, f1, t, half, exact, rest);
-          if (exact) put_rest(p2, t, half, rest);
+          const uint32_t at = half * kHalfBytes;
+          form_parts<NH>(b, 64 * half, p0 + at, p1 + at, kBoxBytes / 2, wt, f0, f1, t, exact, rest);
+          if (exact) put_rest(p2 + at, kBoxBytes / 2, t, rest);
         } else if (half == 0 && !rev && c.cnt < kC) {
           clear_rows(cc, c.cnt, tid - 128, 128);
         }
