@@ -260,7 +260,6 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   const int group = blockIdx.y % groups, batch = blockIdx.y / groups;
   const LaPass& P = args.pass[which];
   const int rev = P.reverse, dr = args.d;   // dr: a head's channels, D or 32 of a 64-wide piece
-  const bool exact = P.zn != nullptr;   // the state leaves: a third part of w b
   if (smem_u32(sm) & 1023u) {           // the swizzled tiles' alignment
     if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
     return;
@@ -295,6 +294,9 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
   const int begin = seg * args.seg_len, end = min(begin + args.seg_len, n);
   const int chunks = end > begin ? (end - begin + kC - 1) / kC : 0;
+  // the segment that holds the last token (the first one of an empty sequence) writes the state
+  // that leaves, and has a third part of w b for it
+  const bool exact = P.zn != nullptr && seg == (n > 0 ? (n - 1) / args.seg_len : 0);
 
   if (warp == 0) {
     if (lane == 0) {
@@ -600,9 +602,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         warp_arrive(&bar[kZ], lane);
       }
     }
-    // the segment that holds the last token (the first one of an empty sequence)
-    const int last = n > 0 ? (n - 1) / args.seg_len : 0;
-    if (P.zn != nullptr && seg == last) {
+    if (exact) {
       const float f = rev && n > 0 ? exp2f(lg) : 1.f;
       float* dst = P.zn + ((int64_t)batch * args.heads + head) * dr * dr + (int64_t)br * dr + hf * Z;
 #pragma unroll 1
