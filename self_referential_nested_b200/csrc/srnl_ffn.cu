@@ -69,7 +69,7 @@ enum Epi { kPlain = 0, kGlu = 1, kGluBack = 2 };
 
 // Staging tiles per warp and ring stages: what the epilogue has in flight against how far the
 // loads run ahead, within 227 KB.
-__host__ __device__ constexpr int epi_boxes(int epi) { return epi == kGluBack ? 3 : 2; }
+__host__ __device__ constexpr int epi_boxes(int epi) { return epi == kPlain ? 2 : 3; }
 __host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + (uint32_t)(bn / 2) * kTileK * 2; }
 __host__ __device__ constexpr int ring_stages(int epi, int bn) {
   return (int)((226 * 1024 - 2048 - kEpiWarps * epi_boxes(epi) * kBox) / stage_bytes(bn));
@@ -80,7 +80,7 @@ constexpr size_t ffn_smem(int epi, int bn) {
 
 struct FfnMaps {
   CUtensorMap a[2], b[2], o[3];
-  CUtensorMap in[2];   // kGluBack: gate, up
+  CUtensorMap in[2];   // kGluBack: gate, up; kPlain: res
 };
 
 struct FfnArgs {
@@ -88,8 +88,7 @@ struct FfnArgs {
   int k0, k1;            // stages of the first and of the second operand pair
   int tiles_m, tiles_n;  // of all outputs
   int stack;             // tiles_m of the first of two stacked outputs (0: one output)
-  int save;
-  const __nv_bfloat16* res;
+  int save, res;         // kGlu: gate and up are kept; kPlain: in[0] is added
   int* err;
 };
 
@@ -124,11 +123,6 @@ __device__ __forceinline__ void tile_of(int t, const FfnArgs& a, int& tm, int& t
   const int rows = min(kBand, a.tiles_m - first), in = t - band * kBand * a.tiles_n;
   tm = first + in % rows;
   tn = in / rows;
-}
-
-// 8 bf16 of a row as fp32; zeros past the row's end.
-__device__ __forceinline__ uint4 load8_row(const __nv_bfloat16* p, bool on) {
-  return on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 template <bool AMN, bool BMN, int EPI, int ACT, int BN>
@@ -256,39 +250,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
                                           : b + lane * 128 + (((4 * c + j) ^ (lane & 7)) << 4)) =
             make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
     };
-    // hand a staging tile to the TMA; tiles wholly past an edge are not sent
-    auto send = [&](const CUtensorMap* map, unsigned char* b, int col, int row) {
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      __syncwarp();
-      if (lane == 0) {
-        if (col < args.N && row < args.M) tma_store(map, smem_u32(b), col, row);
-        bulk_commit();
-      }
-    };
-    auto reuse = [&]() {   // the tile about to be written has left
-      if (lane == 0) bulk_wait_read<1>();
-      __syncwarp();
-    };
-    // kGluBack works in pieces of 32 rows x 32 columns (2 KB, 64-byte swizzle): gate and up arrive
-    // by TMA a piece ahead, dgate and dup are written over them and leave by TMA, h beside them.
-    constexpr int kPieces = kHalf / 32, kPiece = 2048;
+    // kGluBack and kPlain work in pieces of 32 rows, of 32 columns (2 KB tiles, 64-byte swizzle) and
+    // 64.  What a piece reads, gate and up or the residual, arrives by TMA a piece ahead; the results
+    // (dgate and dup; the sum) are written over it and leave by TMA, h beside them.
+    constexpr int kCols = EPI == kGluBack ? 32 : 64, kPieces = kHalf / kCols, kPiece = kCols * 64;
+    constexpr int kBuf = (EPI == kGluBack ? 3 : 1) * kPiece;
+    const bool reads = EPI == kGluBack || (EPI == kPlain && args.res != 0);
     unsigned long long* mybar = inbar + 2 * ew;
     auto fetch = [&](int t, int c, int b) {   // lane 0: piece c of tile t into buffer b
       int tm, tn;
       tile_of(t, args, tm, tn);
-      const int row = tm * kTileM + (int)rank * 128 + quarter * 32, col = tn * BN + half * kHalf + 32 * c;
-      mbar_expect(&mybar[b], 2 * kPiece);
-      tma_load_own(smem_u32(box + b * 3 * kPiece), &maps.in[0], col, row, &mybar[b]);
-      tma_load_own(smem_u32(box + b * 3 * kPiece + kPiece), &maps.in[1], col, row, &mybar[b]);
+      const int row = tm * kTileM + (int)rank * 128 + quarter * 32, col = tn * BN + half * kHalf + kCols * c;
+      mbar_expect(&mybar[b], (EPI == kGluBack ? 2 : 1) * kPiece);
+      for (int i = 0; i < (EPI == kGluBack ? 2 : 1); ++i)
+        tma_load_own(smem_u32(box + b * kBuf + i * kPiece), &maps.in[i], col, row, &mybar[b]);
     };
     int piece = 0;   // pieces so far: buffer piece & 1, phase (piece >> 1) & 1
-    if (EPI == kGluBack && lane == 0 && pair < tiles) fetch(pair, 0, 0);
+    if (reads && lane == 0 && pair < tiles) fetch(pair, 0, 0);
+    // before a piece: the other buffer's results have left, the next piece may come
+    auto ahead = [&](int t, int c, int b) {
+      if (lane == 0) {
+        if (reads) {
+          bulk_wait_read<0>();
+          if (c + 1 < kPieces) fetch(t, c + 1, b ^ 1);
+          else if (t + pairs < tiles) fetch(t + pairs, 0, b ^ 1);
+        } else {
+          bulk_wait_read<1>();   // nothing comes: this buffer alone has to be free
+        }
+      }
+      __syncwarp();
+    };
     for (int t = pair; t < tiles; t += pairs) {
       int tm, tn;
       tile_of(t, args, tm, tn);
       const int second = args.stack != 0 && tm >= args.stack;
       const int row0 = (tm - (second ? args.stack : 0)) * kTileM + (int)rank * 128 + quarter * 32;
-      const int row = row0 + lane;
       const uint32_t acc = tmem + (uint32_t)(buf * BN) + ((uint32_t)(32 * quarter) << 16);
       mbar_pass(&tfull[buf], ph, failed);
       tmem_fence_after();
@@ -296,44 +292,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         // this half's BN / 4 hidden channels: gate in its columns, up BN / 2 further
         constexpr int kHid = BN / 4;
         const int c0 = tn * (BN / 2) + half * kHid;
-        for (int o = 0; o < (args.save ? 3 : 1); ++o) {
-          unsigned char* b = box + (turn & 1) * kBox;
-          reuse();
-#pragma unroll
-          for (int c = 0; c < kHid / 32; ++c) {
-            float g[32], u[32];
-            uint32_t w[16];
-            if (o != 2) tmem_ld32(g, acc + half * kHid + 32 * c);
-            if (o != 1) tmem_ld32(u, acc + kHalf + half * kHid + 32 * c);
-            tmem_wait_ld();
-            if (o == 0) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                float f0, f1, d;
-                activation<ACT>(g[2 * i], f0, d);
-                activation<ACT>(g[2 * i + 1], f1, d);
-                w[i] = pack_bf16(f0 * u[2 * i], f1 * u[2 * i + 1]);
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i) w[i] = o == 1 ? pack_bf16(g[2 * i], g[2 * i + 1]) : pack_bf16(u[2 * i], u[2 * i + 1]);
-            }
-            stage32(b, c, w);
-          }
-          send(&maps.o[o], b, c0, row0);
-          ++turn;
+        // h alone goes through the three staging tiles in turn; with gate and up, each has one
+        unsigned char* b = box + (args.save ? 0 : turn) * kBox;
+        if (lane == 0) {
+          if (args.save) bulk_wait_read<0>();
+          else bulk_wait_read<2>();
         }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < kHid / 32; ++c) {
+          float g[32], u[32];
+          uint32_t w[16];
+          tmem_ld32(g, acc + half * kHid + 32 * c);
+          tmem_ld32(u, acc + kHalf + half * kHid + 32 * c);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float f0, f1, d;
+            activation<ACT>(g[2 * i], f0, d);
+            activation<ACT>(g[2 * i + 1], f1, d);
+            w[i] = pack_bf16(f0 * u[2 * i], f1 * u[2 * i + 1]);
+          }
+          stage32(b, c, w);
+          if (args.save) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(g[2 * i], g[2 * i + 1]);
+            stage32(b + kBox, c, w);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack_bf16(u[2 * i], u[2 * i + 1]);
+            stage32(b + 2 * kBox, c, w);
+          }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          if (c0 < args.N && row0 < args.M)
+            for (int o = 0; o < (args.save ? 3 : 1); ++o) tma_store(&maps.o[o], smem_u32(b + o * kBox), c0, row0);
+          bulk_commit();
+        }
+        turn = turn == 2 ? 0 : turn + 1;
       } else if constexpr (EPI == kGluBack) {
 #pragma unroll 1
         for (int c = 0; c < kPieces; ++c, ++piece) {
           const int b = piece & 1, col = tn * BN + half * kHalf + 32 * c;
           unsigned char* at = box + b * 3 * kPiece;
-          if (lane == 0) {   // the other buffer's results have left: the next piece may come
-            bulk_wait_read<0>();
-            if (c + 1 < kPieces) fetch(t, c + 1, b ^ 1);
-            else if (t + pairs < tiles) fetch(t + pairs, 0, b ^ 1);
-          }
-          __syncwarp();
+          ahead(t, c, b);
           float v[32];
           tmem_ld32(v, acc + half * kHalf + 32 * c);
           mbar_pass(&mybar[b], (piece >> 1) & 1, failed);
@@ -368,35 +371,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         }
       } else {
 #pragma unroll 1
-        for (int cb = 0; cb < kHalf / 64; ++cb) {
-          const int col = tn * BN + half * kHalf + cb * 64;
-          unsigned char* b = box + (turn & 1) * kBox;
-          reuse();
+        for (int c = 0; c < kPieces; ++c, ++piece) {
+          const int b = piece & 1, col = tn * BN + half * kHalf + 64 * c;
+          unsigned char* at = box + b * kBuf;
+          ahead(t, c, b);
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int k = 0; k < 2; ++k) {
             float v[32];
             uint32_t w[16];
-            const int64_t at = (int64_t)row * args.N + col + 32 * c;
-            tmem_ld32(v, acc + half * kHalf + cb * 64 + 32 * c);
-            uint4 r[4];
-            if (args.res != nullptr)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) r[j] = load8_row(args.res + at + 8 * j, row < args.M && col + 32 * c + 8 * j < args.N);
+            tmem_ld32(v, acc + half * kHalf + 64 * c + 32 * k);
+            if (reads && k == 0) mbar_pass(&mybar[b], (piece >> 1) & 1, failed);
             tmem_wait_ld();
-            if (args.res != nullptr) {
-              const uint32_t* rw = reinterpret_cast<const uint32_t*>(r);
+            if (reads) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                v[2 * i] += bf16_lo(rw[i]);
-                v[2 * i + 1] += bf16_hi(rw[i]);
+              for (int j = 0; j < 4; ++j) {
+                const uint4 r4 = *reinterpret_cast<const uint4*>(at + lane * 128 + (((4 * k + j) ^ (lane & 7)) << 4));
+                const uint32_t r[4] = {r4.x, r4.y, r4.z, r4.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  v[8 * j + 2 * i] += bf16_lo(r[i]);
+                  v[8 * j + 2 * i + 1] += bf16_hi(r[i]);
+                }
               }
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-            stage32(b, c, w);
+            stage32(at, k, w);
           }
-          send(&maps.o[second], b, col, row0);
-          ++turn;
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (col < args.N && row0 < args.M) tma_store(&maps.o[second], smem_u32(at), col, row0);
+            bulk_commit();
+          }
         }
       }
       __syncwarp();
@@ -759,8 +766,8 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   b.tiles_m = a.tiles_m;
   bn = pick_bn(b.tiles_m, D, h->sms);
   b.tiles_n = ceil_div(D, bn);
-  b.res = static_cast<const bf16*>(res); b.err = h->dev_err;
-  ok = ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, bn / 2) && ffn_map(&m.o[0], y, D, M, 32);
+  b.res = res != nullptr; b.err = h->dev_err;
+  ok = (res == nullptr || ffn_map(&m.in[0], res, D, M, 32)) && ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, bn / 2) && ffn_map(&m.o[0], y, D, M, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
   e = launch_product<false, false, kPlain, 0>(bn, m, b, h->sms, s);
   return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward output launch");
