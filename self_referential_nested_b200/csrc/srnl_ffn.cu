@@ -241,8 +241,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     int buf = 0, turn = 0;
     uint32_t ph = 0u;
     // bf16 pairs of 32 columns into a staging tile's columns 32 c .. : 16-byte units, swizzled as
-    // its map has it (rows of 128 bytes, or of 64 where a half has only 32 columns)
-    constexpr bool kNarrow = EPI == kGlu && BN == 128;
+    // its map has it (rows of 128 bytes, or of 64 in the 32-column tiles)
+    constexpr bool kNarrow = EPI == kGlu;
     auto stage32 = [&](unsigned char* b, int c, const uint32_t (&w)[16]) {
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -290,17 +290,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       tmem_fence_after();
       if constexpr (EPI == kGlu) {
         // this half's BN / 4 hidden channels: gate in its columns, up BN / 2 further
-        constexpr int kHid = BN / 4;
-        const int c0 = tn * (BN / 2) + half * kHid;
-        // h alone goes through the three staging tiles in turn; with gate and up, each has one
-        unsigned char* b = box + (args.save ? 0 : turn) * kBox;
-        if (lane == 0) {
-          if (args.save) bulk_wait_read<0>();
-          else bulk_wait_read<2>();
-        }
-        __syncwarp();
+        constexpr int kHid = BN / 4, kTile32 = 2048;
+        // 32 channels at a time through 2 KB tiles: h alone takes six of them in turn, h, gate and
+        // up together one of two sets of three
 #pragma unroll
         for (int c = 0; c < kHid / 32; ++c) {
+          const int col = tn * (BN / 2) + half * kHid + 32 * c;
+          unsigned char* b = box + turn * kTile32;
+          if (lane == 0) {
+            if (args.save) bulk_wait_read<1>();
+            else bulk_wait_read<5>();
+          }
+          __syncwarp();
           float g[32], u[32];
           uint32_t w[16];
           tmem_ld32(g, acc + half * kHid + 32 * c);
@@ -313,24 +314,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
             activation<ACT>(g[2 * i + 1], f1, d);
             w[i] = pack_bf16(f0 * u[2 * i], f1 * u[2 * i + 1]);
           }
-          stage32(b, c, w);
+          stage32(b, 0, w);
           if (args.save) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16(g[2 * i], g[2 * i + 1]);
-            stage32(b + kBox, c, w);
+            stage32(b + kTile32, 0, w);
 #pragma unroll
             for (int i = 0; i < 16; ++i) w[i] = pack_bf16(u[2 * i], u[2 * i + 1]);
-            stage32(b + 2 * kBox, c, w);
+            stage32(b + 2 * kTile32, 0, w);
           }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (col < args.N && row0 < args.M)
+              for (int o = 0; o < (args.save ? 3 : 1); ++o) tma_store(&maps.o[o], smem_u32(b + o * kTile32), col, row0);
+            bulk_commit();
+          }
+          turn += args.save ? 3 : 1;
+          if (turn == 6) turn = 0;
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          if (c0 < args.N && row0 < args.M)
-            for (int o = 0; o < (args.save ? 3 : 1); ++o) tma_store(&maps.o[o], smem_u32(b + o * kBox), c0, row0);
-          bulk_commit();
-        }
-        turn = turn == 2 ? 0 : turn + 1;
       } else if constexpr (EPI == kGluBack) {
 #pragma unroll 1
         for (int c = 0; c < kPieces; ++c, ++piece) {
@@ -753,10 +755,9 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   int bn = pick_bn(a.tiles_m, 2 * F, h->sms);
   a.tiles_n = ceil_div(F, bn / 2);
   a.save = gate != nullptr; a.err = h->dev_err;
-  const int cols = bn / 4;   // of a staging tile
   bool ok = ffn_map(&m.a[0], x, D, M, 128) && ffn_map(&m.b[0], p->W_gate, D, F, bn / 2) &&
-            ffn_map(&m.b[1], p->W_up, D, F, bn / 2) && ffn_map(&m.o[0], h->hid, F, M, 32, cols) &&
-            (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32, cols) && ffn_map(&m.o[2], up, F, M, 32, cols)));
+            ffn_map(&m.b[1], p->W_up, D, F, bn / 2) && ffn_map(&m.o[0], h->hid, F, M, 32, 32) &&
+            (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32, 32) && ffn_map(&m.o[2], up, F, M, 32, 32)));
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
   cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, false, kGlu, SRNL_ACT_SILU>(bn, m, a, h->sms, s)
                                                 : launch_product<false, false, kGlu, SRNL_ACT_GELU>(bn, m, a, h->sms, s);
