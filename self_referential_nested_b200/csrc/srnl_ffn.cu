@@ -10,8 +10,9 @@
 //   kGlu      both projections of a 256-token x 128-channel tile at once: Wg's rows are the first
 //             half of the product's N and Wu's the second, so act(gate) * up is formed from two
 //             accumulators of the same thread, and neither projection is written unless asked
-//   kPlain    (+ res), to bf16: y, dx (its K runs over dgate Wg, then dup Wu) and the weights'
-//             gradients (both operands read as they lie, tokens along K)
+//   kPlain    (+ res), to bf16: y
+//   kGrad     the same for dx (its K runs over dgate Wg, then dup Wu) and the weights' gradients (both
+//             operands read as they lie, tokens along K), all in one launch
 //   kGluBack  dh stays in TMEM: the epilogue reads gate and up and writes dgate, dup and h
 //
 // The kernel is persistent; a pair of CTAs (cta_group::2) makes 256 x BN tiles.  In each CTA one
@@ -65,11 +66,11 @@ constexpr int kFfnThreads = 32 * (4 + kEpiWarps);
 constexpr int kBox = 4096;         // a warp's staging tile: 32 rows x 64 bf16
 constexpr uint32_t kABytes = 128 * kTileK * 2;
 
-enum Epi { kPlain = 0, kGlu = 1, kGluBack = 2 };
+enum Epi { kPlain = 0, kGlu = 1, kGluBack = 2, kGrad = 3 };
 
 // Staging tiles per warp and ring stages: what the epilogue has in flight against how far the
 // loads run ahead, within 227 KB.
-__host__ __device__ constexpr int epi_boxes(int epi) { return epi == kPlain ? 2 : 3; }
+__host__ __device__ constexpr int epi_boxes(int epi) { return epi == kPlain || epi == kGrad ? 2 : 3; }
 __host__ __device__ constexpr uint32_t stage_bytes(int bn) { return kABytes + (uint32_t)(bn / 2) * kTileK * 2; }
 __host__ __device__ constexpr int ring_stages(int epi, int bn) {
   return (int)((226 * 1024 - 2048 - kEpiWarps * epi_boxes(epi) * kBox) / stage_bytes(bn));
@@ -79,15 +80,22 @@ constexpr size_t ffn_smem(int epi, int bn) {
 }
 
 struct FfnMaps {
-  CUtensorMap a[2], b[2], o[3];
+  CUtensorMap a[5], b[4], o[4];
   CUtensorMap in[2];   // kGluBack: gate, up; kPlain: res
 };
 
-struct FfnArgs {
-  int M, N;              // of the output (of one of two stacked outputs)
+// One product of a launch: its output and operands, by their places in the maps.  Where k1 is not
+// zero the sum goes on over the next two operands; a_mn: A's rows run along K in memory.
+struct FfnProduct {
+  int first;             // tile it begins with
+  int M, N, tiles_m, tiles_n;
   int k0, k1;            // stages of the first and of the second operand pair
-  int tiles_m, tiles_n;  // of all outputs
-  int stack;             // tiles_m of the first of two stacked outputs (0: one output)
+  int a, b, o, a_mn;
+};
+
+struct FfnArgs {
+  FfnProduct product[4];
+  int products, tiles;
   int save, res;         // kGlu: gate and up are kept; kPlain: in[0] is added
   int* err;
 };
@@ -115,19 +123,29 @@ __device__ __forceinline__ void activation(float v, float& f, float& df) {
   }
 }
 
-// Tiles in bands of 8 along M, M fastest within a band: the pairs that run together share their
-// operands' rows in L2.
-__device__ __forceinline__ void tile_of(int t, const FfnArgs& a, int& tm, int& tn) {
+// A launch's tiles product by product; a product's in bands of 8 along M, M fastest within a
+// band: the pairs that run together share their operands' rows in L2.
+template <int EPI>
+__device__ __forceinline__ const FfnProduct& tile_of(int t, const FfnArgs& args, int& tm, int& tn) {
   constexpr int kBand = 8;
-  const int band = t / (kBand * a.tiles_n), first = band * kBand;
-  const int rows = min(kBand, a.tiles_m - first), in = t - band * kBand * a.tiles_n;
+  int i = 0;
+  if (EPI == kGrad)
+    while (i + 1 < args.products && t >= args.product[i + 1].first) ++i;
+  const FfnProduct& p = args.product[i];
+  t -= p.first;
+  const int band = t / (kBand * p.tiles_n), first = band * kBand;
+  const int rows = min(kBand, p.tiles_m - first), in = t - band * kBand * p.tiles_n;
   tm = first + in % rows;
   tn = in / rows;
+  return p;
 }
 
-template <bool AMN, bool BMN, int EPI, int ACT, int BN>
+// B lies K-major forward (weights' rows along K) and MN-major backward.  A lies K-major but for the
+// weights' gradients, which share a launch (kGrad) with the input's.
+template <int EPI, int ACT, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
-    ffn_product_kernel(const __grid_constant__ FfnMaps maps, const FfnArgs args) {
+    ffn_product_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs args) {
+  constexpr bool BMN = EPI == kGluBack || EPI == kGrad;
   constexpr int S = ring_stages(EPI, BN);
   constexpr uint32_t kStage = stage_bytes(BN);
   constexpr int kBRows = BN / 2;   // of B per CTA
@@ -144,7 +162,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = args.tiles_m * args.tiles_n, ktot = args.k0 + args.k1;
+  const int tiles = args.tiles;
 
   if (warp == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
@@ -179,19 +197,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       const uint32_t lead = map_rank(smem_u32(full), 0), ring = smem_u32(smem);
       for (int t = pair; t < tiles; t += pairs) {
         int tm, tn;
-        tile_of(t, args, tm, tn);
-        const int second = args.stack != 0 && tm >= args.stack;
-        const int m0 = (tm - (second ? args.stack : 0)) * kTileM + (int)rank * 128;
+        const FfnProduct& P = tile_of<EPI>(t, args, tm, tn);
+        const int k0 = P.k0, ktot = P.k0 + P.k1;
+        const bool a_mn = EPI == kGrad && P.a_mn;
+        const int m0 = tm * kTileM + (int)rank * 128;
         const int n0 = EPI == kGlu ? tn * (BN / 2) : tn * BN + (int)rank * kBRows;
         for (int it = 0; it < ktot; ++it) {
-          const int two = it >= args.k0;
-          const int k = (it - (two ? args.k0 : 0)) * kTileK;
-          const CUtensorMap* am = &maps.a[args.stack != 0 ? second : two];
-          const CUtensorMap* bm = &maps.b[EPI == kGlu ? (int)rank : two];
+          const int two = it >= k0;
+          const int k = (it - (two ? k0 : 0)) * kTileK;
+          const CUtensorMap* am = &maps.a[P.a + two];
+          const CUtensorMap* bm = &maps.b[EPI == kGlu ? (int)rank : P.b + two];
           if (!mbar_pass(&empty[s], ph, failed)) break;
           if (rank == 0) mbar_expect(&full[s], 2 * kStage);
           const uint32_t bar = lead + (uint32_t)s * 8, as = ring + s * kStage, bs = as + kABytes;
-          if constexpr (AMN) {
+          if (a_mn) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) tma_load_pair(as + i * 8192, am, m0 + 64 * i, k, bar);
           } else {
@@ -209,13 +228,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
-      constexpr uint32_t idesc = idesc_mn(kTileM, BN, AMN, BMN);
       int s = 0, buf = 0;
       uint32_t ph = 0u, tph = 1u;   // the accumulators start empty
       const uint32_t ring = smem_u32(smem);
-      const uint64_t ad0 = AMN ? desc_mn_major(ring, 8192) : desc_k_major(ring);
       const uint64_t bd0 = BMN ? desc_mn_major(ring + kABytes, 8192) : desc_k_major(ring + kABytes);
       for (int t = pair; t < tiles; t += pairs) {
+        int tm, tn;
+        const FfnProduct& P = tile_of<EPI>(t, args, tm, tn);
+        const int ktot = P.k0 + P.k1;
+        const bool a_mn = EPI == kGrad && P.a_mn;
+        const uint32_t idesc = a_mn ? idesc_mn(kTileM, BN, true, BMN) : idesc_mn(kTileM, BN, false, BMN);
+        const uint64_t ad0 = a_mn ? desc_mn_major(ring, 8192) : desc_k_major(ring), astep = a_mn ? 128 : 2;
         mbar_pass(&tempty[buf], tph, failed);
         tmem_fence_after();
         const uint32_t acc = tmem + (uint32_t)(buf * BN);
@@ -225,7 +248,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           const uint64_t ad = ad0 + (uint64_t)(s * (kStage >> 4)), bd = bd0 + (uint64_t)(s * (kStage >> 4));
 #pragma unroll
           for (int k = 0; k < kTileK / 16; ++k)
-            mma_pair(acc, ad + (uint64_t)(k * (AMN ? 2048 : 32) >> 4), bd + (uint64_t)(k * (BMN ? 2048 : 32) >> 4),
+            mma_pair(acc, ad + k * astep, bd + (uint64_t)(k * (BMN ? 2048 : 32) >> 4),
                      idesc, it > 0 || k > 0);
           mma_commit_pair(&empty[s]);
           if (++s == S) { s = 0; ph ^= 1u; }
@@ -259,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     unsigned long long* mybar = inbar + 2 * ew;
     auto fetch = [&](int t, int c, int b) {   // lane 0: piece c of tile t into buffer b
       int tm, tn;
-      tile_of(t, args, tm, tn);
+      tile_of<EPI>(t, args, tm, tn);
       const int row = tm * kTileM + (int)rank * 128 + quarter * 32, col = tn * BN + half * kHalf + kCols * c;
       mbar_expect(&mybar[b], (EPI == kGluBack ? 2 : 1) * kPiece);
       for (int i = 0; i < (EPI == kGluBack ? 2 : 1); ++i)
@@ -282,9 +305,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     };
     for (int t = pair; t < tiles; t += pairs) {
       int tm, tn;
-      tile_of(t, args, tm, tn);
-      const int second = args.stack != 0 && tm >= args.stack;
-      const int row0 = (tm - (second ? args.stack : 0)) * kTileM + (int)rank * 128 + quarter * 32;
+      const FfnProduct& P = tile_of<EPI>(t, args, tm, tn);
+      const int row0 = tm * kTileM + (int)rank * 128 + quarter * 32;
       const uint32_t acc = tmem + (uint32_t)(buf * BN) + ((uint32_t)(32 * quarter) << 16);
       mbar_pass(&tfull[buf], ph, failed);
       tmem_fence_after();
@@ -326,7 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            if (col < args.N && row0 < args.M)
+            if (col < P.N && row0 < P.M)
               for (int o = 0; o < (args.save ? 3 : 1); ++o) tma_store(&maps.o[o], smem_u32(b + o * kTile32), col, row0);
             bulk_commit();
           }
@@ -366,7 +388,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            if (col < args.N && row0 < args.M)
+            if (col < P.N && row0 < P.M)
               for (int o = 0; o < 3; ++o) tma_store(&maps.o[o], smem_u32(at + o * kPiece), col, row0);
             bulk_commit();
           }
@@ -403,7 +425,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            if (col < args.N && row0 < args.M) tma_store(&maps.o[second], smem_u32(at), col, row0);
+            if (col < P.N && row0 < P.M) tma_store(&maps.o[P.o], smem_u32(at), col, row0);
             bulk_commit();
           }
         }
@@ -559,26 +581,46 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
   return cudaLaunchKernelEx(&lc, kernel, static_cast<P>(args)...);
 }
 
-template <bool AMN, bool BMN, int EPI, int ACT, int BN>
-cudaError_t launch_product(const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
-  const int64_t tiles = (int64_t)a.tiles_m * a.tiles_n;
-  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
-  return launch_after(ffn_product_kernel<AMN, BMN, EPI, ACT, BN>, dim3(2 * pairs), kFfnThreads, ffn_smem(EPI, BN), s, maps, a);
-}
-
-template <bool AMN, bool BMN, int EPI, int ACT>
+template <int EPI, int ACT>
 cudaError_t launch_product(int bn, const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
-  return bn == 256 ? launch_product<AMN, BMN, EPI, ACT, 256>(maps, a, sms, s) : launch_product<AMN, BMN, EPI, ACT, 128>(maps, a, sms, s);
+  const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
+  return bn == 256 ? launch_after(ffn_product_kernel<EPI, ACT, 256>, dim3(2 * pairs), kFfnThreads, ffn_smem(EPI, 256), s, maps, a)
+                   : launch_after(ffn_product_kernel<EPI, ACT, 128>, dim3(2 * pairs), kFfnThreads, ffn_smem(EPI, 128), s, maps, a);
 }
 
-template <bool AMN, bool BMN, int EPI, int ACT>
+template <int EPI, int ACT>
 cudaError_t prepare_product() {
-  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, ACT, 256>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 256));
+  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 256));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(ffn_product_kernel<AMN, BMN, EPI, ACT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)ffn_smem(EPI, 128));
+    e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 128));
   return e;
+}
+
+// One more product of a launch, its tiles after those before it.  cols: columns of its tiles.
+void add_product(FfnArgs& a, int64_t M, int64_t N, int cols, int64_t K, bool two, int am, int bm, int om, bool a_mn) {
+  FfnProduct& p = a.product[a.products++];
+  p.first = a.tiles;
+  p.M = (int)M; p.N = (int)N;
+  p.tiles_m = ceil_div(M, kTileM); p.tiles_n = ceil_div(N, cols);
+  p.k0 = ceil_div(K, kTileK); p.k1 = two ? p.k0 : 0;
+  p.a = am; p.b = bm; p.o = om; p.a_mn = a_mn;
+  a.tiles += p.tiles_m * p.tiles_n;
+}
+
+// Most stages that a pair of CTAs has in a launch.
+int64_t longest_pair(const FfnArgs& a, int pairs) {
+  if (a.tiles <= pairs) {
+    int k = 0;
+    for (int i = 0; i < a.products; ++i) k = a.product[i].k0 + a.product[i].k1 > k ? a.product[i].k0 + a.product[i].k1 : k;
+    return k;
+  }
+  int64_t all = 0;   // tiles go to the pairs in turn: the first pair has the most of each product
+  for (int i = 0; i < a.products; ++i) {
+    const FfnProduct& p = a.product[i];
+    const int n = p.tiles_m * p.tiles_n, after = (p.first + n + pairs - 1) / pairs, before = (p.first + pairs - 1) / pairs;
+    all += (int64_t)(after - before) * (p.k0 + p.k1);
+  }
+  return all;
 }
 
 template <bool GLU, int ACT>
@@ -591,15 +633,14 @@ cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, 
   return launch_after(ffn_few_rows_kernel<GLU, ACT, 4>, grid, t, 0, s, x, W, W2, res, out, gate, up, rows, N, K);
 }
 
-// Columns of a pair's tile for a product of tiles_m x n: 256, or 128 where that fills the SMs
-// better.  A 128-column tile reads as much of A for half the work and takes about 0.8 of a
-// 256-column one (8192 x 2048 x 11264: 409 us in 7 waves of them, 259 us in 4; 1531 x 1384 x 520
-// in one wave each: 16 us against 20).
-int pick_bn(int64_t tiles_m, int64_t n, int sms) {
-  const int64_t pairs = sms / 2;
-  const int64_t w256 = (tiles_m * ((n + 255) / 256) + pairs - 1) / pairs, w128 = (tiles_m * ((n + 127) / 128) + pairs - 1) / pairs;
-  return 10 * w128 < 12 * w256 ? 128 : 256;
+// Columns of the pairs' tiles: 256, or 128 where that fills the SMs better (`wide`, `narrow`: the
+// launch either way).  A 128-column tile reads as much of A for half the work and takes about 0.8
+// of a 256-column one (8192 x 2048 x 11264: 409 us in 7 rounds of them, 259 us in 4; 1531 x 1384 x
+// 520 in one round each: 16 us against 20).
+int pick_bn(const FfnArgs& wide, const FfnArgs& narrow, int sms) {
+  return 10 * longest_pair(narrow, sms / 2) < 12 * longest_pair(wide, sms / 2) ? 128 : 256;
 }
+
 
 }  // namespace
 }  // namespace srnl
@@ -701,13 +742,12 @@ srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg) {
   if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dup, bytes);
   if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
-  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_SILU>();
-  if (e == cudaSuccess) e = prepare_product<false, false, kGlu, SRNL_ACT_GELU>();
-  if (e == cudaSuccess) e = prepare_product<false, false, kPlain, 0>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_SILU>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kGluBack, SRNL_ACT_GELU>();
-  if (e == cudaSuccess) e = prepare_product<false, true, kPlain, 0>();
-  if (e == cudaSuccess) e = prepare_product<true, true, kPlain, 0>();
+  if (e == cudaSuccess) e = prepare_product<kGlu, SRNL_ACT_SILU>();
+  if (e == cudaSuccess) e = prepare_product<kGlu, SRNL_ACT_GELU>();
+  if (e == cudaSuccess) e = prepare_product<kPlain, 0>();
+  if (e == cudaSuccess) e = prepare_product<kGluBack, SRNL_ACT_SILU>();
+  if (e == cudaSuccess) e = prepare_product<kGluBack, SRNL_ACT_GELU>();
+  if (e == cudaSuccess) e = prepare_product<kGrad, 0>();
   if (e == cudaSuccess && ffn_tensor_map_encoder() == nullptr) e = cudaErrorNotSupported;
   if (e != cudaSuccess) {
     const srnl_status st = ffn_cuda_fail(nullptr, e, "feed-forward create");
@@ -749,28 +789,31 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   }
   FfnMaps m;
   memset(&m, 0, sizeof m);
-  FfnArgs a{};
-  a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
-  a.tiles_m = ceil_div(M, kTileM);
-  int bn = pick_bn(a.tiles_m, 2 * F, h->sms);
-  a.tiles_n = ceil_div(F, bn / 2);
-  a.save = gate != nullptr; a.err = h->dev_err;
+  FfnArgs a[2] = {};   // tiles of 256 and of 128 columns
+  for (int i = 0; i < 2; ++i) {
+    add_product(a[i], M, F, 128 >> i, D, false, 0, 0, 0, false);
+    a[i].save = gate != nullptr;
+    a[i].err = h->dev_err;
+  }
+  int bn = pick_bn(a[0], a[1], h->sms);
   bool ok = ffn_map(&m.a[0], x, D, M, 128) && ffn_map(&m.b[0], p->W_gate, D, F, bn / 2) &&
             ffn_map(&m.b[1], p->W_up, D, F, bn / 2) && ffn_map(&m.o[0], h->hid, F, M, 32, 32) &&
             (gate == nullptr || (ffn_map(&m.o[1], gate, F, M, 32, 32) && ffn_map(&m.o[2], up, F, M, 32, 32)));
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, false, kGlu, SRNL_ACT_SILU>(bn, m, a, h->sms, s)
-                                                : launch_product<false, false, kGlu, SRNL_ACT_GELU>(bn, m, a, h->sms, s);
+  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<kGlu, SRNL_ACT_SILU>(bn, m, a[bn == 128], h->sms, s)
+                                                : launch_product<kGlu, SRNL_ACT_GELU>(bn, m, a[bn == 128], h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward projections launch");
-  FfnArgs b{};
-  b.M = rows; b.N = (int)D; b.k0 = ceil_div(F, kTileK);
-  b.tiles_m = a.tiles_m;
-  bn = pick_bn(b.tiles_m, D, h->sms);
-  b.tiles_n = ceil_div(D, bn);
-  b.res = res != nullptr; b.err = h->dev_err;
-  ok = (res == nullptr || ffn_map(&m.in[0], res, D, M, 32)) && ffn_map(&m.a[0], h->hid, F, M, 128) && ffn_map(&m.b[0], p->W_down, F, D, bn / 2) && ffn_map(&m.o[0], y, D, M, 32);
+  FfnArgs b[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    add_product(b[i], M, D, 256 >> i, F, false, 0, 0, 0, false);
+    b[i].res = res != nullptr;
+    b[i].err = h->dev_err;
+  }
+  bn = pick_bn(b[0], b[1], h->sms);
+  ok = (res == nullptr || ffn_map(&m.in[0], res, D, M, 32)) && ffn_map(&m.a[0], h->hid, F, M, 128) &&
+       ffn_map(&m.b[0], p->W_down, F, D, bn / 2) && ffn_map(&m.o[0], y, D, M, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  e = launch_product<false, false, kPlain, 0>(bn, m, b, h->sms, s);
+  e = launch_product<kPlain, 0>(bn, m, b[bn == 128], h->sms, s);
   return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward output launch");
 }
 
@@ -809,59 +852,39 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
   FfnMaps m;
   memset(&m, 0, sizeof m);
   // dgate, dup and h from dh = dy Wd
-  FfnArgs a{};
-  a.M = rows; a.N = (int)F; a.k0 = ceil_div(D, kTileK);
-  a.tiles_m = ceil_div(M, kTileM);
-  int bn = pick_bn(a.tiles_m, F, h->sms);
-  a.tiles_n = ceil_div(F, bn);
-  a.err = h->dev_err;
+  FfnArgs a[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    add_product(a[i], M, F, 256 >> i, D, false, 0, 0, 0, false);
+    a[i].err = h->dev_err;
+  }
+  int bn = pick_bn(a[0], a[1], h->sms);
   bool ok = ffn_map(&m.a[0], dy, D, M, 128) && ffn_map(&m.b[0], w.W_down, F, D, 64) &&
             ffn_map(&m.o[0], h->dgate, F, M, 32, 32) && ffn_map(&m.o[1], h->dup, F, M, 32, 32) &&
             ffn_map(&m.o[2], h->hid, F, M, 32, 32) && ffn_map(&m.in[0], gate, F, M, 32, 32) && ffn_map(&m.in[1], up, F, M, 32, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<false, true, kGluBack, SRNL_ACT_SILU>(bn, m, a, h->sms, s)
-                                                : launch_product<false, true, kGluBack, SRNL_ACT_GELU>(bn, m, a, h->sms, s);
+  cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<kGluBack, SRNL_ACT_SILU>(bn, m, a[bn == 128], h->sms, s)
+                                                : launch_product<kGluBack, SRNL_ACT_GELU>(bn, m, a[bn == 128], h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward backward launch");
-  if (dx != nullptr) {
-    FfnArgs b{};
-    b.M = rows; b.N = (int)D; b.k0 = b.k1 = ceil_div(F, kTileK);
-    b.tiles_m = a.tiles_m;
-    bn = pick_bn(b.tiles_m, D, h->sms);
-    b.tiles_n = ceil_div(D, bn); b.err = h->dev_err;
-    ok = ffn_map(&m.a[0], h->dgate, F, M, 128) && ffn_map(&m.a[1], h->dup, F, M, 128) &&
-         ffn_map(&m.b[0], w.W_gate, D, F, 64) && ffn_map(&m.b[1], w.W_up, D, F, 64) && ffn_map(&m.o[0], dx, D, M, 32);
-    if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<false, true, kPlain, 0>(bn, m, b, h->sms, s);
-    if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward input gradient launch");
+  // what is asked for of dx and the weights' gradients in one launch: the longest sums first, the
+  // others' tiles fill up the SMs behind them
+  FfnArgs b[2] = {};
+  for (int i = 0; i < 2; ++i) {
+    const int cols = 256 >> i;
+    if (dx != nullptr) add_product(b[i], M, D, cols, F, true, 0, 0, 0, false);
+    if (g.W_gate != nullptr) add_product(b[i], F, D, cols, M, false, 2, 2, 1, true);
+    if (g.W_up != nullptr) add_product(b[i], F, D, cols, M, false, 3, 2, 2, true);
+    if (g.W_down != nullptr) add_product(b[i], D, F, cols, M, false, 4, 3, 3, true);
+    b[i].err = h->dev_err;
   }
-  if (g.W_gate != nullptr || g.W_up != nullptr) {
-    // one launch for both: their tiles stacked along M
-    const bool both = g.W_gate != nullptr && g.W_up != nullptr;
-    const void* d0 = g.W_gate != nullptr ? h->dgate : h->dup;
-    void* o0 = g.W_gate != nullptr ? g.W_gate : g.W_up;
-    FfnArgs b{};
-    b.M = (int)F; b.N = (int)D; b.k0 = ceil_div(M, kTileK);
-    b.stack = both ? ceil_div(F, kTileM) : 0;
-    b.tiles_m = ceil_div(F, kTileM) * (both ? 2 : 1);
-    bn = pick_bn(b.tiles_m, D, h->sms);
-    b.tiles_n = ceil_div(D, bn); b.err = h->dev_err;
-    ok = ffn_map(&m.a[0], d0, F, M, 64) && ffn_map(&m.b[0], x, D, M, 64) && ffn_map(&m.o[0], o0, D, F, 32) &&
-         (!both || (ffn_map(&m.a[1], h->dup, F, M, 64) && ffn_map(&m.o[1], g.W_up, D, F, 32)));
-    if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<true, true, kPlain, 0>(bn, m, b, h->sms, s);
-    if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
-  }
-  if (g.W_down != nullptr) {
-    FfnArgs b{};
-    b.M = (int)D; b.N = (int)F; b.k0 = ceil_div(M, kTileK);
-    b.tiles_m = ceil_div(D, kTileM);
-    bn = pick_bn(b.tiles_m, F, h->sms);
-    b.tiles_n = ceil_div(F, bn); b.err = h->dev_err;
-    ok = ffn_map(&m.a[0], dy, D, M, 64) && ffn_map(&m.b[0], h->hid, F, M, 64) && ffn_map(&m.o[0], g.W_down, F, D, 32);
-    if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-    e = launch_product<true, true, kPlain, 0>(bn, m, b, h->sms, s);
-    if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward weight gradient launch");
-  }
+  bn = pick_bn(b[0], b[1], h->sms);
+  ok = ffn_map(&m.a[0], h->dgate, F, M, 128) && ffn_map(&m.a[1], h->dup, F, M, 128) && ffn_map(&m.a[2], h->dgate, F, M, 64) &&
+       ffn_map(&m.a[3], h->dup, F, M, 64) && ffn_map(&m.a[4], dy, D, M, 64) && ffn_map(&m.b[0], w.W_gate, D, F, 64) &&
+       ffn_map(&m.b[1], w.W_up, D, F, 64) && ffn_map(&m.b[2], x, D, M, 64) && ffn_map(&m.b[3], h->hid, F, M, 64) &&
+       (dx == nullptr || ffn_map(&m.o[0], dx, D, M, 32)) && (g.W_gate == nullptr || ffn_map(&m.o[1], g.W_gate, D, F, 32)) &&
+       (g.W_up == nullptr || ffn_map(&m.o[2], g.W_up, D, F, 32)) && (g.W_down == nullptr || ffn_map(&m.o[3], g.W_down, F, D, 32));
+  if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
+  e = launch_product<kGrad, 0>(bn, m, b[bn == 128], h->sms, s);
+  if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward gradients launch");
   return SRNL_OK;
 }
 
