@@ -42,9 +42,8 @@ constexpr int kC = 128;                  // tokens per chunk, and channels per C
 constexpr uint32_t kBoxBytes = kC * 128; // 128 tokens x 64 channels
 constexpr uint32_t kTile = 2 * kBoxBytes;
 __host__ __device__ constexpr int la_threads(int nh) { return 128 * (3 + nh); }   // loads and products, 4 row warps a head, 8 state warps
-constexpr int kSegThreads = 512;         // of the segments' kernel
+constexpr int kSegFormers = 16, kSegThreads = 128 + 32 * kSegFormers;   // of the segments' kernel
 constexpr int kStateThreads = 256;
-constexpr uint32_t kHalfBytes = kTile / 2;   // 64 tokens of a part of w b: two boxes of 64 x 64
 
 struct LaMaps {
   CUtensorMap m[3][4];   // [pass][a, b, c, out]: (channel of 64 or fewer, 64-channel piece, token, batch)
@@ -144,6 +143,57 @@ __device__ __forceinline__ void form_parts(const unsigned char* b, int row0, uns
     *reinterpret_cast<uint4*>(p0 + off + i * 2048) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
     *reinterpret_cast<uint4*>(p1 + off + i * 2048) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
     rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+  }
+}
+// The parts of w b as the left operand in TMEM: for 32 channels (lanes 32 q on) and 32 N tokens from
+// `token` of tile b, part p to columns ta + 64 p + token / 2 on.  ldmatrix transposes as it reads: a
+// register holds two tokens of a channel, in the places tcgen05.st's 16-lane shape wants them.
+__device__ __forceinline__ void ldmatrix_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_16lanes(uint32_t addr, const uint32_t (&v)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void form_tmem(uint32_t b, uint32_t ta, int q, int token, const float* w, float scale, bool third, int lane) {
+#pragma unroll 1
+  for (int k = 0; k < N; ++k) {
+    const int t0 = token + 32 * k;
+    uint32_t raw[2][2][4];
+    float2 f[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // 16 channels
+      const int unit = 2 * h + 4 * (q & 1) + ((lane >> 3) & 1);
+      const uint32_t at = b + (q >> 1) * kBoxBytes + (uint32_t)(t0 + (lane >> 4) * 8 + (lane & 7)) * 128 + ((unit ^ (lane & 7)) << 4);
+      ldmatrix_t(raw[h][0], at);
+      ldmatrix_t(raw[h][1], at + 16 * 128);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = *reinterpret_cast<const float2*>(w + t0 + 8 * i + 2 * (lane & 3));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t o[3][8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 g = f[i >> 1];
+        const uint32_t in = raw[h][i >> 2][i & 3];
+        float2 x = make_float2(g.x != 0.f ? bf16_lo(in) : 0.f, g.y != 0.f ? bf16_hi(in) : 0.f);
+        x = __fmul2_rn(x, make_float2(g.x * scale, g.y * scale));
+        o[0][i] = pack_bf16(x.x, x.y);
+        x = __fadd2_rn(x, make_float2(-bf16_lo(o[0][i]), -bf16_hi(o[0][i])));
+        o[1][i] = pack_bf16(x.x, x.y);
+        if (third) o[2][i] = pack_bf16(x.x - bf16_lo(o[1][i]), x.y - bf16_hi(o[1][i]));
+      }
+      const uint32_t at = ta + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(t0 >> 1);
+      tmem_st_16lanes(at, o[0]);
+      tmem_st_16lanes(at + 64, o[1]);
+      if (third) tmem_st_16lanes(at + 128, o[2]);
+    }
   }
 }
 // The rest into a part of its own.
@@ -634,15 +684,15 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
 // ------------------------------------------------------------------ the segments' states
 // What a segment adds to the state, from zero: sum_j g^(tokens behind j) b_j c_j^T.  The weights
 // reach to the segment's end, so the products of all its chunks add up in TMEM.
-enum { sFull = 0, sFree = 2, sParts = 4, sDone = 6, sBars = 8 };   // parts and done: one for each half
+constexpr int kSegStages = 3;
+enum { sFull = 0, sFree = kSegStages, sParts = 2 * kSegStages, sDone = sParts + 2, sBars = sDone + 2 };   // parts and done: one for each buffer
 
 template <int D>
 __global__ void __launch_bounds__(kSegThreads, 1)
     decay_segment_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
   constexpr int NH = kC / D;
   extern __shared__ __align__(1024) unsigned char sm[];
-  unsigned char *ring = sm, *p0 = sm + 4 * kTile, *p1 = p0 + kTile, *p2 = p1 + kTile;   // ring: two stages of b, c
-  float* wt = reinterpret_cast<float*>(p2 + kTile);   // [NH][kC]
+  float* wt = reinterpret_cast<float*>(sm + 2 * kSegStages * kTile);   // stages of b, c; then [NH][kC]
   unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + sBars);
   int* failed = reinterpret_cast<int*>(tmem_slot + 1);
@@ -656,12 +706,12 @@ __global__ void __launch_bounds__(kSegThreads, 1)
     return;
   }
   if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(128u));
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
     *failed = 0;
-    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i >= sParts && i < sDone ? 12 : i >= sFree && i < sParts ? 13 : 1);
+    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i >= sParts && i < sDone ? kSegFormers : i >= sFree && i < sParts ? kSegFormers + 1 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = tid; i < NH * kC; i += kSegThreads) {   // weights of a whole chunk
@@ -673,7 +723,7 @@ __global__ void __launch_bounds__(kSegThreads, 1)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = *tmem_slot, tP = tmem + 128;   // the sum, then two buffers of three parts
   int n = args.T;
   if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
   const int begin = seg * args.seg_len, end = min(begin + args.seg_len, n);
@@ -683,75 +733,66 @@ __global__ void __launch_bounds__(kSegThreads, 1)
     if (lane == 0)
       for (int k = 0; k < chunks; ++k) {
         const Chunk c = chunk_of(begin + k * kC, end, n, rev);
-        const int s = k & 1;
-        if (!mbar_pass(&bar[sFree + s], ((k >> 1) & 1) ^ 1, failed)) break;
+        const int s = k % kSegStages;
+        if (!mbar_pass(&bar[sFree + s], (k / kSegStages & 1) ^ 1, failed)) break;
         mbar_expect(&bar[sFull + s], 2 * kTile);
         for (int i = 0; i < 2; ++i)
           for (int h = 0; h < 2; ++h)
-            tma_load_4d(smem_u32(ring + (2 * s + i) * kTile) + h * kBoxBytes, &maps.m[which][1 + i], 2 * group + h, c.token0, batch,
+            tma_load_4d(smem_u32(sm + (2 * s + i) * kTile) + h * kBoxBytes, &maps.m[which][1 + i], 2 * group + h, c.token0, batch,
                         &bar[sFull + s]);
       }
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
-      const uint64_t d0 = desc_mn_major(smem_u32(p0), kBoxBytes / 2);
+      constexpr uint32_t iZ = idesc_mn(128, 128, false, true);
       for (int k = 0; k < chunks; ++k) {
-        const uint64_t dc = desc_mn_major(smem_u32(ring + (2 * (k & 1) + 1) * kTile), kBoxBytes);
-        mbar_pass(&bar[sFull + (k & 1)], (k >> 1) & 1, failed);
-        for (int half = 0; half < 2; ++half) {
-          mbar_pass(&bar[sParts + half], k & 1, failed);
-          tmem_fence_after();
-          for (int part = 0; part < (exact ? 3 : 2); ++part)
+        const int s = k % kSegStages;
+        const uint64_t dc = desc_mn_major(smem_u32(sm + (2 * s + 1) * kTile), kBoxBytes);
+        mbar_pass(&bar[sFull + s], k / kSegStages & 1, failed);
+        mbar_pass(&bar[sParts + (k & 1)], k >> 1 & 1, failed);
+        tmem_fence_after();
+        for (int part = 0; part < (exact ? 3 : 2); ++part)
 #pragma unroll
-            for (int s = 0; s < 4; ++s)
-              mma_k16_desc(tmem, d0 + (uint64_t)part * (kTile >> 4) + (uint64_t)half * (kHalfBytes >> 4) + (uint64_t)s * 128,
-                           dc + (uint64_t)(half * 4 + s) * 128, iZ, k > 0 || half > 0 || part > 0 || s > 0);
-          mma_commit(&bar[sDone + half]);
-        }
-        mma_commit(&bar[sFree + (k & 1)]);
+          for (int i = 0; i < 8; ++i)
+            mma_k16_tmem_a(tmem, tP + (k & 1) * 192 + part * 64 + i * 8, dc + (uint64_t)i * 128, iZ, k > 0 || part > 0 || i > 0);
+        mma_commit(&bar[sDone + (k & 1)]);
+        mma_commit(&bar[sFree + s]);
       }
     }
   } else if (warp >= 4) {
-    // 12 warps: a half's rows go to the 256 threads of the last eight, half 0 and half 1 in turn
-    const int t = tid - 256;
-    const int h0 = group * NH;
-    const float lg0 = h0 < args.heads ? args.log2g[h0] : 0.f, lg1 = NH == 2 && h0 + 1 < args.heads ? args.log2g[h0 + 1] : 0.f;
+    // 32 channels and a share of the tokens a warp
+    const int q = warp & 3, share = (warp - 4) >> 2, h = NH == 2 ? q >> 1 : 0, head = group * NH + h;
+    const float lg = head < args.heads ? args.log2g[head] : 0.f;
     for (int k = 0; k < chunks; ++k) {
-      const int s = k & 1, t0 = begin + k * kC;
+      const int s = k % kSegStages, t0 = begin + k * kC;
       const Chunk c = chunk_of(t0, end, n, rev);
-      unsigned char *b = ring + 2 * s * kTile, *cc = b + kTile;
-      float f0 = 1.f, f1 = 1.f;
+      unsigned char *b = sm + 2 * s * kTile, *cc = b + kTile;
+      float f = 1.f;
       if (c.cnt < kC) {
-        asm volatile("bar.sync 2, 384;" ::: "memory");
-        for (int i = tid - 128; i < NH * kC; i += 384) {
+        asm volatile("bar.sync 2, %0;" ::"n"(32 * kSegFormers) : "memory");
+        for (int i = tid - 128; i < NH * kC; i += kSegThreads - 128) {
           const int row = i % kC, o = rev ? kC - 1 - row : row;
-          const float lg = i >= kC ? lg1 : lg0;
-          wt[i] = o < c.cnt && h0 + i / kC < args.heads ? exp2f(lg * (float)(c.cnt - 1 - o)) : 0.f;
+          const float l = group * NH + i / kC < args.heads ? args.log2g[group * NH + i / kC] : 0.f;
+          wt[i] = o < c.cnt && group * NH + i / kC < args.heads ? exp2f(l * (float)(c.cnt - 1 - o)) : 0.f;
         }
-        asm volatile("bar.sync 2, 384;" ::: "memory");
+        asm volatile("bar.sync 2, %0;" ::"n"(32 * kSegFormers) : "memory");
       } else {   // a whole chunk's weights, decayed over the tokens behind it
-        f0 = exp2f(lg0 * (float)(end - t0 - kC));
-        f1 = exp2f(lg1 * (float)(end - t0 - kC));
+        f = exp2f(lg * (float)(end - t0 - kC));
       }
-      mbar_pass(&bar[sFull + s], (k >> 1) & 1, failed);
-      for (int half = 0; half < 2; ++half) {
-        if (k > 0) mbar_pass(&bar[sDone + half], (k - 1) & 1, failed);   // the half's last products are done
-        if (warp >= 8) {
-          uint4 rest[4];
-          const uint32_t at = half * kHalfBytes;
-          form_parts<NH>(b, 64 * half, p0 + at, p1 + at, kBoxBytes / 2, wt, f0, f1, t, exact, rest);
-          if (exact) put_rest(p2 + at, kBoxBytes / 2, t, rest);
-        } else if (half == 0 && !rev && c.cnt < kC) {
-          clear_rows(cc, c.cnt, tid - 128, 128);
-        }
+      if (k > 1) mbar_pass(&bar[sDone + (k & 1)], ((k >> 1) & 1) ^ 1, failed);   // the buffer's last products are done
+      mbar_pass(&bar[sFull + s], k / kSegStages & 1, failed);
+      tmem_fence_after();
+      if (!rev && c.cnt < kC) {
+        clear_rows(cc, c.cnt, tid - 128, kSegThreads - 128);
         fence_async();
-        warp_arrive(&bar[sParts + half], lane);
       }
-      warp_arrive(&bar[sFree + s], lane);
+      form_tmem<kC / 32 * 4 / kSegFormers>(smem_u32(b), tP + (k & 1) * 192, q, share * (kC * 4 / kSegFormers), wt + h * kC, f, exact, lane);
+      tmem_wait_st();
+      warp_arrive(&bar[sParts + (k & 1)], lane);
+      if (lane == 0) mbar_arrive(&bar[sFree + s]);
     }
     if (warp < 8) {
-      const int q = warp & 3, r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, head = group * NH + h;
-      if (chunks > 0) mbar_pass(&bar[sDone + 1], (chunks - 1) & 1, failed);
+      const int r = 32 * q + lane;
+      if (chunks > 0) mbar_pass(&bar[sDone + ((chunks - 1) & 1)], (chunks - 1) >> 1 & 1, failed);
       tmem_fence_after();
       float* dst = args.seg_state +
                    ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * dr * dr + (int64_t)(r % D) * dr;
@@ -781,7 +822,7 @@ __global__ void __launch_bounds__(kSegThreads, 1)
   }
   if (warp == 2) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(128u));
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u));
   }
 }
 
