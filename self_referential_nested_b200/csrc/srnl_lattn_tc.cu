@@ -217,29 +217,46 @@ __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, in
   }
 }
 
-// One 32-column block of a warp's 32 rows of G, masked and decayed, as bf16 pairs; `diff`: blocks
-// between it and the diagonal one.  The distance falls along a row's columns (rises, in reverse).
-// Away from the diagonal the powers are one product after another from the nearest token on, two
-// columns an instruction; on it, where powers below zero would overflow, they are read from the
-// table (zeros lie before its start).
+// A warp's rows of a head's G (block q of 32 tokens), masked and decayed, as bf16 pairs over G's own
+// columns: block j's at 32 j .. + 15.  The distance falls along a row's columns (rises, in reverse).
+// The powers of g are one product after another from the nearest token on, two columns an
+// instruction, and come from registers: while the products run a read of shared memory waits some
+// hundred cycles for its turn, and a table of powers cost 2000 a block.
 template <bool REV>
-__device__ __forceinline__ void mask_block(const float (&v)[32], uint32_t (&w)[16], const float* p, int diff, int lane) {
-  if (diff < 0) {
+__device__ __forceinline__ void mask_rows(uint32_t tG, float log2g, int q, int lane) {
+  const float g = exp2f(log2g);
+  const float2 g2 = make_float2(g * g, g * g);
+  float v[32];
+  uint32_t w[16];
+  tmem_ld32(v, tG + q * 32);
+  tmem_wait_ld();
+  {
+    // the diagonal block, outwards from pair `own`, which holds the row's token: its first column
+    // is at 1, or masked, where the row's token is the second one; then the next pair's first is
+    // at g.  Masked by selection: such a token may hold anything.
+    const int own = lane >> 1;
+    const bool late = ((lane & 1) != 0) == REV;
+    const int next = late ? (REV ? own + 1 : own - 1) : -1;
+    const uint32_t keep = !late ? 0xFFFFFFFFu : REV ? 0xFFFF0000u : 0x0000FFFFu;
+    float first = 0.f, second = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = 0u;
-  } else if (diff == 0) {
-    const float* at = p + (REV ? -lane : lane);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int j = 2 * i;
-      const float x = (REV ? j >= lane : j <= lane) ? v[j] * at[REV ? j : -j] : 0.f;
-      const float y = (REV ? j + 1 >= lane : j + 1 <= lane) ? v[j + 1] * at[REV ? j + 1 : -j - 1] : 0.f;
-      w[i] = pack_bf16(x, y);
+    for (int k = 0; k < 16; ++k) {
+      const int i = REV ? k : 15 - k;
+      const float2 f = __fmul2_rn(make_float2(first, second), g2);
+      first = i == own ? (late ? 0.f : 1.f) : i == next ? g : f.x;
+      second = i == own ? (late ? 1.f : g) : f.y;
+      const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), REV ? make_float2(first, second) : make_float2(second, first));
+      w[i] = (REV ? i >= own : i <= own) ? pack_bf16(x.x, x.y) & (i == own ? keep : 0xFFFFFFFFu) : 0u;
     }
-  } else {
-    const float g1 = p[1], near = REV ? p[diff * 32 - lane] : p[diff * 32 + lane - 31];
-    const float2 g2 = make_float2(g1 * g1, g1 * g1);
-    float2 f = REV ? make_float2(near, near * g1) : make_float2(near * g1, near);
+  }
+  tmem_st16(tG + q * 32, w);
+  const float g32 = exp2f(log2g * 32.f);
+  float near = exp2f(log2g * (float)(REV ? 32 - lane : lane + 1));   // of the next block's nearest token
+#pragma unroll 1
+  for (int j = REV ? q + 1 : q - 1; REV ? j < 4 : j >= 0; j += REV ? 1 : -1) {
+    tmem_ld32(v, tG + j * 32);
+    tmem_wait_ld();
+    float2 f = REV ? make_float2(near, near * g) : make_float2(near * g, near);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int i = REV ? k : 15 - k;
@@ -247,25 +264,13 @@ __device__ __forceinline__ void mask_block(const float (&v)[32], uint32_t (&w)[1
       w[i] = pack_bf16(x.x, x.y);
       f = __fmul2_rn(f, g2);
     }
+    tmem_st16(tG + j * 32, w);
+    near *= g32;
   }
-}
-
-// A warp's rows of a head's G, over G's own columns: block jb's result goes to columns
-// 16 jb .. + 15, which lie on blocks already read.
-template <bool REV>
-__device__ __forceinline__ void mask_rows(uint32_t tG, const float* pw, int q, int lane) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = 0u;
 #pragma unroll 1
-  for (int j = 0; j < 4; j += 2) {
-    float v0[32], v1[32];
-    uint32_t w[16];
-    tmem_ld32(v0, tG + j * 32);
-    tmem_ld32(v1, tG + j * 32 + 32);
-    tmem_wait_ld();
-    mask_block<REV>(v0, w, pw, REV ? j - q : q - j, lane);
-    tmem_st16(tG + j * 16, w);
-    mask_block<REV>(v1, w, pw, REV ? j + 1 - q : q - j - 1, lane);
-    tmem_st16(tG + j * 16 + 16, w);
-  }
+  for (int j = REV ? 0 : q + 1; j < (REV ? q : 4); ++j) tmem_st16(tG + j * 32, w);
 }
 
 struct Chunk {
@@ -298,9 +303,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   constexpr int NH = kC / D;
   extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char *sa = sm, *sb = sa + kTile, *sc = sb + kTile, *ps = sc + kTile, *so = ps + kTile, *zh = so + kTile, *zl = zh + kTile;
-  constexpr int kPw = 32 + kC;
-  float* pw = reinterpret_cast<float*>(zl + kTile) + 32; // [NH][kPw]: g^n, after 32 zeros each
-  float* wt = pw - 32 + NH * kPw;                        // [NH][kC]: weights of the chunk's rows of b
+  float* wt = reinterpret_cast<float*>(zl + kTile);      // [NH][kC]: weights of the chunk's rows of b
   unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
   int* failed = reinterpret_cast<int*>(tmem_slot + 1);
@@ -328,10 +331,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   }
   for (int i = tid; i < NH * kC; i += la_threads(NH)) {
     const int h = group * NH + i / kC, m = i % kC;
-    const float f = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
-    pw[i / kC * kPw + m] = f;
-    if (m < 32) pw[i / kC * kPw + m - 32] = 0.f;
-    wt[i - m + (rev ? m : kC - 1 - m)] = f;   // of a whole chunk; m tokens behind the row's
+    wt[i - m + (rev ? m : kC - 1 - m)] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;   // of a whole chunk; m tokens behind the row's
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         for (int h = 0; h < NH; ++h)
 #pragma unroll
           for (int s = 0; s < 8; ++s)
-            mma_k16_tmem_a(tO + h * 64, tG + h * 128 + s * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
+            mma_k16_tmem_a(tO + h * 64, tG + h * 128 + (s >> 1) * 32 + (s & 1) * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
         mma_commit(&bar[kO]);
         mma_commit(&bar[kFreeC]);
       }
@@ -459,19 +459,21 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
     const int q = warp & 3, head = NH == 2 ? (warp - 4) >> 2 : 0, r = 32 * q + lane;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
     const int ord = rev ? kC - 1 - r : r;   // the token's place in the chunk's order
-    const float* p = pw + head * kPw;
-    const uint32_t tH = tG + lanes + head * 128, tR = tO + lanes + head * 64;
     const bool live = group * NH + head < args.heads;
+    const float lg = live ? args.log2g[group * NH + head] : 0.f;
+    const uint32_t tH = tG + lanes + head * 128, tR = tO + lanes + head * 64;
 #pragma unroll 1
     for (int k = 0; k < chunks; ++k) {
       const uint32_t ph = k & 1;
       const Chunk c = chunk_of(begin + k * kC, end, n, rev);
       mbar_pass(&bar[kG], ph, failed);
       tmem_fence_after();
-      if (rev) mask_rows<true>(tH, p, q, lane);
-      else mask_rows<false>(tH, p, q, lane);
+      int own = lane;
+      asm volatile("" : "+r"(own));   // nothing of a row's place is taken out of the loop: it would cost 40 registers
+      if (rev) mask_rows<true>(tH, lg, q, own);
+      else mask_rows<false>(tH, lg, q, own);
       // the state's share of O, decayed to the row
-      const float f = ord + c.lead < kC ? p[ord + c.lead] : p[kC - 1] * p[1];
+      const float f = exp2f(lg * (float)((rev ? kC - 1 - own : own) - (rev ? 32 * q : -32 * q) + c.lead));
       mbar_pass(&bar[kO2], ph, failed);
       tmem_fence_after();
 #pragma unroll
@@ -588,7 +590,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         asm volatile("bar.sync 2, 256;" ::: "memory");
         for (int i = t; i < NH * kC; i += kStateThreads) {
           const int row = i % kC, o = rev ? kC - 1 - row : row;
-          wt[i] = o < c.cnt ? pw[i / kC * kPw + c.cnt - 1 - o] : 0.f;
+          const int hh = group * NH + i / kC;
+          wt[i] = o < c.cnt && hh < args.heads ? exp2f(args.log2g[hh] * (float)(c.cnt - 1 - o)) : 0.f;
         }
         asm volatile("bar.sync 2, 256;" ::: "memory");
         if (!rev) {
@@ -857,7 +860,7 @@ __global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant_
   }
 }
 
-constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + (size_t)(kC / d) * (2 * kC + 32) * 4 + kBars * 8 + 16; }
+constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + (size_t)(kC / d) * kC * 4 + kBars * 8 + 16; }
 
 template <typename... P, typename... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
