@@ -219,9 +219,14 @@ __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, in
 
 // A warp's rows of a head's G (block q of 32 tokens), masked and decayed, as bf16 pairs over G's own
 // columns: block j's at 32 j .. + 15.  The distance falls along a row's columns (rises, in reverse).
-// The powers of g are one product after another from the nearest token on, two columns an
-// instruction, and come from registers: while the products run a read of shared memory waits some
-// hundred cycles for its turn, and a table of powers cost 2000 a block.
+// Away from the diagonal the powers of g are one product after another from the nearest token on,
+// two columns an instruction.  Nothing is read from shared memory, where a load waits some hundred
+// cycles for its turn while the products run: a table of powers cost 2000 cycles a block.
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 template <bool REV>
 __device__ __forceinline__ void mask_rows(uint32_t tG, float log2g, int q, int lane) {
   const float g = exp2f(log2g);
@@ -230,24 +235,16 @@ __device__ __forceinline__ void mask_rows(uint32_t tG, float log2g, int q, int l
   uint32_t w[16];
   tmem_ld32(v, tG + q * 32);
   tmem_wait_ld();
-  {
-    // the diagonal block, outwards from pair `own`, which holds the row's token: its first column
-    // is at 1, or masked, where the row's token is the second one; then the next pair's first is
-    // at g.  Masked by selection: such a token may hold anything.
-    const int own = lane >> 1;
-    const bool late = ((lane & 1) != 0) == REV;
-    const int next = late ? (REV ? own + 1 : own - 1) : -1;
-    const uint32_t keep = !late ? 0xFFFFFFFFu : REV ? 0xFFFF0000u : 0x0000FFFFu;
-    float first = 0.f, second = 0.f;
+  // the diagonal block: no product of powers from one end reaches every row's own token without
+  // leaving the range, so each power is an exponential.  Masked by selection: such a token may
+  // hold anything, and its power may be infinite.
+  float2 e = REV ? make_float2(log2g * -(float)lane, log2g * (float)(1 - lane)) : make_float2(log2g * (float)lane, log2g * (float)(lane - 1));
+  const float2 de = make_float2(REV ? 2.f * log2g : -2.f * log2g, REV ? 2.f * log2g : -2.f * log2g);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int i = REV ? k : 15 - k;
-      const float2 f = __fmul2_rn(make_float2(first, second), g2);
-      first = i == own ? (late ? 0.f : 1.f) : i == next ? g : f.x;
-      second = i == own ? (late ? 1.f : g) : f.y;
-      const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), REV ? make_float2(first, second) : make_float2(second, first));
-      w[i] = (REV ? i >= own : i <= own) ? pack_bf16(x.x, x.y) & (i == own ? keep : 0xFFFFFFFFu) : 0u;
-    }
+  for (int i = 0; i < 16; ++i) {
+    const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(exp2_approx(e.x), exp2_approx(e.y)));
+    w[i] = pack_bf16((REV ? 2 * i >= lane : 2 * i <= lane) ? x.x : 0.f, (REV ? 2 * i + 1 >= lane : 2 * i + 1 <= lane) ? x.y : 0.f);
+    e = __fadd2_rn(e, de);
   }
   tmem_st16(tG + q * 32, w);
   const float g32 = exp2f(log2g * 32.f);
