@@ -145,6 +145,7 @@ __device__ __forceinline__ void form_parts(const unsigned char* b, int row0, uns
     rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
   }
 }
+enum { kTwo, kThree, kThirdOnly };   // parts to write; the third alone takes the first's place
 // The parts of w b as the left operand in TMEM: for 32 channels (lanes 32 q on) and 32 N tokens from
 // `token` of tile b, part p to columns ta + 64 p + token / 2 on.  ldmatrix transposes as it reads: a
 // register holds two tokens of a channel, in the places tcgen05.st's 16-lane shape wants them.
@@ -160,7 +161,7 @@ __device__ __forceinline__ void tmem_st_16lanes(uint32_t addr, const uint32_t (&
                : "memory");
 }
 template <int N>
-__device__ __forceinline__ void form_tmem(uint32_t b, uint32_t ta, int q, int token, const float* w, float scale, bool third, int lane) {
+__device__ __forceinline__ void form_tmem(uint32_t b, uint32_t ta, int q, int token, const float* w, float scale, int parts, int lane) {
 #pragma unroll 1
   for (int k = 0; k < N; ++k) {
     const int t0 = token + 32 * k;
@@ -187,12 +188,14 @@ __device__ __forceinline__ void form_tmem(uint32_t b, uint32_t ta, int q, int to
         o[0][i] = pack_bf16(x.x, x.y);
         x = __fadd2_rn(x, make_float2(-bf16_lo(o[0][i]), -bf16_hi(o[0][i])));
         o[1][i] = pack_bf16(x.x, x.y);
-        if (third) o[2][i] = pack_bf16(x.x - bf16_lo(o[1][i]), x.y - bf16_hi(o[1][i]));
+        if (parts != kTwo) o[2][i] = pack_bf16(x.x - bf16_lo(o[1][i]), x.y - bf16_hi(o[1][i]));
       }
       const uint32_t at = ta + ((uint32_t)(32 * q + 16 * h) << 16) + (uint32_t)(t0 >> 1);
-      tmem_st_16lanes(at, o[0]);
-      tmem_st_16lanes(at + 64, o[1]);
-      if (third) tmem_st_16lanes(at + 128, o[2]);
+      if (parts != kThirdOnly) {
+        tmem_st_16lanes(at, o[0]);
+        tmem_st_16lanes(at + 64, o[1]);
+      }
+      if (parts != kTwo) tmem_st_16lanes(parts == kThree ? at + 128 : at, o[2]);
     }
   }
 }
@@ -287,20 +290,23 @@ __device__ __forceinline__ void load_tile(unsigned char* dst, const CUtensorMap*
   mbar_expect(bar, kTile);
   for (int h = 0; h < 2; ++h) tma_load_4d(smem_u32(dst) + h * kBoxBytes, map, 2 * group + h, token, batch, bar);
 }
-// A tile into L2: the tiles have one buffer each and are loaded late.
+// A tile into L2: c has one buffer and is loaded late.
 __device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int group, int token, int batch) {
   for (int h = 0; h < 2; ++h) tma_prefetch_4d(map, 2 * group + h, token, batch);
 }
 
-enum { kFullA, kFullB, kFullC, kFreeA, kFreeB, kFreeC, kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars };   // kParts, kPDone: the ring's slots
+enum { kFullA, kFullB = kFullA + 2, kFullC = kFullB + 2, kFreeA, kFreeB = kFreeA + 2, kFreeC = kFreeB + 2, kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars };   // two of those whose next name is 2 further
 
 template <int D>
 __global__ void __launch_bounds__(la_threads(kC / D), 1)
     decay_tc_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
   constexpr int NH = kC / D;
   extern __shared__ __align__(1024) unsigned char sm[];
-  unsigned char *sa = sm, *sb = sa + kTile, *sc = sb + kTile, *ps = sc + kTile, *so = ps + kTile, *zh = so + kTile, *zl = zh + kTile;
-  float* wt = reinterpret_cast<float*>(zl + kTile);      // [NH][kC]: weights of the chunk's rows of b
+  // two tiles of a (O leaves through a's, when its products are done), two of b, c, the state's two
+  // parts and, for narrow heads, the ring of w b
+  constexpr uint32_t kZPart = NH == 2 ? kTile / 2 : kTile;
+  unsigned char *sa = sm, *sb = sa + 2 * kTile, *sc = sb + 2 * kTile, *zh = sc + kTile, *zl = zh + kZPart, *ps = zl + kZPart;
+  float* wt = reinterpret_cast<float*>(sm + 7 * kTile);  // [NH][kC]: weights of the chunk's rows of b
   unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
   int* failed = reinterpret_cast<int*>(tmem_slot + 1);
@@ -322,7 +328,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   if (tid == 0) {
     *failed = 0;
     for (int i = 0; i < kBars; ++i) {
-      mbar_init(&bar[i], i == kRows || i == kOFree ? 4 * NH : i == kParts || i == kParts + 1 || i == kZ || i == kClear ? 8 : i == kFreeB ? 9 : i == kFreeC ? 2 : 1);
+      const bool rows = i == kRows || i == kOFree || i == kFreeA || i == kFreeA + 1, parts = i == kParts || i == kParts + 1;
+      mbar_init(&bar[i], rows || parts ? 4 * NH : i == kZ || i == kClear ? 8 : i == kFreeB || i == kFreeB + 1 ? 9 : i == kFreeC ? 2 : 1);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const uint32_t tmem = *tmem_slot, tG = tmem, tO = tmem + 256, tZ = tmem + 384;
+  const uint32_t tmem = *tmem_slot, tG = tmem, tP = tmem + 128, tO = tmem + 256, tZ = tmem + 384;   // tP: wide heads' w b
 
   int n = args.T;
   if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
@@ -348,21 +355,17 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   if (warp == 0) {
     if (lane == 0) {
       for (int k = 0; k < chunks; ++k) {
-        if (k + 1 < chunks) prefetch_chunk(&maps.m[which][1], group, chunk_of(begin + (k + 1) * kC, end, n, rev).token0, batch);
-        if (!mbar_pass(&bar[kFreeB], (k & 1) ^ 1, failed)) break;
-        load_tile(sb, &maps.m[which][1], group, chunk_of(begin + k * kC, end, n, rev).token0, batch, &bar[kFullB]);
+        if (!mbar_pass(&bar[kFreeB + (k & 1)], (k >> 1 & 1) ^ 1, failed)) break;
+        load_tile(sb + (k & 1) * kTile, &maps.m[which][1], group, chunk_of(begin + k * kC, end, n, rev).token0, batch, &bar[kFullB + (k & 1)]);
       }
     }
   } else if (warp == 3) {
     if (lane == 0) {
       for (int k = 0; k < chunks; ++k) {
-        const int token0 = chunk_of(begin + k * kC, end, n, rev).token0, next = chunk_of(begin + (k + 1) * kC, end, n, rev).token0;
-        if (k + 1 < chunks) {
-          prefetch_chunk(&maps.m[which][0], group, next, batch);
-          prefetch_chunk(&maps.m[which][2], group, next, batch);
-        }
-        if (!mbar_pass(&bar[kFreeA], (k & 1) ^ 1, failed)) break;
-        load_tile(sa, &maps.m[which][0], group, token0, batch, &bar[kFullA]);
+        const int token0 = chunk_of(begin + k * kC, end, n, rev).token0;
+        if (k + 1 < chunks) prefetch_chunk(&maps.m[which][2], group, chunk_of(begin + (k + 1) * kC, end, n, rev).token0, batch);
+        if (!mbar_pass(&bar[kFreeA + (k & 1)], (k >> 1 & 1) ^ 1, failed)) break;
+        load_tile(sa + (k & 1) * kTile, &maps.m[which][0], group, token0, batch, &bar[kFullA + (k & 1)]);
         if (!mbar_pass(&bar[kFreeC], (k & 1) ^ 1, failed)) break;
         load_tile(sc, &maps.m[which][2], group, token0, batch, &bar[kFullC]);
       }
@@ -371,16 +374,17 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
     if (lane == 0) {
       constexpr uint32_t iG = idesc_mn(128, 128, false, false);                 // a b^T
       constexpr uint32_t iO = idesc_mn(128, NH == 2 ? 64 : 128, false, true);   // a Z, P c
-      const uint64_t da = desc_k_major(smem_u32(sa)), db = desc_k_major(smem_u32(sb)), dc = desc_mn_major(smem_u32(sc), kBoxBytes);
+      const uint64_t da0 = desc_k_major(smem_u32(sa)), db0 = desc_k_major(smem_u32(sb)), dc = desc_mn_major(smem_u32(sc), kBoxBytes);
       const uint64_t dzh = desc_mn_major(smem_u32(zh), kBoxBytes), dzl = desc_mn_major(smem_u32(zl), kBoxBytes);
       constexpr uint64_t kBox16 = kBoxBytes >> 4;
 #pragma unroll 1
       for (int k = 0; k < chunks; ++k) {
-        const uint32_t ph = k & 1;
+        const uint32_t ph = k & 1, ph2 = k >> 1 & 1;
+        const uint64_t da = da0 + (uint64_t)ph * (kTile >> 4), db = db0 + (uint64_t)ph * (kTile >> 4);
         // (1) G; its columns hold the previous chunk's left operand until (3) is done
         if (k > 0) mbar_pass(&bar[kO], ph ^ 1, failed);
-        mbar_pass(&bar[kFullB], ph, failed);
-        mbar_pass(&bar[kFullA], ph, failed);
+        mbar_pass(&bar[kFullB + ph], ph2, failed);
+        mbar_pass(&bar[kFullA + ph], ph2, failed);
         tmem_fence_after();
 #pragma unroll
         for (int s = 0; s < 8; ++s) {   // 16 channels a step, four to a box
@@ -388,7 +392,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
           mma_k16_desc(tG + (NH == 2 ? (s >> 2) * 128 : 0), da + at, db + at, iG, NH == 2 ? (s & 3) > 0 : s > 0);
         }
         mma_commit(&bar[kG]);
-        mma_commit(&bar[kFreeB]);
+        mma_commit(&bar[kFreeB + ph]);
         // (4) O = a Z, once Z is written and the last O read
         mbar_pass(&bar[kZ], ph, failed);
         mbar_pass(&bar[kOFree], ph ^ 1, failed);
@@ -398,12 +402,11 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
             const int h = NH == 2 ? s >> 2 : 0;
-            const uint64_t az = (part == 0 ? dzh : dzl) + (uint64_t)s * 128 + (uint64_t)h * kBox16;   // 16 rows of Z
+            const uint64_t az = (part == 0 ? dzh : dzl) + (NH == 2 ? (uint64_t)h * (kTile >> 6) + (uint64_t)(s & 3) * 128 : (uint64_t)s * 128);   // 16 rows of Z
             mma_k16_desc(tO + h * 64, da + (uint64_t)(s >> 2) * kBox16 + (uint64_t)(s & 3) * 2, az, iO,
                          part > 0 || (NH == 2 ? (s & 3) > 0 : s > 0));
           }
         mma_commit(&bar[kO2]);
-        mma_commit(&bar[kFreeA]);
         // (3) O += P c
         mbar_pass(&bar[kRows], ph, failed);
         mbar_pass(&bar[kFullC], ph, failed);
@@ -420,32 +423,40 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
     }
   } else if (warp == 2) {
     if (lane == 0) {
-      // (5) dZ from the parts of w b, a quarter of the tokens a step, then from the rest, two
-      // quarters a step; steps alternate between the ring's slots
-      constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
-      const uint64_t dc = desc_mn_major(smem_u32(sc), kBoxBytes), dp = desc_mn_major(smem_u32(ps), kSlotBox);
-      const int uses = exact ? 3 : 2;   // of a slot in a chunk
+      // (5) dZ from the parts of w b
+      const uint64_t dc = desc_mn_major(smem_u32(sc), kBoxBytes);
+      const int uses = NH == 1 ? (exact ? 2 : 1) : exact ? 3 : 2;   // of a place of the parts in a chunk
 #pragma unroll 1
       for (int k = 0; k < chunks; ++k) {
         mbar_pass(&bar[kFullC], k & 1, failed);
+        if constexpr (NH == 1) {   // in TMEM, half the tokens a step; then the rest in the first part's place
+          constexpr uint32_t iZ = idesc_mn(128, 128, false, true);
 #pragma unroll 1
-        for (int st = 0; st < 2 * uses; ++st) {
-          const int slot = st & 1;
-          mbar_pass(&bar[kParts + slot], (k * uses + (st >> 1)) & 1, failed);
-          tmem_fence_after();
-          const uint64_t pa = dp + (uint64_t)slot * (kSlot >> 4);
-          if (st < 4) {
+          for (int st = 0; st < 2 * uses; ++st) {
+            const int half = st & 1;
+            mbar_pass(&bar[kParts + half], (k * uses + (st >> 1)) & 1, failed);
+            tmem_fence_after();
 #pragma unroll
-            for (int i = 0; i < 4; ++i)   // part i >> 1, 16 tokens i & 1
-              mma_k16_desc(tZ, pa + (uint64_t)(i >> 1) * (kSlotPart >> 4) + (uint64_t)(i & 1) * 128, dc + (uint64_t)(st * 2 + (i & 1)) * 128,
-                           iZ, st > 0 || i > 0);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)   // quarter i >> 1 of two, 16 tokens i & 1
-              mma_k16_desc(tZ, pa + (uint64_t)(i >> 1) * (kSlotPart >> 4) + (uint64_t)(i & 1) * 128, dc + (uint64_t)((st - 4) * 4 + i) * 128,
-                           iZ, true);
+            for (int i = 0; i < 8; ++i)   // part i >> 2, 16 tokens i & 3
+              if (st < 2 || i < 4)
+                mma_k16_tmem_a(tZ, tP + (i >> 2) * 64 + half * 32 + (i & 3) * 8, dc + (uint64_t)(half * 4 + (i & 3)) * 128, iZ, st > 0 || i > 0);
+            mma_commit(&bar[kPDone + half]);
           }
-          mma_commit(&bar[kPDone + slot]);
+        } else {   // in the ring, a quarter of the tokens a step, then the rest, two quarters a step; the slots in turn
+          constexpr uint32_t iZ = idesc_mn(128, 128, true, true);
+          const uint64_t dp = desc_mn_major(smem_u32(ps), kSlotBox);
+#pragma unroll 1
+          for (int st = 0; st < 2 * uses; ++st) {
+            const int slot = st & 1;
+            mbar_pass(&bar[kParts + slot], (k * uses + (st >> 1)) & 1, failed);
+            tmem_fence_after();
+            const uint64_t pa = dp + (uint64_t)slot * (kSlot >> 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)   // part i >> 1, 16 tokens i & 1; of the rest: quarter i >> 1 of two
+              mma_k16_desc(tZ, pa + (uint64_t)(i >> 1) * (kSlotPart >> 4) + (uint64_t)(i & 1) * 128,
+                           dc + (uint64_t)(st < 4 ? st * 2 + (i & 1) : (st - 4) * 4 + i) * 128, iZ, st > 0 || i > 0);
+            mma_commit(&bar[kPDone + slot]);
+          }
         }
         mma_commit(&bar[kDZ]);
         mma_commit(&bar[kFreeC]);
@@ -469,6 +480,10 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       asm volatile("" : "+r"(own));   // nothing of a row's place is taken out of the loop: it would cost 40 registers
       if (rev) mask_rows<true>(tH, lg, q, own);
       else mask_rows<false>(tH, lg, q, own);
+      if (k > 0 && lane == 0) {   // the last chunk's O has left a's tile
+        bulk_wait_read<0>();
+        mbar_arrive(&bar[kFreeA + (ph ^ 1)]);
+      }
       // the state's share of O, decayed to the row
       const float f = exp2f(lg * (float)((rev ? kC - 1 - own : own) - (rev ? 32 * q : -32 * q) + c.lead));
       mbar_pass(&bar[kO2], ph, failed);
@@ -488,8 +503,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       }
       tmem_wait_st();
       warp_arrive(&bar[kRows], lane);
+      unsigned char* so = sa + ph * kTile;
       // O: a whole chunk's leaves by TMA, the last, shorter one's goes straight to its rows
-      if (lane == 0) bulk_wait_read<0>();   // the last chunk's has left the staging tile
       mbar_pass(&bar[kO], ph, failed);
       __syncwarp();
       tmem_fence_after();
@@ -522,60 +537,51 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
     }
     if (lane == 0) bulk_wait_all();
   } else if (warp >= 4 + 4 * NH) {
-    // ---- rows of the state: channel r of the group's b, half of its head's c channels, fp32, in
-    // 32-column blocks: one in registers (64-wide heads) or two in TMEM, where G leaves room.  The
+    // ---- rows of the state: channel r of the group's b, half of its head's c channels, fp32.  The
     // sums are taken here, not in the products' accumulator: their rounding there is not to
     // nearest and would add up over a long memory.
-    constexpr int Z = D / 2, kBlocks = Z / 32;
+    constexpr int Z = D / 2;
     const int q = warp & 3, t = tid - 128 * (1 + NH), r = 32 * q + lane, h = NH == 2 ? r / 64 : 0, br = r % D,
               hf = (warp - 4 - 4 * NH) >> 2;
     const int head = group * NH + h;
     const uint32_t lanes = (uint32_t)(32 * q) << 16;
-    const uint32_t tS = tmem + 128 + lanes + hf * Z;                              // 128-wide heads: the state
-    const uint32_t tD = tZ + lanes + (NH == 2 ? h * 64 : 0) + hf * Z;             // dZ
+    const uint32_t tD = tZ + lanes + (NH == 2 ? h * 64 : 0) + hf * Z;   // dZ
     const bool live = head < args.heads && br < dr && hf * Z < dr;
     const float lg = head < args.heads ? args.log2g[head] : 0.f;
-    float z[32];
-    // block cb in two bf16 parts: row r of Z, its head's columns (a box for each half of a
-    // 128-wide head)
-    auto put_z = [&](int cb) {
+    float z[Z];
+    // columns 8 u .. + 7 in two bf16 parts: row r of Z, its head's columns (a box for each half of
+    // a 128-wide head)
+    auto put_z = [&](int u) {
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = z[8 * u + 2 * i], y = z[8 * u + 2 * i + 1];
-          hi[i] = pack_bf16(x, y);
-          const float2 e = __fadd2_rn(make_float2(x, y), make_float2(-bf16_lo(hi[i]), -bf16_hi(hi[i])));
-          lo[i] = pack_bf16(e.x, e.y);
-        }
-        const int box = NH == 2 ? h : hf, unit = (NH == 2 ? hf : cb) * 4 + u;
-        const uint32_t off = (uint32_t)box * kBoxBytes + (uint32_t)r * 128 + (uint32_t)((unit ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(zh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(zl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      for (int i = 0; i < 4; ++i) {
+        const float x = z[8 * u + 2 * i], y = z[8 * u + 2 * i + 1];
+        hi[i] = pack_bf16(x, y);
+        const float2 e = __fadd2_rn(make_float2(x, y), make_float2(-bf16_lo(hi[i]), -bf16_hi(hi[i])));
+        lo[i] = pack_bf16(e.x, e.y);
       }
+      const int unit = NH == 2 ? hf * 4 + u : u;
+      const uint32_t off = (NH == 2 ? (uint32_t)r * 128 : (uint32_t)hf * kBoxBytes + (uint32_t)r * 128) + (uint32_t)((unit ^ (r & 7)) << 4);
+      *reinterpret_cast<uint4*>(zh + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(zl + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
     {
       const int64_t sq = (int64_t)batch * args.heads + head;
       const float* src = args.segs > 1 ? args.seg_state + (((int64_t)which * args.B * args.heads + sq) * args.segs + seg) * dr * dr
                                        : P.z0 != nullptr ? P.z0 + sq * dr * dr : nullptr;
       const bool tr = args.segs == 1 && P.z0_t;
-#pragma unroll 1
-      for (int cb = 0; cb < kBlocks; ++cb) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          const int c = hf * Z + cb * 32 + i;
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (live && src != nullptr) {
-            if (tr) v = make_float4(src[c * dr + br], src[(c + 1) * dr + br], src[(c + 2) * dr + br], src[(c + 3) * dr + br]);
-            else v = *reinterpret_cast<const float4*>(src + br * dr + c);
-          }
-          z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
+      for (int i = 0; i < Z; i += 4) {
+        const int c = hf * Z + i;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (live && src != nullptr) {
+          if (tr) v = make_float4(src[c * dr + br], src[(c + 1) * dr + br], src[(c + 2) * dr + br], src[(c + 3) * dr + br]);
+          else v = *reinterpret_cast<const float4*>(src + br * dr + c);
         }
-        if (kBlocks > 1) tmem_st32(tS + cb * 32, z);
-        put_z(cb);
+        z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
       }
-      if (kBlocks > 1) tmem_wait_st();
+#pragma unroll
+      for (int u = 0; u < Z / 8; ++u) put_z(u);
       fence_async();
       warp_arrive(&bar[kZ], lane);
     }
@@ -598,27 +604,46 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
           warp_arrive(&bar[kClear], lane);
         }
       }
-      mbar_pass(&bar[kFullB], ph, failed);
-      uint4 rest[4][2];
-      const int uses = exact ? 3 : 2;
+      mbar_pass(&bar[kFullB + ph], k >> 1 & 1, failed);
+      if constexpr (NH == 1) {   // 64 tokens of 32 channels a warp
+        const uint32_t tile = smem_u32(sb + ph * kTile);
+        const int first = k * (exact ? 2 : 1);   // use of the parts' place
+        if (first > 0) mbar_pass(&bar[kPDone + hf], (first - 1) & 1, failed);   // its last products are done
+        tmem_fence_after();
+        form_tmem<2>(tile, tP, q, 64 * hf, wt, 1.f, kTwo, lane);
+        tmem_wait_st();
+        warp_arrive(&bar[kParts + hf], lane);
+        if (exact) {
+          mbar_pass(&bar[kPDone + hf], first & 1, failed);
+          tmem_fence_after();
+          form_tmem<2>(tile, tP, q, 64 * hf, wt, 1.f, kThirdOnly, lane);
+          tmem_wait_st();
+          warp_arrive(&bar[kParts + hf], lane);
+        }
+        warp_arrive(&bar[kFreeB + ph], lane);
+      } else {
+        unsigned char* tile = sb + ph * kTile;
+        uint4 rest[4][2];
+        const int uses = exact ? 3 : 2;
 #pragma unroll
-      for (int st = 0; st < 4; ++st) {
-        const int use = k * uses + (st >> 1);
-        if (use > 0) mbar_pass(&bar[kPDone + (st & 1)], (use - 1) & 1, failed);   // the slot's last products are done
-        unsigned char* slot = ps + (st & 1) * kSlot;
-        form_parts<NH>(sb, 32 * st, slot, slot + kSlotPart, kSlotBox, wt, 1.f, 1.f, t, exact, rest[st]);
-        fence_async();
-        warp_arrive(&bar[kParts + (st & 1)], lane);
-      }
-      warp_arrive(&bar[kFreeB], lane);
-      if (exact) {
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          mbar_pass(&bar[kPDone + st], (k * uses + 1) & 1, failed);
-          put_rest(ps + st * kSlot, kSlotBox, t, rest[2 * st]);
-          put_rest(ps + st * kSlot + kSlotPart, kSlotBox, t, rest[2 * st + 1]);
+        for (int st = 0; st < 4; ++st) {
+          const int use = k * uses + (st >> 1);
+          if (use > 0) mbar_pass(&bar[kPDone + (st & 1)], (use - 1) & 1, failed);   // the slot's last products are done
+          unsigned char* slot = ps + (st & 1) * kSlot;
+          form_parts<NH>(tile, 32 * st, slot, slot + kSlotPart, kSlotBox, wt, 1.f, 1.f, t, exact, rest[st]);
           fence_async();
-          warp_arrive(&bar[kParts + st], lane);
+          warp_arrive(&bar[kParts + (st & 1)], lane);
+        }
+        warp_arrive(&bar[kFreeB + ph], lane);
+        if (exact) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            mbar_pass(&bar[kPDone + st], (k * uses + 1) & 1, failed);
+            put_rest(ps + st * kSlot, kSlotBox, t, rest[2 * st]);
+            put_rest(ps + st * kSlot + kSlotPart, kSlotBox, t, rest[2 * st + 1]);
+            fence_async();
+            warp_arrive(&bar[kParts + st], lane);
+          }
         }
       }
       // z <- g^m z + dZ; a factor near one is applied as z + (g^m - 1) z, whose error does not
@@ -630,23 +655,23 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       mbar_pass(&bar[kDZ], ph, failed);
       if (k + 1 < chunks) mbar_pass(&bar[kO2], ph, failed);   // (4) has read the old Z
       tmem_fence_after();
-#pragma unroll 1
-      for (int cb = 0; cb < kBlocks; ++cb) {
-        float v[32];
-        tmem_ld32(v, tD + cb * 32);
-        if (kBlocks > 1) tmem_ld32(z, tS + cb * 32);
+#pragma unroll
+      for (int cb = 0; cb < Z / 16; ++cb) {
+        float v[16];
+        tmem_ld16(v, tD + cb * 16);
         tmem_wait_ld();
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float2 x = make_float2(z[j], z[j + 1]);
+        for (int j = 0; j < 16; j += 2) {
+          const float2 x = make_float2(z[16 * cb + j], z[16 * cb + j + 1]);
           const float2 y = __fadd2_rn(__ffma2_rn(x, f2, near ? x : make_float2(0.f, 0.f)), make_float2(v[j], v[j + 1]));
-          z[j] = y.x;
-          z[j + 1] = y.y;
+          z[16 * cb + j] = y.x;
+          z[16 * cb + j + 1] = y.y;
         }
-        if (kBlocks > 1) tmem_st32(tS + cb * 32, z);
-        if (k + 1 < chunks) put_z(cb);
+        if (k + 1 < chunks) {
+          put_z(2 * cb);
+          put_z(2 * cb + 1);
+        }
       }
-      if (kBlocks > 1) tmem_wait_st();
       if (k + 1 < chunks) {
         fence_async();
         warp_arrive(&bar[kZ], lane);
@@ -655,17 +680,9 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
     if (exact) {
       const float f = rev && n > 0 ? exp2f(lg) : 1.f;
       float* dst = P.zn + ((int64_t)batch * args.heads + head) * dr * dr + (int64_t)br * dr + hf * Z;
-#pragma unroll 1
-      for (int cb = 0; cb < kBlocks; ++cb) {
-        if (kBlocks > 1) {
-          tmem_ld32(z, tS + cb * 32);
-          tmem_wait_ld();
-        }
-        if (live)
+      if (live)
 #pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<float4*>(dst + cb * 32 + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
-      }
+        for (int i = 0; i < Z; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
     }
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -785,7 +802,7 @@ __global__ void __launch_bounds__(kSegThreads, 1)
         clear_rows(cc, c.cnt, tid - 128, kSegThreads - 128);
         fence_async();
       }
-      form_tmem<kC / 32 * 4 / kSegFormers>(smem_u32(b), tP + (k & 1) * 192, q, share * (kC * 4 / kSegFormers), wt + h * kC, f, exact, lane);
+      form_tmem<kC / 32 * 4 / kSegFormers>(smem_u32(b), tP + (k & 1) * 192, q, share * (kC * 4 / kSegFormers), wt + h * kC, f, exact ? kThree : kTwo, lane);
       tmem_wait_st();
       warp_arrive(&bar[sParts + (k & 1)], lane);
       if (lane == 0) mbar_arrive(&bar[sFree + s]);
