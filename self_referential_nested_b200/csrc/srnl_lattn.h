@@ -24,6 +24,7 @@ struct LaArgs {
   int passes, B, T, heads, d, segs, seg_len;   // segments of seg_len tokens per sequence
   const float* log2g;                       // [heads]
   const int* lengths;                       // [B] or nullptr
+  int longest_first;                        // CTAs take the longest sequences first
   float* seg_state;                         // [pass][B][heads][segs][D][D]: what each segment adds, then its start
   int* err;
 };

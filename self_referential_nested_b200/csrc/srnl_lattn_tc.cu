@@ -42,6 +42,7 @@ constexpr int kC = 128;                  // tokens per chunk, and channels per C
 constexpr uint32_t kBoxBytes = kC * 128; // 128 tokens x 64 channels
 constexpr uint32_t kTile = 2 * kBoxBytes;
 __host__ __device__ constexpr int la_threads(int nh) { return 128 * (3 + nh); }   // loads and products, 4 row warps a head, 8 state warps
+constexpr int kMaxSorted = 512;          // sequences that a CTA ranks by length
 constexpr int kSegFormers = 16, kSegThreads = 128 + 32 * kSegFormers;   // of the segments' kernel
 constexpr int kStateThreads = 256;
 
@@ -312,19 +313,13 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   int* failed = reinterpret_cast<int*>(tmem_slot + 1);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int which = blockIdx.z, seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
-  const int group = blockIdx.y % groups, batch = blockIdx.y / groups;
-  const LaPass& P = args.pass[which];
-  const int rev = P.reverse, dr = args.d;   // dr: a head's channels, D or 32 of a 64-wide piece
+  const int seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
+  int which = blockIdx.z, group = blockIdx.y % groups, batch = blockIdx.y / groups;
   if (smem_u32(sm) & 1023u) {           // the swizzled tiles' alignment
     if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
     return;
   }
 
-  if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
   if (tid == 0) {
     *failed = 0;
     for (int i = 0; i < kBars; ++i) {
@@ -333,11 +328,36 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (args.longest_first) {
+    // the CTAs do not all run at once: batch is the one with so many longer sequences
+    int* len = reinterpret_cast<int*>(sm);
+    const int per = groups * gridDim.z, id = blockIdx.z * gridDim.y + blockIdx.y, rank = id / per;
+    which = id % per / groups;
+    group = id % groups;
+    for (int i = tid; i < args.B; i += la_threads(NH)) len[i] = args.lengths[i];
+    __syncthreads();
+    for (int i = tid; i < args.B; i += la_threads(NH)) {
+      const int mine = len[i];
+      int before = 0;
+      for (int j = 0; j < args.B; ++j) before += len[j] > mine || (len[j] == mine && j < i);
+      if (before == rank) *tmem_slot = i;
+    }
+    __syncthreads();
+    batch = *tmem_slot;
+    fence_async();
+    __syncthreads();
+  }
+  const LaPass& P = args.pass[which];
+  const int rev = P.reverse, dr = args.d;   // dr: a head's channels, D or 32 of a 64-wide piece
   for (int i = tid; i < NH * kC; i += la_threads(NH)) {
     const int h = group * NH + i / kC, m = i % kC;
     wt[i - m + (rev ? m : kC - 1 - m)] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;   // of a whole chunk; m tokens behind the row's
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
@@ -919,6 +939,7 @@ cudaError_t launch_la_tc(LaArgs& a, int sms, cudaStream_t s) {
   const int want = la_tc_segments(a.T, a.B * la_groups(a.heads, a.d) * a.passes, sms);
   a.seg_len = (chunks + want - 1) / want * kC;
   a.segs = (a.T + a.seg_len - 1) / a.seg_len;
+  a.longest_first = a.lengths != nullptr && a.segs == 1 && a.B <= kMaxSorted && a.B * la_groups(a.heads, a.d) * a.passes > sms;
   const TensorMapEncoder enc = ffn_tensor_map_encoder();
   if (enc == nullptr) return cudaErrorNotSupported;
   LaMaps m;
