@@ -106,47 +106,45 @@ __device__ __forceinline__ void warp_arrive(unsigned long long* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
-// Parts of w b for U x 16 tokens from row `row0` of tile b: x = w b, part 0 = bf16(x) to p0, part 1 =
-// bf16(x - part 0) to p1, both boxes of 64 channels, `box_stride` apart; the rest, as bf16, stays in
-// `rest`.  256 threads (t), a 16-byte unit of each U-th row.  A row without weight (no token of this
-// sequence: it may hold anything) becomes zero.  All loads come first: the products' operands take
-// most of the shared memory's time, and a load waits long for its turn.
-template <int NH, int U>
-__device__ __forceinline__ void form_parts(const unsigned char* b, int row0, unsigned char* p0, unsigned char* p1, uint32_t box_stride,
-                                           const float* w, float scale0, float scale1, int t, bool third, uint4 (&rest)[U]) {
+enum { kTwo, kThree, kThirdOnly };   // parts of w b to write; the third alone takes the first's place
+
+// Parts of w b for 32 tokens from row `row0` of tile b into a slot of the ring: x = w b, part 0 =
+// bf16(x), part 1 = bf16(x - part 0), or the rest alone.  256 threads (t), a 16-byte unit of two
+// rows.  A row without weight (no token of this sequence: it may hold anything) becomes zero.  All
+// loads come first: the products' operands take most of the shared memory's time, and a load waits
+// long for its turn.
+constexpr uint32_t kSlot = 16384, kSlotPart = 8192, kSlotBox = 4096;   // two parts of 32 tokens, two boxes of 64 channels each
+__device__ __forceinline__ void form_parts(const unsigned char* b, int row0, unsigned char* to, const float* w, int t, bool rest) {
   const int u = t & 15, box = u >> 3;
   const uint32_t sw = (uint32_t)(((u & 7) ^ ((t >> 4) & 7)) << 4);
-  const float* wr = w + (NH == 2 ? box : 0) * kC + row0 + (t >> 4);
-  const float scale = NH == 2 && box ? scale1 : scale0;
+  const float* wr = w + box * kC + row0 + (t >> 4);
   const unsigned char* src = b + box * kBoxBytes + (row0 + (t >> 4)) * 128 + sw;
-  const uint32_t off = (uint32_t)box * box_stride + (uint32_t)(t >> 4) * 128 + sw;
-  uint4 raw[U];
-  float f[U];
+  unsigned char* dst = to + (uint32_t)box * kSlotBox + (uint32_t)(t >> 4) * 128 + sw;
+  uint4 raw[2];
+  float f[2];
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < 2; ++i) {
     raw[i] = *reinterpret_cast<const uint4*>(src + i * 2048);
     f[i] = wr[16 * i];
   }
 #pragma unroll
-  for (int i = 0; i < U; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const bool on = f[i] != 0.f;
-    const float2 g = make_float2(f[i] * scale, f[i] * scale);
+    const float2 g = make_float2(f[i], f[i]);
     const uint32_t in[4] = {on ? raw[i].x : 0u, on ? raw[i].y : 0u, on ? raw[i].z : 0u, on ? raw[i].w : 0u};
-    uint32_t o0[4], o1[4], o2[4] = {0u, 0u, 0u, 0u};
+    uint32_t o0[4], o1[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       float2 x = __fmul2_rn(make_float2(bf16_lo(in[k]), bf16_hi(in[k])), g);
       o0[k] = pack_bf16(x.x, x.y);
       x = __fadd2_rn(x, make_float2(-bf16_lo(o0[k]), -bf16_hi(o0[k])));
       o1[k] = pack_bf16(x.x, x.y);
-      if (third) o2[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
+      if (rest) o0[k] = pack_bf16(x.x - bf16_lo(o1[k]), x.y - bf16_hi(o1[k]));
     }
-    *reinterpret_cast<uint4*>(p0 + off + i * 2048) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-    *reinterpret_cast<uint4*>(p1 + off + i * 2048) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
-    rest[i] = make_uint4(o2[0], o2[1], o2[2], o2[3]);
+    *reinterpret_cast<uint4*>(dst + i * 2048) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+    if (!rest) *reinterpret_cast<uint4*>(dst + kSlotPart + i * 2048) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
   }
 }
-enum { kTwo, kThree, kThirdOnly };   // parts to write; the third alone takes the first's place
 // The parts of w b as the left operand in TMEM: for 32 channels (lanes 32 q on) and 32 N tokens from
 // `token` of tile b, part p to columns ta + 64 p + token / 2 on.  ldmatrix transposes as it reads: a
 // register holds two tokens of a channel, in the places tcgen05.st's 16-lane shape wants them.
@@ -200,18 +198,6 @@ __device__ __forceinline__ void form_tmem(uint32_t b, uint32_t ta, int q, int to
     }
   }
 }
-// The rest into a part of its own.
-template <int U>
-__device__ __forceinline__ void put_rest(unsigned char* p, uint32_t box_stride, int t, const uint4 (&rest)[U]) {
-  const int u = t & 15;
-#pragma unroll
-  for (int i = 0; i < U; ++i)
-    *reinterpret_cast<uint4*>(p + (uint32_t)(u >> 3) * box_stride + (uint32_t)(t >> 4) * 128 + i * 2048 +
-                              (uint32_t)(((u & 7) ^ ((t >> 4) & 7)) << 4)) = rest[i];
-}
-// The main kernel's ring: a slot holds two parts of 32 tokens.
-constexpr uint32_t kSlot = 16384, kSlotPart = 8192, kSlotBox = 4096;
-
 // Rows of tile c from token `from` on become zero (tokens behind a sequence's last one hold
 // anything, and zero times NaN is NaN).
 __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, int threads) {
@@ -643,28 +629,26 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         warp_arrive(&bar[kFreeB + ph], lane);
       } else {
         unsigned char* tile = sb + ph * kTile;
-        uint4 rest[4][2];
         const int uses = exact ? 3 : 2;
-#pragma unroll
+#pragma unroll 1
         for (int st = 0; st < 4; ++st) {
           const int use = k * uses + (st >> 1);
           if (use > 0) mbar_pass(&bar[kPDone + (st & 1)], (use - 1) & 1, failed);   // the slot's last products are done
-          unsigned char* slot = ps + (st & 1) * kSlot;
-          form_parts<NH>(tile, 32 * st, slot, slot + kSlotPart, kSlotBox, wt, 1.f, 1.f, t, exact, rest[st]);
+          form_parts(tile, 32 * st, ps + (st & 1) * kSlot, wt, t, false);
           fence_async();
           warp_arrive(&bar[kParts + (st & 1)], lane);
         }
-        warp_arrive(&bar[kFreeB + ph], lane);
-        if (exact) {
-#pragma unroll
+        if (exact) {   // the rest of two quarters a slot
+#pragma unroll 1
           for (int st = 0; st < 2; ++st) {
             mbar_pass(&bar[kPDone + st], (k * uses + 1) & 1, failed);
-            put_rest(ps + st * kSlot, kSlotBox, t, rest[2 * st]);
-            put_rest(ps + st * kSlot + kSlotPart, kSlotBox, t, rest[2 * st + 1]);
+            form_parts(tile, 64 * st, ps + st * kSlot, wt, t, true);
+            form_parts(tile, 64 * st + 32, ps + st * kSlot + kSlotPart, wt, t, true);
             fence_async();
             warp_arrive(&bar[kParts + st], lane);
           }
         }
+        warp_arrive(&bar[kFreeB + ph], lane);
       }
       // z <- g^m z + dZ; a factor near one is applied as z + (g^m - 1) z, whose error does not
       // add up over thousands of chunks
