@@ -518,16 +518,31 @@ __global__ void __launch_bounds__(few_warps<GLU>() * 32, GLU && NT == 1 ? 5 : 2)
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[t][e] = 0.f;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  uint4 a[U][2], b[U][NT];
+  auto weights = [&](int u, int k) {
+    a[u][0] = k < K && on0 ? load_once(w0 + k) : zero;
+    a[u][1] = k < K && on1 ? load_once(w1 + k) : zero;
+  };
+  // the second kernel's first weights come while the first one ends: that one waited for all before
+  // it, so nothing writes them any more (4 rows, 2048 x 5632: 17.7 -> 16.7 us; at 16 rows the
+  // registers do not suffice, and it cost 2 us)
+  constexpr bool kEarly = !GLU && NT == 1;
+  if constexpr (kEarly)
+#pragma unroll
+    for (int u = 0; u < U; ++u) weights(u, (warp + u * kWarps) * 32 + kk);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   for (int k0 = warp * 32; k0 < K; k0 += kWarps * 32 * U) {   // the same passes in every lane: the products are the warp's
-    uint4 a[U][2], b[U][NT];
+    if constexpr (NT == 1) {   // all of them before the tokens, which L1 holds
+      if (!kEarly || k0 != warp * 32)
+#pragma unroll
+        for (int u = 0; u < U; ++u) weights(u, k0 + u * kWarps * 32 + kk);
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int k = k0 + u * kWarps * 32 + kk;
-      a[u][0] = k < K && on0 ? load_once(w0 + k) : zero;
-      a[u][1] = k < K && on1 ? load_once(w1 + k) : zero;
+      if constexpr (NT > 1) weights(u, k);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         const int r = t * 8 + g;
