@@ -91,12 +91,16 @@ struct FfnProduct {
   int M, N, tiles_m, tiles_n;
   int k0, k1;            // stages of the first and of the second operand pair
   int a, b, o, a_mn;
+  int parts;             // K is cut into so many, each a tile of its own; at most one product of a launch
 };
 
 struct FfnArgs {
   FfnProduct product[4];
   int products, tiles;
   int save, res;         // kGlu: gate and up are kept; kPlain: in[0] is added
+  const bf16_t* res_at;  // the same as in[0]
+  float* partial;        // the sums of a cut product's parts: [tile][CTA][warp][part][32 rows x columns]
+  unsigned* arrived;     // [tile][CTA][warp], zeros between launches
   int* err;
 };
 
@@ -147,24 +151,41 @@ __device__ __forceinline__ void activation(float2 v, float2& f, float2& df) {
 
 // A launch's tiles product by product; a product's in bands of 8 along M, M fastest within a
 // band: the pairs that run together share their operands' rows in L2.
-template <int EPI>
-__device__ __forceinline__ const FfnProduct& tile_of(int t, const FfnArgs& args, int& tm, int& tn) {
+struct Tile {
+  int tm, tn, n, part;   // n: its number in the product
+};
+template <int EPI, bool CUT>
+__device__ __forceinline__ const FfnProduct& tile_of(int t, const FfnArgs& args, Tile& tile) {
   constexpr int kBand = 8;
   int i = 0;
   if (EPI == kGrad)
     while (i + 1 < args.products && t >= args.product[i + 1].first) ++i;
   const FfnProduct& p = args.product[i];
   t -= p.first;
+  tile.part = 0;
+  if (CUT && p.parts > 1) {
+    tile.part = t % p.parts;
+    t /= p.parts;
+  }
+  tile.n = t;
   const int band = t / (kBand * p.tiles_n), first = band * kBand;
   const int rows = min(kBand, p.tiles_m - first), in = t - band * kBand * p.tiles_n;
-  tm = first + in % rows;
-  tn = in / rows;
+  tile.tm = first + in % rows;
+  tile.tn = in / rows;
   return p;
 }
 
+// The stage that a part of a cut product begins with.
+template <bool CUT>
+__device__ __forceinline__ int stage_of(const FfnProduct& p, int part) {
+  return CUT ? (p.k0 + p.k1) * part / p.parts : part ? p.k0 + p.k1 : 0;
+}
+
 // B lies K-major forward (weights' rows along K) and MN-major backward.  A lies K-major but for the
-// weights' gradients, which share a launch (kGrad) with the input's.
-template <int EPI, int ACT, int BN>
+// weights' gradients, which share a launch (kGrad) with the input's.  CUT: the first product's K
+// comes in parts; a kernel of its own, since the others lost 6 us at 1531 x 520 x 1384 to code that
+// they do not run.
+template <int EPI, int ACT, int BN, bool CUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     ffn_product_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnArgs args) {
   constexpr bool BMN = EPI == kGluBack || EPI == kGrad;
@@ -218,13 +239,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       uint32_t ph = 1u;   // the ring starts empty
       const uint32_t lead = map_rank(smem_u32(full), 0), ring = smem_u32(smem);
       for (int t = pair; t < tiles; t += pairs) {
-        int tm, tn;
-        const FfnProduct& P = tile_of<EPI>(t, args, tm, tn);
-        const int k0 = P.k0, ktot = P.k0 + P.k1;
+        Tile T;
+        const FfnProduct& P = tile_of<EPI, CUT>(t, args, T);
+        const int k0 = P.k0, end = stage_of<CUT>(P, T.part + 1);
         const bool a_mn = EPI == kGrad && P.a_mn;
-        const int m0 = tm * kTileM + (int)rank * 128;
-        const int n0 = EPI == kGlu ? tn * (BN / 2) : tn * BN + (int)rank * kBRows;
-        for (int it = 0; it < ktot; ++it) {
+        const int m0 = T.tm * kTileM + (int)rank * 128;
+        const int n0 = EPI == kGlu ? T.tn * (BN / 2) : T.tn * BN + (int)rank * kBRows;
+        for (int it = stage_of<CUT>(P, T.part); it < end; ++it) {
           const int two = it >= k0;
           const int k = (it - (two ? k0 : 0)) * kTileK;
           const CUtensorMap* am = &maps.a[P.a + two];
@@ -255,9 +276,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       const uint32_t ring = smem_u32(smem);
       const uint64_t bd0 = BMN ? desc_mn_major(ring + kABytes, 8192) : desc_k_major(ring + kABytes);
       for (int t = pair; t < tiles; t += pairs) {
-        int tm, tn;
-        const FfnProduct& P = tile_of<EPI>(t, args, tm, tn);
-        const int ktot = P.k0 + P.k1;
+        Tile T;
+        const FfnProduct& P = tile_of<EPI, CUT>(t, args, T);
+        const int ktot = stage_of<CUT>(P, T.part + 1) - stage_of<CUT>(P, T.part);
         const bool a_mn = EPI == kGrad && P.a_mn;
         const uint32_t idesc = a_mn ? idesc_mn(kTileM, BN, true, BMN) : idesc_mn(kTileM, BN, false, BMN);
         const uint64_t ad0 = a_mn ? desc_mn_major(ring, 8192) : desc_k_major(ring), astep = a_mn ? 128 : 2;
@@ -300,12 +321,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
     // (dgate and dup; the sum) are written over it and leave by TMA, h beside them.
     constexpr int kCols = EPI == kGluBack ? 32 : 64, kPieces = kHalf / kCols, kPiece = kCols * 64;
     constexpr int kBuf = (EPI == kGluBack ? 3 : 1) * kPiece;
-    const bool reads = EPI == kGluBack || (EPI == kPlain && args.res != 0);
+    const bool reads = EPI == kGluBack || (EPI == kPlain && !CUT && args.res != 0);
     unsigned long long* mybar = inbar + 2 * ew;
     auto fetch = [&](int t, int c, int b) {   // lane 0: piece c of tile t into buffer b
-      int tm, tn;
-      tile_of<EPI>(t, args, tm, tn);
-      const int row = tm * kTileM + (int)rank * 128 + quarter * 32, col = tn * BN + half * kHalf + kCols * c;
+      Tile T;
+      tile_of<EPI, CUT>(t, args, T);
+      const int row = T.tm * kTileM + (int)rank * 128 + quarter * 32, col = T.tn * BN + half * kHalf + kCols * c;
       mbar_expect(&mybar[b], (EPI == kGluBack ? 2 : 1) * kPiece);
       for (int i = 0; i < (EPI == kGluBack ? 2 : 1); ++i)
         tma_load_own(smem_u32(box + b * kBuf + i * kPiece), &maps.in[i], col, row, &mybar[b]);
@@ -326,9 +347,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
       __syncwarp();
     };
     for (int t = pair; t < tiles; t += pairs) {
-      int tm, tn;
-      const FfnProduct& P = tile_of<EPI>(t, args, tm, tn);
-      const int row0 = tm * kTileM + (int)rank * 128 + quarter * 32;
+      Tile T;
+      const FfnProduct& P = tile_of<EPI, CUT>(t, args, T);
+      const int tn = T.tn, row0 = T.tm * kTileM + (int)rank * 128 + quarter * 32;
       const uint32_t acc = tmem + (uint32_t)(buf * BN) + ((uint32_t)(32 * quarter) << 16);
       mbar_pass(&tfull[buf], ph, failed);
       tmem_fence_after();
@@ -418,8 +439,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           }
         }
       } else {
+        // of a cut product: this part's sums go to memory; who comes last adds up all parts, in
+        // their order, and goes on with the sum
+        const bool cut = CUT && P.parts > 1;
+        const int64_t slot = ((int64_t)T.n * 2 + rank) * kEpiWarps + ew;
+        float4* mine = reinterpret_cast<float4*>(args.partial + slot * P.parts * (32 * kHalf)) + lane;
+        constexpr int kPart = 32 * kHalf / 4;
+        bool finish = true;
+        if (cut) {
+          finish = false;
+          if (row0 < P.M) {
 #pragma unroll 1
-        for (int c = 0; c < kPieces; ++c, ++piece) {
+            for (int c = 0; c < kHalf / 32; ++c) {
+              float v[32];
+              tmem_ld32(v, acc + half * kHalf + 32 * c);
+              tmem_wait_ld();
+              if (row0 + lane < P.M)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  mine[T.part * kPart + (c * 8 + j) * 32] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            }
+            __threadfence();
+            __syncwarp();
+            unsigned before = 0;
+            if (lane == 0) before = atomicAdd(&args.arrived[slot], 1u);
+            finish = __shfl_sync(0xFFFFFFFFu, before, 0) == (unsigned)P.parts - 1;
+            if (finish) {
+              __threadfence();
+              if (lane == 0) args.arrived[slot] = 0;
+            }
+          }
+        }
+#pragma unroll 1
+        for (int c = 0; c < kPieces && finish; ++c, ++piece) {
           const int b = piece & 1, col = tn * BN + half * kHalf + 64 * c;
           unsigned char* at = box + b * kBuf;
           ahead(t, c, b);
@@ -427,9 +479,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
           for (int k = 0; k < 2; ++k) {
             float v[32];
             uint32_t w[16];
-            tmem_ld32(v, acc + half * kHalf + 64 * c + 32 * k);
-            if (reads && k == 0) mbar_pass(&mybar[b], (piece >> 1) & 1, failed);
-            tmem_wait_ld();
+            if (!cut) {
+              tmem_ld32(v, acc + half * kHalf + 64 * c + 32 * k);
+              if (reads && k == 0) mbar_pass(&mybar[b], (piece >> 1) & 1, failed);
+              tmem_wait_ld();
+            } else {
+              const bool on = row0 + lane < P.M;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+              if (on) {
+                const float4* from = mine + (2 * c + k) * 8 * 32;
+#pragma unroll 2
+                for (int p = 0; p < P.parts; ++p, from += kPart) {
+                  float4 x[8];
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) x[j] = __ldcg(from + j * 32);
+#pragma unroll
+                  for (int j = 0; j < 8; ++j) {
+                    v[4 * j] += x[j].x; v[4 * j + 1] += x[j].y; v[4 * j + 2] += x[j].z; v[4 * j + 3] += x[j].w;
+                  }
+                }
+                if (EPI == kPlain && args.res) {
+                  const bf16_t* r = args.res_at + (int64_t)(row0 + lane) * P.N + col + 32 * k;
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if (col + 32 * k + 8 * j < P.N) {
+                      const uint4 q = *reinterpret_cast<const uint4*>(r + 8 * j);
+                      const uint32_t rw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                      for (int i = 0; i < 4; ++i) {
+                        v[8 * j + 2 * i] += bf16_lo(rw[i]);
+                        v[8 * j + 2 * i + 1] += bf16_hi(rw[i]);
+                      }
+                    }
+                }
+              }
+            }
             if (reads) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
@@ -623,44 +708,53 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 template <int EPI, int ACT>
 cudaError_t launch_product(int bn, const FfnMaps& maps, const FfnArgs& a, int sms, cudaStream_t s) {
   const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
-  return bn == 256 ? launch_after(ffn_product_kernel<EPI, ACT, 256>, dim3(2 * pairs), kFfnThreads, ffn_smem(EPI, 256), s, maps, a)
-                   : launch_after(ffn_product_kernel<EPI, ACT, 128>, dim3(2 * pairs), kFfnThreads, ffn_smem(EPI, 128), s, maps, a);
+  const dim3 grid(2 * pairs);
+  if constexpr (EPI == kPlain || EPI == kGrad) {
+    if (a.product[0].parts > 1)
+      return bn == 256 ? launch_after(ffn_product_kernel<EPI, ACT, 256, true>, grid, kFfnThreads, ffn_smem(EPI, 256), s, maps, a)
+                       : launch_after(ffn_product_kernel<EPI, ACT, 128, true>, grid, kFfnThreads, ffn_smem(EPI, 128), s, maps, a);
+  }
+  return bn == 256 ? launch_after(ffn_product_kernel<EPI, ACT, 256, false>, grid, kFfnThreads, ffn_smem(EPI, 256), s, maps, a)
+                   : launch_after(ffn_product_kernel<EPI, ACT, 128, false>, grid, kFfnThreads, ffn_smem(EPI, 128), s, maps, a);
 }
 
-template <int EPI, int ACT>
+template <int EPI, int ACT, bool CUT = false>
 cudaError_t prepare_product() {
-  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 256>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 256));
+  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 256, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 256));
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 128));
+    e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 128, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 128));
   return e;
 }
 
 // One more product of a launch, its tiles after those before it.  cols: columns of its tiles.
-void add_product(FfnArgs& a, int64_t M, int64_t N, int cols, int64_t K, bool two, int am, int bm, int om, bool a_mn) {
+void add_product(FfnArgs& a, int64_t M, int64_t N, int cols, int64_t K, bool two, int am, int bm, int om, bool a_mn,
+                 int parts = 1) {
   FfnProduct& p = a.product[a.products++];
   p.first = a.tiles;
   p.M = (int)M; p.N = (int)N;
   p.tiles_m = ceil_div(M, kTileM); p.tiles_n = ceil_div(N, cols);
   p.k0 = ceil_div(K, kTileK); p.k1 = two ? p.k0 : 0;
   p.a = am; p.b = bm; p.o = om; p.a_mn = a_mn;
-  a.tiles += p.tiles_m * p.tiles_n;
+  p.parts = parts;
+  a.tiles += p.tiles_m * p.tiles_n * parts;
 }
 
 // Most stages that a pair of CTAs has in a launch.
 int64_t longest_pair(const FfnArgs& a, int pairs) {
-  if (a.tiles <= pairs) {
-    int k = 0;
-    for (int i = 0; i < a.products; ++i) k = a.product[i].k0 + a.product[i].k1 > k ? a.product[i].k0 + a.product[i].k1 : k;
-    return k;
-  }
-  int64_t all = 0;   // tiles go to the pairs in turn: the first pair has the most of each product
+  int64_t all = 0, most = 0;   // tiles go to the pairs in turn: the first pair has the most of each product
   for (int i = 0; i < a.products; ++i) {
     const FfnProduct& p = a.product[i];
-    const int n = p.tiles_m * p.tiles_n, after = (p.first + n + pairs - 1) / pairs, before = (p.first + pairs - 1) / pairs;
-    all += (int64_t)(after - before) * (p.k0 + p.k1);
+    const int n = p.tiles_m * p.tiles_n * p.parts, after = (p.first + n + pairs - 1) / pairs, before = (p.first + pairs - 1) / pairs;
+    const int k = ceil_div(p.k0 + p.k1, p.parts);
+    all += (int64_t)(after - before) * k;
+    most = k > most ? k : most;
   }
-  return all;
+  return a.tiles <= pairs ? most : all;
 }
+
+// Parts of K at most, and what a cut costs, in stages of a 256-column tile: in any case, and for
+// each part of such a tile.
+constexpr int kMostParts = 8, kCutStages = 12, kPartStages = 3;
 
 template <bool GLU, int ACT>
 cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, const bf16_t* res, bf16_t* out, bf16_t* gate,
@@ -673,13 +767,41 @@ cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, 
 }
 
 // Columns of the pairs' tiles: 256, or 128 where that fills the SMs better (`wide`, `narrow`: the
-// launch either way).  A 128-column tile reads as much of A for half the work and takes about 0.8
-// of a 256-column one (8192 x 2048 x 11264: 409 us in 7 rounds of them, 259 us in 4; 1531 x 1384 x
-// 520 in one round each: 16 us against 20).
+// launch either way).  A 128-column tile reads as much of A for half the work.  It takes about 0.85
+// of a 256-column one where the rounds of tiles follow one another (8192 x 2048 x 11264: 409 us in
+// 7 rounds of them, 259 us in 4) and two thirds in a single round (512 x 5632 x 2048, with the
+// projections before it: 58 us against 65; 1024 rows: 70 us, against 74 in 256 columns and two
+// parts).
+int64_t launch_cost(const FfnArgs& a, int bn, int sms) {
+  return (bn == 256 ? 12 : a.tiles <= sms / 2 ? 8 : 10) * longest_pair(a, sms / 2);
+}
 int pick_bn(const FfnArgs& wide, const FfnArgs& narrow, int sms) {
-  return 10 * longest_pair(narrow, sms / 2) < 12 * longest_pair(wide, sms / 2) ? 128 : 256;
+  return launch_cost(narrow, 128, sms) < launch_cost(wide, 256, sms) ? 128 : 256;
 }
 
+// The launch `build(cols, parts)` with the columns and the parts of K of its first product that
+// take least.  A long sum over few tiles leaves most SMs idle; a cut one pays for its partial sums,
+// which go through L2 and are added up by whoever comes last (output product of 2048 x 5632, 64
+// rows, with the projections before it: 44 us uncut, 39, 36.5 and 35.5 in 2, 3 and 4 parts; of 520 x
+// 1384, 22 stages: 15.6 uncut, 16.5 in 2).
+template <typename Build>
+FfnArgs pick_launch(int sms, bool may_cut, int& bn, const Build& build) {
+  FfnArgs best{};
+  int64_t least = INT64_MAX;
+  for (int cols = 256; cols >= 128; cols -= 128)
+    for (int parts = 1; parts <= (may_cut ? kMostParts : 1); ++parts) {
+      const FfnArgs a = build(cols, parts);
+      const FfnProduct& p = a.product[0];
+      if (parts > 1 && (p.tiles_m * p.tiles_n * parts > sms / 2 || p.k0 + p.k1 < parts)) continue;
+      const int64_t cost = launch_cost(a, cols, sms) + (parts > 1 ? 12 * (kCutStages + kPartStages * parts * cols / 256) : 0);
+      if (cost < least) {
+        least = cost;
+        best = a;
+        bn = cols;
+      }
+    }
+  return best;
+}
 
 }  // namespace
 }  // namespace srnl
@@ -690,6 +812,8 @@ struct srnl_ffn {
   int device = 0, sms = 0;
   // workspace, bf16 [max_rows][hidden]: the branch's hidden rows; in training also dgate, dup
   __nv_bfloat16 *hid = nullptr, *dgate = nullptr, *dup = nullptr;
+  float* partial = nullptr;       // a tile of 256 x 256 sums for each pair of SMs
+  unsigned* arrived = nullptr;    // a counter for each of their warps
   int* dev_err = nullptr;
   char err[256] = "";
 };
@@ -711,7 +835,7 @@ srnl_status ffn_cuda_fail(srnl_ffn* h, cudaError_t e, const char* what) {
 }
 
 void ffn_free(srnl_ffn* h) {
-  void* ptrs[] = {h->hid, h->dgate, h->dup, h->dev_err};
+  void* ptrs[] = {h->hid, h->dgate, h->dup, h->partial, h->arrived, h->dev_err};
   for (void* p : ptrs)
     if (p != nullptr) cudaFree(p);
 }
@@ -779,14 +903,20 @@ srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg) {
   if (e == cudaSuccess) e = cudaMalloc(&h->hid, bytes);
   if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dgate, bytes);
   if (e == cudaSuccess && cfg->training) e = cudaMalloc(&h->dup, bytes);
+  const size_t pairs = (size_t)(h->sms / 2);
+  if (e == cudaSuccess) e = cudaMalloc(&h->partial, pairs * kTileM * 256 * sizeof(float));
+  if (e == cudaSuccess) e = cudaMalloc(&h->arrived, pairs * 2 * kEpiWarps * sizeof(unsigned));
+  if (e == cudaSuccess) e = cudaMemset(h->arrived, 0, pairs * 2 * kEpiWarps * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
   if (e == cudaSuccess) e = prepare_product<kGlu, SRNL_ACT_SILU>();
   if (e == cudaSuccess) e = prepare_product<kGlu, SRNL_ACT_GELU>();
   if (e == cudaSuccess) e = prepare_product<kPlain, 0>();
+  if (e == cudaSuccess) e = prepare_product<kPlain, 0, true>();
   if (e == cudaSuccess) e = prepare_product<kGluBack, SRNL_ACT_SILU>();
   if (e == cudaSuccess) e = prepare_product<kGluBack, SRNL_ACT_GELU>();
   if (e == cudaSuccess) e = prepare_product<kGrad, 0>();
+  if (e == cudaSuccess) e = prepare_product<kGrad, 0, true>();
   if (e == cudaSuccess && ffn_tensor_map_encoder() == nullptr) e = cudaErrorNotSupported;
   if (e != cudaSuccess) {
     const srnl_status st = ffn_cuda_fail(nullptr, e, "feed-forward create");
@@ -842,17 +972,20 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<kGlu, SRNL_ACT_SILU>(bn, m, a[bn == 128], h->sms, s)
                                                 : launch_product<kGlu, SRNL_ACT_GELU>(bn, m, a[bn == 128], h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward projections launch");
-  FfnArgs b[2] = {};
-  for (int i = 0; i < 2; ++i) {
-    add_product(b[i], M, D, 256 >> i, F, false, 0, 0, 0, false);
-    b[i].res = res != nullptr;
-    b[i].err = h->dev_err;
-  }
-  bn = pick_bn(b[0], b[1], h->sms);
+  const FfnArgs b = pick_launch(h->sms, true, bn, [&](int cols, int parts) {
+    FfnArgs l{};
+    add_product(l, M, D, cols, F, false, 0, 0, 0, false, parts);
+    l.res = res != nullptr;
+    l.res_at = static_cast<const bf16*>(res);
+    l.partial = h->partial;
+    l.arrived = h->arrived;
+    l.err = h->dev_err;
+    return l;
+  });
   ok = (res == nullptr || ffn_map(&m.in[0], res, D, M, 32)) && ffn_map(&m.a[0], h->hid, F, M, 128) &&
        ffn_map(&m.b[0], p->W_down, F, D, bn / 2) && ffn_map(&m.o[0], y, D, M, 32);
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  e = launch_product<kPlain, 0>(bn, m, b[bn == 128], h->sms, s);
+  e = launch_product<kPlain, 0>(bn, m, b, h->sms, s);
   return e == cudaSuccess ? SRNL_OK : ffn_cuda_fail(h, e, "feed-forward output launch");
 }
 
@@ -906,23 +1039,24 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward backward launch");
   // what is asked for of dx and the weights' gradients in one launch: the longest sums first, the
   // others' tiles fill up the SMs behind them
-  FfnArgs b[2] = {};
-  for (int i = 0; i < 2; ++i) {
-    const int cols = 256 >> i;
-    if (dx != nullptr) add_product(b[i], M, D, cols, F, true, 0, 0, 0, false);
-    if (g.W_gate != nullptr) add_product(b[i], F, D, cols, M, false, 2, 2, 1, true);
-    if (g.W_up != nullptr) add_product(b[i], F, D, cols, M, false, 3, 2, 2, true);
-    if (g.W_down != nullptr) add_product(b[i], D, F, cols, M, false, 4, 3, 3, true);
-    b[i].err = h->dev_err;
-  }
-  bn = pick_bn(b[0], b[1], h->sms);
+  const FfnArgs b = pick_launch(h->sms, dx != nullptr, bn, [&](int cols, int parts) {
+    FfnArgs l{};
+    if (dx != nullptr) add_product(l, M, D, cols, F, true, 0, 0, 0, false, parts);
+    if (g.W_gate != nullptr) add_product(l, F, D, cols, M, false, 2, 2, 1, true);
+    if (g.W_up != nullptr) add_product(l, F, D, cols, M, false, 3, 2, 2, true);
+    if (g.W_down != nullptr) add_product(l, D, F, cols, M, false, 4, 3, 3, true);
+    l.partial = h->partial;
+    l.arrived = h->arrived;
+    l.err = h->dev_err;
+    return l;
+  });
   ok = ffn_map(&m.a[0], h->dgate, F, M, 128) && ffn_map(&m.a[1], h->dup, F, M, 128) && ffn_map(&m.a[2], h->dgate, F, M, 64) &&
        ffn_map(&m.a[3], h->dup, F, M, 64) && ffn_map(&m.a[4], dy, D, M, 64) && ffn_map(&m.b[0], w.W_gate, D, F, 64) &&
        ffn_map(&m.b[1], w.W_up, D, F, 64) && ffn_map(&m.b[2], x, D, M, 64) && ffn_map(&m.b[3], h->hid, F, M, 64) &&
        (dx == nullptr || ffn_map(&m.o[0], dx, D, M, 32)) && (g.W_gate == nullptr || ffn_map(&m.o[1], g.W_gate, D, F, 32)) &&
        (g.W_up == nullptr || ffn_map(&m.o[2], g.W_up, D, F, 32)) && (g.W_down == nullptr || ffn_map(&m.o[3], g.W_down, F, D, 32));
   if (!ok) return ffn_fail(h, SRNL_E_CUDA, "a tensor map could not be encoded");
-  e = launch_product<kGrad, 0>(bn, m, b[bn == 128], h->sms, s);
+  e = launch_product<kGrad, 0>(bn, m, b, h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward gradients launch");
   return SRNL_OK;
 }

@@ -59,7 +59,9 @@ def within(got, ref, magnitude, spread2, K, slack=0.0):
 
 
 SHAPES = [(1, 8, 8), (3, 64, 128), (7, 72, 136), (16, 128, 256), (33, 264, 520), (64, 256, 1024), (128, 512, 648),
-          (129, 136, 1384), (256, 256, 256), (300, 520, 1384), (777, 1024, 2056), (2050, 264, 264)]
+          (129, 136, 1384), (256, 256, 256), (300, 520, 1384), (777, 1024, 2056), (2050, 264, 264),
+          # long sums over few tiles: K goes to the CTAs in parts
+          (40, 72, 2056), (65, 264, 4104), (301, 136, 4104), (300, 136, 4104), (34, 1096, 3000)]
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -209,9 +211,8 @@ def test_saturated_activations():
         assert bool((dx[0::2] == 400).all()) and bool((dx[1::2] == 0).all())
 
 
-@pytest.mark.parametrize("rows", [3, 200])
-def test_two_calls_a_stream_and_a_graph_give_equal_bits(rows):
-    dim, hidden = 264, 520
+@pytest.mark.parametrize("rows,dim,hidden", [(3, 264, 520), (200, 264, 520), (200, 264, 4104)])   # the last: K in parts
+def test_two_calls_a_stream_and_a_graph_give_equal_bits(rows, dim, hidden):
     t = make(rows, dim, hidden, seed=9)
     h = S.srnl_ffn_create(dict(dim=dim, hidden=hidden, max_rows=rows, training=True))
     h2 = S.srnl_ffn_create(dict(dim=dim, hidden=hidden, max_rows=rows, training=True))
