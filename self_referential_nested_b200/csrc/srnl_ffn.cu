@@ -792,7 +792,7 @@ FfnArgs pick_launch(int sms, bool may_cut, int& bn, const Build& build) {
     for (int parts = 1; parts <= (may_cut ? kMostParts : 1); ++parts) {
       const FfnArgs a = build(cols, parts);
       const FfnProduct& p = a.product[0];
-      if (parts > 1 && (p.tiles_m * p.tiles_n * parts > sms / 2 || p.k0 + p.k1 < parts)) continue;
+      if (parts > 1 && (p.tiles_m * p.tiles_n * parts > sms / 2 || p.k0 + p.k1 < parts)) break;
       const int64_t cost = launch_cost(a, cols, sms) + (parts > 1 ? 12 * (kCutStages + kPartStages * parts * cols / 256) : 0);
       if (cost < least) {
         least = cost;
