@@ -357,6 +357,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
   // the segment that holds the last token (the first one of an empty sequence) writes the state
   // that leaves, and has a third part of w b for it
   const bool exact = P.zn != nullptr && seg == (n > 0 ? (n - 1) / args.seg_len : 0);
+  const int chunks_z = exact ? chunks : chunks - 1;                 // those whose update of the state is of use
+  const bool fresh = P.z0 == nullptr && seg == 0;                   // the first chunk meets a zero state
 
   if (warp == 0) {
     if (lane == 0) {
@@ -403,6 +405,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         mbar_pass(&bar[kZ], ph, failed);
         mbar_pass(&bar[kOFree], ph ^ 1, failed);
         tmem_fence_after();
+        if (k > 0 || !fresh)
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -422,7 +425,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         for (int h = 0; h < NH; ++h)
 #pragma unroll
           for (int s = 0; s < 8; ++s)
-            mma_k16_tmem_a(tO + h * 64, tG + h * 128 + (s >> 1) * 32 + (s & 1) * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO, true);
+            mma_k16_tmem_a(tO + h * 64, tG + h * 128 + (s >> 1) * 32 + (s & 1) * 8, dc + (uint64_t)s * 128 + (uint64_t)h * kBox16, iO,
+                           s > 0 || k > 0 || !fresh);
         mma_commit(&bar[kO]);
         mma_commit(&bar[kFreeC]);
       }
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       const uint64_t dc = desc_mn_major(smem_u32(sc), kBoxBytes);
       const int uses = NH == 1 ? (exact ? 2 : 1) : exact ? 3 : 2;   // of a place of the parts in a chunk
 #pragma unroll 1
-      for (int k = 0; k < chunks; ++k) {
+      for (int k = 0; k < chunks_z; ++k) {
         mbar_pass(&bar[kFullC], k & 1, failed);
         if constexpr (NH == 1) {   // in TMEM, half the tokens a step; then the rest in the first part's place
           constexpr uint32_t iZ = idesc_mn(128, 128, false, true);
@@ -494,8 +498,9 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       const float f = exp2f(lg * (float)((rev ? kC - 1 - own : own) - (rev ? 32 * q : -32 * q) + c.lead));
       mbar_pass(&bar[kO2], ph, failed);
       tmem_fence_after();
+      if (k > 0 || !fresh)
 #pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
+        for (int cb = 0; cb < D / 32; ++cb) {
         float v[32];
         tmem_ld32(v, tR + cb * 32);
         tmem_wait_ld();
@@ -586,9 +591,11 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         }
         z[i] = v.x; z[i + 1] = v.y; z[i + 2] = v.z; z[i + 3] = v.w;
       }
+      if (!fresh) {
 #pragma unroll
-      for (int u = 0; u < Z / 8; ++u) put_z(u);
-      fence_async();
+        for (int u = 0; u < Z / 8; ++u) put_z(u);
+        fence_async();
+      }
       warp_arrive(&bar[kZ], lane);
     }
 #pragma unroll 1
@@ -610,6 +617,7 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
           warp_arrive(&bar[kClear], lane);
         }
       }
+      if (k == chunks_z) break;   // nobody asks for the state behind the last chunk
       mbar_pass(&bar[kFullB + ph], k >> 1 & 1, failed);
       if constexpr (NH == 1) {   // 64 tokens of 32 channels a warp
         const uint32_t tile = smem_u32(sb + ph * kTile);
