@@ -922,7 +922,10 @@ int la_groups(int heads, int d) { return d == 128 ? heads : (heads + 1) / 2; }
 
 int la_tc_segments(int T, int seqs, int sms) {
   const int chunks = (T + kC - 1) / kC, want = sms / seqs;
-  const int most = chunks / 2 > 1 ? chunks / 2 : 1;
+  // two chunks a segment at least, and six chunks: below, the two launches before the pass cost more
+  // than the chunks that follow one another (512 tokens, 4 heads of 64: 15.6 us whole, 18.6 cut; 1024:
+  // 28 and 19.7; 2048: 45 and 20)
+  const int most = chunks < 6 ? 1 : chunks / 2;
   return want < 1 ? 1 : want < most ? want : most;
 }
 
