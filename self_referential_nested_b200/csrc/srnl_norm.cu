@@ -118,9 +118,19 @@ __device__ __forceinline__ void load_weights(const float* p, int c, int dim, flo
   }
 }
 
-// Sums of N values over a row's lanes: LPR of a warp, or (LPR == 0) the block, by way of red
-// ([16 warps][N]; calls alternate between two of them, so that one barrier a call is enough).
-template <int LPR, int N>
+__device__ __forceinline__ uint32_t cluster_block() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums of N values over a row's lanes: LPR of a warp, or (LPR == 0) CL blocks, by way of red ([CL]
+// [kMostWarps][N] in each; calls alternate between two of them, so that one barrier a call is enough).
+constexpr int kLongWarps = 17, kMostWarps = 32;
+template <int LPR, int CL, int N>
 __device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
 #pragma unroll
   for (int o = (LPR == 0 ? 32 : LPR) / 2; o > 0; o >>= 1)
@@ -128,12 +138,28 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
     for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
   if constexpr (LPR == 0) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0)
+    if constexpr (CL == 1) {
+      if (lane == 0)
 #pragma unroll
-      for (int i = 0; i < N; ++i) red[warp * N + i] = s[i];
-    __syncthreads();
+        for (int i = 0; i < N; ++i) red[warp * N + i] = s[i];
+      __syncthreads();
+    } else {
+      // a warp's sums go to every block of the cluster
+      if (lane < CL) {
+        const uint32_t own = (uint32_t)__cvta_generic_to_shared(red + (cluster_block() * kMostWarps + warp) * N);
+        uint32_t to;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(own), "r"(lane));
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = lane < warps ? red[lane * N + i] : 0.f;
+        for (int i = 0; i < N; ++i) asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + 4 * i), "f"(s[i]) : "memory");
+      }
+      cluster_barrier();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      s[i] = 0.f;
+#pragma unroll
+      for (int k = 0; k < CL; ++k) s[i] += lane < warps ? red[(k * kMostWarps + lane) * N + i] : 0.f;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -141,28 +167,31 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
   }
 }
 
-constexpr int kLongThreads = 544;   // 8192 columns and an odd start: 1025 bf16 vectors by two, 2049 fp32 ones by four
+constexpr int kLongThreads = 32 * kLongWarps;   // 8192 columns and an odd start: 1025 bf16 vectors by two, 2049 fp32 ones by four
 // Most threads of a block, and the blocks whose registers an SM has to hold.
-__host__ __device__ constexpr int norm_threads(int lpr, int per, bool bwd) {
-  return lpr == 0 ? (per == 1 ? 256 : kLongThreads) : bwd ? 128 : 256;
+__host__ __device__ constexpr int norm_threads(int lpr, int per, int r, bool bwd) {
+  return lpr == 0 ? (per > 1 ? kLongThreads : r > 1 ? 256 : 1024) : bwd ? 128 : 256;
 }
-__host__ __device__ constexpr int norm_resident(int lpr, int per, bool bwd) {
-  return lpr == 0 ? (per == 1 ? (bwd ? 2 : 4) : (bwd ? 1 : 2)) : bwd ? 4 : 3;
+__host__ __device__ constexpr int norm_resident(int lpr, int per, int r, bool bwd) {
+  return lpr == 0 ? (per > 1 ? (bwd ? 1 : 2) : r > 1 ? (bwd ? 2 : 4) : 1) : bwd ? 4 : 3;
 }
 
-// LPR: lanes per row (0: a block); PER: vectors per lane; R: rows at once.
-template <typename T, int LPR, int PER, int R, bool ODD>
-__global__ void __launch_bounds__(norm_threads(LPR, PER, false), norm_resident(LPR, PER, false))
+// LPR: lanes per row (0: CL blocks, a cluster); PER: vectors per lane; R: rows at once.
+template <typename T, int LPR, int PER, int R, bool ODD, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, PER, R, false), norm_resident(LPR, PER, R, false))
     norm_forward_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
                         T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t rows,
                         int dim, float eps) {
   constexpr int V = 16 / sizeof(T), H = V / 2;
+  if constexpr (CL > 1) cluster_barrier();   // its blocks are all there
   // gamma and beta in registers, else from L1 for each R rows (an odd row's value by value)
   constexpr bool kKeep = LPR != 0 && PER * V <= (ODD ? 24 : 16);
-  __shared__ float red[LPR == 0 ? 2 * 18 * R : 1];
-  const int lanes = LPR == 0 ? blockDim.x : LPR, lane = LPR == 0 ? threadIdx.x : threadIdx.x % LPR;
-  const int64_t group = LPR == 0 ? blockIdx.x : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
-  const int64_t groups = LPR == 0 ? gridDim.x : (int64_t)gridDim.x * blockDim.x / LPR;
+  constexpr int kRed = CL * kMostWarps * R;
+  __shared__ float red[LPR == 0 ? 2 * kRed : 1];
+  const int lanes = LPR == 0 ? CL * blockDim.x : LPR;
+  const int lane = LPR != 0 ? threadIdx.x % LPR : CL == 1 ? threadIdx.x : cluster_block() * blockDim.x + threadIdx.x;
+  const int64_t group = LPR == 0 ? blockIdx.x / CL : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
+  const int64_t groups = LPR == 0 ? gridDim.x / CL : (int64_t)gridDim.x * blockDim.x / LPR;
   // of the warp's first group: all lanes of a warp make the same passes
   const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (threadIdx.x % 32) / LPR;
   const int c0 = lane * V - (ODD ? (int)(group * dim % V) : 0), cs = lanes * V;
@@ -206,7 +235,7 @@ __global__ void __launch_bounds__(norm_threads(LPR, PER, false), norm_resident(L
       s[q] = t.x + t.y;
     }
     if (LPR == 0) load(r0 + groups * R);   // a block waits on its barriers: the next rows are on their way meanwhile
-    row_sum<LPR, R>(s, red);
+    row_sum<LPR, CL, R>(s, red);
     float mean[R];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -229,7 +258,7 @@ __global__ void __launch_bounds__(norm_threads(LPR, PER, false), norm_resident(L
       }
       s[q] = t.x + t.y;
     }
-    row_sum<LPR, R>(s, red + (LPR == 0 ? 18 * R : 0));
+    row_sum<LPR, CL, R>(s, red + (LPR == 0 ? kRed : 0));
 #pragma unroll
     for (int q = 0; q < R; ++q) s[q] = rsqrtf(s[q] * inv_d + eps);
 #pragma unroll
@@ -263,21 +292,25 @@ __global__ void __launch_bounds__(norm_threads(LPR, PER, false), norm_resident(L
       }
     }
   }
+  if constexpr (CL > 1) cluster_barrier();   // no block leaves while another may still write to it
 }
 
 // dx per row, and per block the partial sums of dgamma and dbeta: part[block][2][dim].
-template <typename T, int LPR, int PER, int R, bool ODD>
-__global__ void __launch_bounds__(norm_threads(LPR, PER, true), norm_resident(LPR, PER, true))
+template <typename T, int LPR, int PER, int R, bool ODD, int CL>
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, PER, R, true), norm_resident(LPR, PER, R, true))
     norm_backward_kernel(const T* __restrict__ x, const T* __restrict__ dy, const T* __restrict__ dres,
                          const float* __restrict__ gamma, const float* __restrict__ mean_in,
                          const float* __restrict__ rstd_in, T* __restrict__ dx, float* __restrict__ part,
                          int64_t rows, int dim) {
   constexpr int V = 16 / sizeof(T), H = V / 2;
+  if constexpr (CL > 1) cluster_barrier();   // its blocks are all there
   extern __shared__ float fold[];   // [warps][2][dim]: groups of different warps share columns
-  __shared__ float red[LPR == 0 ? 2 * 18 * 2 * R : 1];
-  const int lanes = LPR == 0 ? blockDim.x : LPR, lane = LPR == 0 ? threadIdx.x : threadIdx.x % LPR;
-  const int64_t group = LPR == 0 ? blockIdx.x : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
-  const int64_t groups = LPR == 0 ? gridDim.x : (int64_t)gridDim.x * blockDim.x / LPR;
+  constexpr int kRed = CL * kMostWarps * 2 * R;
+  __shared__ float red[LPR == 0 ? 2 * kRed : 1];
+  const int lanes = LPR == 0 ? CL * blockDim.x : LPR;
+  const int lane = LPR != 0 ? threadIdx.x % LPR : CL == 1 ? threadIdx.x : cluster_block() * blockDim.x + threadIdx.x;
+  const int64_t group = LPR == 0 ? blockIdx.x / CL : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
+  const int64_t groups = LPR == 0 ? gridDim.x / CL : (int64_t)gridDim.x * blockDim.x / LPR;
   const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (threadIdx.x % 32) / LPR;
   const int sh = ODD ? (int)(group * dim % V) : 0, c0 = lane * V - sh, cs = lanes * V;
   const float inv_d = 1.f / (float)dim;
@@ -313,8 +346,8 @@ __global__ void __launch_bounds__(norm_threads(LPR, PER, true), norm_resident(LP
     }
   };
   // Between a block's barriers its next rows are on their way; not with two bf16 vectors a lane,
-  // whose sums leave no registers for it (8192 columns: 139 us without, 175 us with).
-  constexpr bool kAhead = LPR == 0 && PER * V < (sizeof(T) == 2 ? 16 : 32);
+  // whose sums leave no registers for it.
+  constexpr bool kAhead = LPR == 0 && PER * V < 16;
   if (kAhead) load(group);
   for (int64_t r0 = group, base = lead; base < rows; r0 += groups * R, base += groups * R, flip ^= 1) {
     float s[2 * R], f[R];
@@ -360,7 +393,7 @@ __global__ void __launch_bounds__(norm_threads(LPR, PER, true), norm_resident(LP
       for (int i = 0; i < PER; ++i) res[q][i] = er[q][i];
     }
     if (kAhead) load(r0 + groups * R);
-    row_sum<LPR, 2 * R>(s, red + (LPR == 0 ? 18 * 2 * R * flip : 0));
+    row_sum<LPR, CL, 2 * R>(s, red + (LPR == 0 ? kRed * flip : 0));
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       const int64_t r = r0 + q * groups;
@@ -379,9 +412,10 @@ __global__ void __launch_bounds__(norm_threads(LPR, PER, true), norm_resident(LP
     }
   }
   asm volatile("griddepcontrol.launch_dependents;");
+  if constexpr (CL > 1) cluster_barrier();   // no block leaves while another may still write to it
   // groups in one order: those of a warp with equal columns, then the warps; an odd row's groups
   // start at different columns, so each adds its own in turn
-  float* mine = part + (int64_t)blockIdx.x * 2 * dim;
+  float* mine = part + (int64_t)(blockIdx.x / CL) * 2 * dim;
   auto put = [&](float* to, bool add) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
@@ -454,11 +488,12 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* __r
 
 // The lanes a row length takes.
 struct NormPlan {
-  int lpr, per, threads;   // threads of a block per row (lpr == 0)
+  int lpr, per, threads;   // threads of a block (lpr == 0)
+  int blocks;              // blocks a row (lpr == 0)
   bool odd;                // rows that are not whole 16-byte vectors
 };
 
-NormPlan norm_plan(int dim, int esize) {
+NormPlan norm_plan(int dim, int esize, bool bwd) {
   NormPlan p{};
   const int V = 16 / esize;
   p.odd = dim % V != 0;
@@ -472,8 +507,13 @@ NormPlan norm_plan(int dim, int esize) {
   else if (n <= 128) { p.lpr = 32; p.per = 4; }
   else {
     p.lpr = 0;
-    p.per = n <= 256 ? 1 : n <= 2 * kLongThreads ? 2 : 4;
-    p.threads = ((n + p.per - 1) / p.per + 31) / 32 * 32;
+    // The backward pass keeps its sums in registers.  fp32: a second block for the longest rows,
+    // where four vectors a lane would not fit (2000 x 8192: 90 us in one block, 71 in two; forward
+    // it would cost: 25 and 46).  bf16: a vector a lane, so that the next row's loads fit (2000 x
+    // 8192: 49 us with two, @@ with one), but for odd rows, which may touch 1025 of them.
+    p.blocks = bwd && esize == 4 && n > 2 * kLongThreads ? 2 : 1;
+    p.per = n <= 256 || (bwd && esize == 2 && !p.odd) ? 1 : n <= 2 * kLongThreads * p.blocks ? 2 : 4;
+    p.threads = ((n + p.per * p.blocks - 1) / (p.per * p.blocks) + 31) / 32 * 32;
   }
   return p;
 }
@@ -481,25 +521,27 @@ NormPlan norm_plan(int dim, int esize) {
 // Blocks of a call: what the SMs hold at once, or fewer for few rows; groups a multiple of 8 (a
 // vector's values), which an odd row's groups rely on.
 int norm_blocks(const NormPlan& p, int threads, int64_t rows, int sms, int per_sm) {
-  const int per_block = p.lpr == 0 ? 1 : threads / p.lpr;
-  const int64_t need = (rows + per_block - 1) / per_block, most = (int64_t)sms * per_sm;
-  const int blocks = (int)(need < most ? need : most);
-  return p.odd && per_block % 8 != 0 ? (blocks + 7) / 8 * 8 : blocks;
+  const int per_block = p.lpr == 0 ? 1 : threads / p.lpr, each = p.lpr == 0 ? p.blocks : 1;
+  const int64_t need = (rows + per_block - 1) / per_block, most = (int64_t)sms * per_sm / each;
+  int n = (int)(need < most ? need : most);
+  if (p.odd && per_block % 8 != 0) n = n < 8 || (n + 7) / 8 * 8 <= most ? (n + 7) / 8 * 8 : n / 8 * 8;   // never a few more than fit at once
+  return n * each;
 }
 
 // Short rows go several at a time, so that a lane has two to four vectors in flight.
 #define SRNL_NORM_PLAN(T, ODD, FWD, CALL)                                  \
   do {                                                                     \
-    if (p.lpr == 8) { CALL(T, 8, 1, (FWD ? 4 : 2), ODD); }                 \
-    else if (p.lpr == 16 && p.per == 1) { CALL(T, 16, 1, (FWD ? 4 : 2), ODD); } \
-    else if (p.lpr == 16 && p.per == 2) { CALL(T, 16, 2, (FWD ? 2 : 1), ODD); } \
-    else if (p.lpr == 16) { CALL(T, 16, 3, 1, ODD); }                      \
-    else if (p.lpr == 32 && p.per == 2) { CALL(T, 32, 2, (FWD ? 2 : 1), ODD); } \
-    else if (p.lpr == 32 && p.per == 3) { CALL(T, 32, 3, 1, ODD); }        \
-    else if (p.lpr == 32) { CALL(T, 32, 4, 1, ODD); }                      \
-    else if (p.per == 1) { CALL(T, 0, 1, 2, ODD); }                        \
-    else if (p.per == 2) { CALL(T, 0, 2, 1, ODD); }                        \
-    else if (sizeof(T) == 4) { CALL(T, 0, (sizeof(T) == 4 ? 4 : 2), 1, ODD); } \
+    if (p.lpr == 8) { CALL(T, 8, 1, (FWD ? 4 : 2), ODD, 1); }                 \
+    else if (p.lpr == 16 && p.per == 1) { CALL(T, 16, 1, (FWD ? 4 : 2), ODD, 1); } \
+    else if (p.lpr == 16 && p.per == 2) { CALL(T, 16, 2, (FWD ? 2 : 1), ODD, 1); } \
+    else if (p.lpr == 16) { CALL(T, 16, 3, 1, ODD, 1); }                      \
+    else if (p.lpr == 32 && p.per == 2) { CALL(T, 32, 2, (FWD ? 2 : 1), ODD, 1); } \
+    else if (p.lpr == 32 && p.per == 3) { CALL(T, 32, 3, 1, ODD, 1); }        \
+    else if (p.lpr == 32) { CALL(T, 32, 4, 1, ODD, 1); }                      \
+    else if (p.per == 1 && p.threads <= 256) { CALL(T, 0, 1, 2, ODD, 1); }  \
+    else if (p.per == 1) { CALL(T, 0, 1, (FWD || sizeof(T) == 4 ? 2 : 1), ODD, 1); } \
+    else if (p.per == 2 && p.blocks == 1) { CALL(T, 0, 2, 1, ODD, 1); }    \
+    else if (sizeof(T) == 4) { CALL(T, 0, (sizeof(T) == 4 && FWD ? 4 : 2), 1, ODD, (sizeof(T) == 4 && !FWD ? 2 : 1)); } \
   } while (0)
 #define SRNL_NORM_DISPATCH(FWD, CALL)                                      \
   do {                                                                     \
@@ -516,7 +558,7 @@ int norm_blocks(const NormPlan& p, int threads, int64_t rows, int sms, int per_s
 struct srnl_ln {
   srnl_ln_config cfg{};
   int device = 0, sms = 0;
-  srnl::NormPlan plan{};
+  srnl::NormPlan fwd{}, bwd{};
   int fwd_per_sm = 1, bwd_per_sm = 1;   // blocks an SM holds
   float* part = nullptr;                // [bwd_per_sm * sms + 8][2][dim]
   char err[256] = "";
@@ -568,22 +610,31 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
   srnl_ln* h = new (std::nothrow) srnl_ln;
   if (h == nullptr) return ln_fail(nullptr, SRNL_E_NOMEM, "host allocation failed");
   h->cfg = *cfg;
-  h->plan = srnl::norm_plan(cfg->dim, cfg->act_dtype == SRNL_BF16 ? 2 : 4);
+  h->fwd = srnl::norm_plan(cfg->dim, cfg->act_dtype == SRNL_BF16 ? 2 : 4, false);
+  h->bwd = srnl::norm_plan(cfg->dim, cfg->act_dtype == SRNL_BF16 ? 2 : 4, true);
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) {
-    const srnl::NormPlan& p = h->plan;
     const bool bf16 = cfg->act_dtype == SRNL_BF16;
-    const int ft = p.lpr == 0 ? p.threads : 256, bt = p.lpr == 0 ? p.threads : 128;
-    const size_t smem = p.lpr == 0 ? 0 : (size_t)(bt / 32) * 2 * cfg->dim * sizeof(float);
-#define SRNL_NORM_OCC(T, LPR, PER, R, ODD)                                                                             \
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD>, ft, 0)
-    SRNL_NORM_DISPATCH(true, SRNL_NORM_OCC);
+    {
+      const srnl::NormPlan& p = h->fwd;
+      const int threads = p.lpr == 0 ? p.threads : 256;
+#define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                             \
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>,    \
+                                                    threads, 0)
+      SRNL_NORM_DISPATCH(true, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
-#define SRNL_NORM_OCC(T, LPR, PER, R, ODD)                                                                             \
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD>, bt, smem)
-    if (e == cudaSuccess) SRNL_NORM_DISPATCH(false, SRNL_NORM_OCC);
+    }
+    if (e == cudaSuccess) {
+      const srnl::NormPlan& p = h->bwd;
+      const int threads = p.lpr == 0 ? p.threads : 128;
+      const size_t smem = p.lpr == 0 ? 0 : (size_t)(threads / 32) * 2 * cfg->dim * sizeof(float);
+#define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                             \
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>,   \
+                                                    threads, smem)
+      SRNL_NORM_DISPATCH(false, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
+    }
     if (h->fwd_per_sm < 1) h->fwd_per_sm = 1;
     if (h->bwd_per_sm < 1) h->bwd_per_sm = 1;
     if (h->bwd_per_sm > srnl::kNormBlocks) h->bwd_per_sm = srnl::kNormBlocks;
@@ -622,11 +673,11 @@ srnl_status srnl_ln_forward(srnl_ln* h, const void* x, const float* gamma, const
   }
   const srnl_status st = ln_device(h);
   if (st != SRNL_OK) return st;
-  const srnl::NormPlan& p = h->plan;
+  const srnl::NormPlan& p = h->fwd;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int threads = p.lpr == 0 ? p.threads : 256, blocks = srnl::norm_blocks(p, threads, rows, h->sms, h->fwd_per_sm);
-#define SRNL_NORM_RUN(T, LPR, PER, R, ODD)                                                      \
-  srnl::norm_forward_kernel<T, LPR, PER, R, ODD><<<blocks, threads, 0, s>>>(                    \
+#define SRNL_NORM_RUN(T, LPR, PER, R, ODD, CL)                                                      \
+  srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL><<<blocks, threads, 0, s>>>(                    \
       static_cast<const T*>(x), gamma, beta, static_cast<T*>(y), mean, rstd, rows, dim, h->cfg.eps)
   SRNL_NORM_DISPATCH(true, SRNL_NORM_RUN);
 #undef SRNL_NORM_RUN
@@ -659,13 +710,13 @@ srnl_status srnl_ln_backward(srnl_ln* h, const void* x, const void* dy, const vo
   }
   const srnl_status st = ln_device(h);
   if (st != SRNL_OK) return st;
-  const srnl::NormPlan& p = h->plan;
+  const srnl::NormPlan& p = h->bwd;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int threads = p.lpr == 0 ? p.threads : 128, blocks = srnl::norm_blocks(p, threads, rows, h->sms, h->bwd_per_sm);
   if (rows > 0) {
     const size_t smem = p.lpr == 0 ? 0 : (size_t)(threads / 32) * 2 * dim * sizeof(float);
-#define SRNL_NORM_RUN(T, LPR, PER, R, ODD)                                                                     \
-  srnl::norm_backward_kernel<T, LPR, PER, R, ODD><<<blocks, threads, smem, s>>>(                               \
+#define SRNL_NORM_RUN(T, LPR, PER, R, ODD, CL)                                                                     \
+  srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL><<<blocks, threads, smem, s>>>(                               \
       static_cast<const T*>(x), static_cast<const T*>(dy), static_cast<const T*>(dres), gamma, mean, rstd,     \
       static_cast<T*>(dx), h->part, rows, dim)
     SRNL_NORM_DISPATCH(false, SRNL_NORM_RUN);
@@ -683,7 +734,8 @@ srnl_status srnl_ln_backward(srnl_ln* h, const void* x, const void* dy, const vo
     at.val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = &at;
     lc.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&lc, srnl::norm_weight_grad_kernel, static_cast<const float*>(h->part), blocks,
+    const cudaError_t e = cudaLaunchKernelEx(&lc, srnl::norm_weight_grad_kernel, static_cast<const float*>(h->part),
+                                             p.lpr == 0 ? blocks / p.blocks : blocks,
                                              dim, dgamma, dbeta);
     if (e != cudaSuccess) return ln_cuda_fail(h, e, "layer norm weight gradient launch");
   }
