@@ -68,17 +68,38 @@ __device__ __forceinline__ uint4 repack(const float2* v) {
   }
 }
 
-// The V values at column c of a row (c < 0 or c + V > dim only for odd rows: the rest is zero).
-template <typename T, bool ODD>
-__device__ __forceinline__ uint4 load_cols(const T* row, int c, int dim) {
+// The 16-byte unit at column c of a row.  An odd row's units at its ends hold values of its
+// neighbours too.  They are read whole and the neighbours' values taken out once they have arrived
+// (clip): value by value a lane packs bf16 ones, and so waits for each unit in turn (8000 x 1533
+// backward: 81 us, 48 whole).  fp32 ones need no packing, and blocks of long rows take them value by
+// value (44 us whole, 41 so).  Behind the last row there is nothing to read.
+template <typename T, int LPR, bool ODD>
+__host__ __device__ constexpr bool whole_units() { return ODD && (sizeof(T) == 2 || LPR != 0); }
+
+template <typename T, int LPR, bool ODD>
+__device__ __forceinline__ uint4 load_cols(const T* row, int c, int dim, bool last) {
   constexpr int V = 16 / sizeof(T);
-  if (!ODD || (c >= 0 && c + V <= dim)) return *reinterpret_cast<const uint4*>(row + c);
+  constexpr bool kWhole = whole_units<T, LPR, ODD>();
+  if (!ODD || (c + V <= dim && (kWhole || c >= 0)) || (kWhole && !last)) return *reinterpret_cast<const uint4*>(row + c);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < V; ++e)
     if (c + e >= 0 && c + e < dim) {
       if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)__bfloat16_as_ushort(row[c + e]) << (16 * (e & 1));
       else w[e] = __float_as_uint(row[c + e]);
+    }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <typename T, int LPR, bool ODD>
+__device__ __forceinline__ uint4 clip(const uint4& raw, int c, int dim) {
+  constexpr int V = 16 / sizeof(T);
+  if (!whole_units<T, LPR, ODD>() || (c >= 0 && c + V <= dim)) return raw;
+  uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (c + e < 0 || c + e >= dim) {
+      if constexpr (sizeof(T) == 2) w[e >> 1] &= e & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+      else w[e] = 0u;
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -215,7 +236,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
       for (int i = 0; i < PER; ++i) {
         raw[q][i] = make_uint4(0u, 0u, 0u, 0u);
         const int64_t r = from + q * groups;
-        if (on[i] && r < rows) raw[q][i] = load_cols<T, ODD>(x + r * dim, c0 + i * cs, dim);
+        if (on[i] && r < rows) raw[q][i] = load_cols<T, LPR, ODD>(x + r * dim, c0 + i * cs, dim, r + 1 == rows);
       }
   };
   if (LPR == 0) load(group);
@@ -228,7 +249,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
       float2 t = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        unpack<T>(raw[q][i], v[q] + i * H);
+        unpack<T>(clip<T, LPR, ODD>(raw[q][i], c0 + i * cs, dim), v[q] + i * H);
 #pragma unroll
         for (int e = 0; e < H; ++e) t = __fadd2_rn(t, v[q][i * H + e]);
       }
@@ -338,9 +359,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
       for (int i = 0; i < PER; ++i) {
         xr[q][i] = yr[q][i] = er[q][i] = make_uint4(0u, 0u, 0u, 0u);
         if (on[i] && r < rows) {
-          xr[q][i] = load_cols<T, ODD>(x + r * dim, c0 + i * cs, dim);
-          yr[q][i] = load_cols<T, ODD>(dy + r * dim, c0 + i * cs, dim);
-          if (dres != nullptr) er[q][i] = load_cols<T, ODD>(dres + r * dim, c0 + i * cs, dim);
+          xr[q][i] = load_cols<T, LPR, ODD>(x + r * dim, c0 + i * cs, dim, r + 1 == rows);
+          yr[q][i] = load_cols<T, LPR, ODD>(dy + r * dim, c0 + i * cs, dim, r + 1 == rows);
+          if (dres != nullptr) er[q][i] = load_cols<T, LPR, ODD>(dres + r * dim, c0 + i * cs, dim, r + 1 == rows);
         }
       }
     }
@@ -353,7 +374,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
     float s[2 * R], f[R];
     uint4 res[R][PER];
     if (!kAhead) load(r0);
-    // values past a row's ends have dy = 0 and add nothing to any sum
+    // values past a row's ends are zeros in x and dy and add nothing to any sum
     float2 xh[R][PER * H], w[R][PER * H];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -361,8 +382,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         float2 xv[H], yv[H], gw[H];
-        unpack<T>(xr[q][i], xv);
-        unpack<T>(yr[q][i], yv);
+        unpack<T>(clip<T, LPR, ODD>(xr[q][i], c0 + i * cs, dim), xv);
+        unpack<T>(clip<T, LPR, ODD>(yr[q][i], c0 + i * cs, dim), yv);
         if (!on[i]) {
 #pragma unroll
           for (int e = 0; e < H; ++e) gw[e] = make_float2(0.f, 0.f);
@@ -510,7 +531,7 @@ NormPlan norm_plan(int dim, int esize, bool bwd) {
     // The backward pass keeps its sums in registers.  fp32: a second block for the longest rows,
     // where four vectors a lane would not fit (2000 x 8192: 90 us in one block, 71 in two; forward
     // it would cost: 25 and 46).  bf16: a vector a lane, so that the next row's loads fit (2000 x
-    // 8192: 49 us with two, @@ with one), but for odd rows, which may touch 1025 of them.
+    // 8192: 49 us with two, 41 with one), but for odd rows, which may touch 1025 of them.
     p.blocks = bwd && esize == 4 && n > 2 * kLongThreads ? 2 : 1;
     p.per = n <= 256 || (bwd && esize == 2 && !p.odd) ? 1 : n <= 2 * kLongThreads * p.blocks ? 2 : 4;
     p.threads = ((n + p.per * p.blocks - 1) / (p.per * p.blocks) + 31) / 32 * 32;

@@ -165,6 +165,30 @@ def test_a_row_touches_no_other(dim):
     assert float((y1[30] - t["beta"]).abs().max()) <= 43 * U * 2.5 * 1000 * float(t["gamma"].abs().max())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [9, 33, 301, 509, 1533, 4097, 8191])
+def test_an_odd_row_keeps_its_neighbours_out(dim, dtype):
+    """Rows share 16-byte units with their neighbours where the row's length is odd: rows of NaN and
+    infinity in x, dy and dres change no bit of the rows beside them, forward or backward."""
+    t = make(37, dim, dtype, seed=6)
+    h = S.srnl_ln_create(dict(dim=dim, act_dtype=dtype))
+    bad = [0, 2, 17, 35]
+    keep = [i for i in range(37) if i not in bad]
+    try:
+        outs = []
+        for spoil in (False, True):
+            if spoil:
+                t["x"][bad], t["dy"][bad], t["dres"][bad] = float("nan"), float("inf"), float("nan")
+            y, mean, rstd = forward(h, t)
+            dx = torch.empty_like(t["x"])
+            S.srnl_ln_backward(h, t["x"], t["dy"], t["gamma"], mean, rstd, dx, dres=t["dres"])
+            outs.append((y[keep], mean[keep], rstd[keep], dx[keep]))
+        for a, b in zip(*outs):
+            assert torch.equal(a, b) and bool(torch.isfinite(a).all())
+    finally:
+        h.close()
+
+
 def test_large_offset_keeps_the_spread():
     """The variance is taken from the centred values: an offset of 4096 spreads leaves it right."""
     x = torch.randn(64, 512, generator=torch.Generator().manual_seed(1)).cuda() + 4096.0
