@@ -497,7 +497,8 @@ typedef enum { SRNL_ACT_SILU = 0, SRNL_ACT_GELU = 1 } srnl_activation;
 typedef struct {
   int dim, hidden;  /* widths of x and of the hidden layer: multiples of 8, at most 65536 */
   int max_rows;     /* most rows of a call, at most 2^24: the workspace holds max_rows x hidden
-                       bf16 values, three times that in training */
+                       bf16 values, three times that in training, and 256 x 256 fp32 sums for
+                       every two SMs */
   int activation;   /* srnl_activation */
   int act_dtype;    /* SRNL_BF16 */
   int training;     /* nonzero: the handle can run the backward pass */
@@ -522,8 +523,9 @@ SRNL_API srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg)
 /* Forward pass.  DEVICE pointers, dense bf16, 16-byte aligned: x, y [rows][dim]; res, the
  * residual added to y, [rows][dim] or NULL; gate, up [rows][hidden] receive the
  * pre-activations x Wg^T and x Wu^T for the backward pass, both or neither.  Outputs overlap
- * neither inputs nor one another.  0 <= rows <= max_rows; 0 does nothing.  Asynchronous on
- * `stream`; calls on one handle must not overlap on the device (they share its workspace). */
+ * neither inputs nor one another.  0 <= rows <= max_rows; 0 does nothing.  Equal inputs give
+ * equal bits.  Asynchronous on `stream`; calls on one handle must not overlap on the device (they
+ * share its workspace). */
 SRNL_API srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* params, const void* res,
                                       void* y, void* gate, void* up, int rows, void* stream);
 
@@ -569,7 +571,7 @@ SRNL_API srnl_status srnl_lattn_create(srnl_lattn** out, const srnl_lattn_config
 
 /* Forward pass.  DEVICE pointers, 16-byte aligned: q, k, v bf16 [B][T] rows, ld elements apart;
  * o bf16 [B][T][heads x d], dense.  lengths: int32 [B] on the device or NULL (T everywhere);
- * a sequence's tokens from its length on are neither read nor written (a length is clamped to
+ * a sequence's tokens from its length on are neither used nor written (a length is clamped to
  * 0..T).  state_in: fp32 [B][heads][d][d] (rows of k, columns of v), the memory before the
  * first token, or NULL for zeros; state_out: the memory after the last one, or NULL.  Outputs
  * overlap neither inputs nor one another.  A NaN or infinity in a token may reach the outputs

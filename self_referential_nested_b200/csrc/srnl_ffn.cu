@@ -19,7 +19,9 @@
 // thread fills a ring of 64-wide K stages by TMA (128-byte swizzle; a ragged edge reads as
 // zeros), one thread of the leading CTA issues the products into one of two accumulators in
 // TMEM, and eight warps empty the other.  Results leave by TMA from per-warp staging tiles,
-// which clips them at the edges.
+// which clips them at the edges.  8192 rows, 2048 x 5632: forward 440 us (1290 TF/s), backward 940
+// (1205 TF/s), bound by the tensor cores under the power limit, but for kGluBack, whose epilogue moves
+// 461 MB; 12544 rows, 256 x 1024, both pre-activations kept: 39 us, bound by the epilogue.
 //
 // Roundings: h, dgate and dup are rounded to bf16 between the products, as the tensor cores
 // take them; everything else is rounded once, on output.  gate and up are kept in bf16 for the
@@ -567,7 +569,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
 // consecutive values of K in one 16-byte load of each row and the two products of a 32-wide piece
 // use them as they lie; the tokens are loaded by the same rule, and nothing passes through shared
 // memory but the warps' sums.  Small blocks (8 channels; 5 to an SM) come out even over the SMs:
-// 5632 channels are 704 of them.
+// 5632 channels are 704 of them.  4 rows, 2048 x 5632 (69 MB): 16.8 us, 4.1 TB/s; 32 rows: 34 us, where
+// the tiles' kernel takes 35.
 constexpr int kFewRows = 32;
 
 __device__ __forceinline__ uint4 load_once(const bf16_t* p) {   // weights are met once: not kept in L1

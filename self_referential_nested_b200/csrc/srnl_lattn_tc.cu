@@ -10,17 +10,25 @@
 // All five are tcgen05 products with accumulators in TMEM.  a, b and c arrive by TMA as 64-channel
 // boxes, 128-byte rows, and serve as they lie, K-major where channels are summed over and
 // MN-major where tokens are.  The masked G goes back to TMEM over G's own columns as the left
-// operand of (3).  Roles: one thread loads, two issue products (those of the rows, and (5), whose
-// chain of decayed b, dZ and Z goes on beside them), four warps own a token's row per thread
-// (masking, O), eight half a row of the state per thread, in fp32 registers (the decayed b, Z).
-// Z and w b are split into two bf16 parts (a third of w b where the state itself is asked for).
+// operand of (3), and so does w b for (5) where TMEM has room (128-wide heads; narrower ones keep it
+// in a ring in shared memory).  O leaves through a's tile.  Roles: two threads load, two issue
+// products (those of the rows, and (5), whose chain of decayed b, dZ and Z goes on beside them), four
+// warps a head own a token's row per thread (masking, O), eight half a row of the state per thread,
+// in fp32 registers (the decayed b, Z).  Z and w b are split into two bf16 parts (a third of w b where
+// the state itself is asked for).
 //
 // Two heads of up to 64 channels share a CTA so that every product has 128 rows; (5) computes
 // the two heads' cross terms with it and nobody reads them.  A 32-wide head runs as a 64-wide one
 // whose upper half the loads fill with zeros and the stores leave out.
 //
-// What bounds it: the chain of a chunk (products, masking and the state's update wait for one
-// another, about 2 us) where few sequences run, memory where many do.
+// What bounds it: a chunk's operands, parts and results pass through shared memory about 4400 times
+// 128 bytes (5400 for narrow heads), two thirds of the 7000 cycles that a chunk takes; the rest is the
+// chain of products, masking and the state's update, which wait for one another.  One sequence of
+// 16384 tokens, 16 heads of 128: 112 us (2.4 TB/s; 31 of them the segments' states); backward of 8 x
+// 2048 tokens, 16 heads of 64, lengths at random: 62 us (3.8 TB/s).
+//
+// Sequences that leave SMs idle are cut into segments.  One kernel sums what each segment adds to
+// the state, a second turns the sums into the states they start from, and the pass itself follows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -3,8 +3,8 @@
 Tolerances.  u = 2^-24 is half an fp32 step.  A row's sum is at most 32 additions in a lane and
 10 across lanes, so a sum is off by at most 42 u times the sum of magnitudes; a product or a
 difference adds u each, rsqrtf 2 u.  An output rounded to its type adds eps / 2 of its value.  A
-column's sum over rows is at most rows / 148 + 8 + 19 + 32 additions (blocks' rows, a block's
-warps, 592 partials over 32 warps), under 200 for the rows used here.
+column's sum over rows is at most rows / 148 + 8 + 4 + 37 + 32 additions (a block's rows, its groups and
+warps, 1184 partials over 32 warps), under 200 for the rows used here.
 """
 import numpy as np
 import pytest
