@@ -30,6 +30,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
@@ -93,12 +94,14 @@ struct FfnProduct {
   int M, N, tiles_m, tiles_n;
   int k0, k1;            // stages of the first and of the second operand pair
   int a, b, o, a_mn;
-  int parts;             // K is cut into so many, each a tile of its own; at most one product of a launch
+  int parts;             // K is cut into so many, each a tile of its own; one number above 1 in a launch
+  int slot;              // tiles of cut products before its own
 };
 
 struct FfnArgs {
   FfnProduct product[4];
   int products, tiles;
+  int slots;             // tiles of cut products
   int save, res;         // kGlu: gate and up are kept; kPlain: in[0] is added
   const bf16_t* res_at;  // the same as in[0]
   float* partial;        // the sums of a cut product's parts: [tile][CTA][warp][part][32 rows x columns]
@@ -184,7 +187,7 @@ __device__ __forceinline__ int stage_of(const FfnProduct& p, int part) {
 }
 
 // B lies K-major forward (weights' rows along K) and MN-major backward.  A lies K-major but for the
-// weights' gradients, which share a launch (kGrad) with the input's.  CUT: the first product's K
+// weights' gradients, which share a launch (kGrad) with the input's.  CUT: the K of some products
 // comes in parts; a kernel of its own, since the others lost 6 us at 1531 x 520 x 1384 to code that
 // they do not run.
 template <int EPI, int ACT, int BN, bool CUT>
@@ -444,7 +447,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFfnThreads, 1)
         // of a cut product: this part's sums go to memory; who comes last adds up all parts, in
         // their order, and goes on with the sum
         const bool cut = CUT && P.parts > 1;
-        const int64_t slot = ((int64_t)T.n * 2 + rank) * kEpiWarps + ew;
+        const int64_t slot = ((int64_t)(P.slot + T.n) * 2 + rank) * kEpiWarps + ew;
         float4* mine = reinterpret_cast<float4*>(args.partial + slot * P.parts * (32 * kHalf)) + lane;
         constexpr int kPart = 32 * kHalf / 4;
         bool finish = true;
@@ -713,7 +716,7 @@ cudaError_t launch_product(int bn, const FfnMaps& maps, const FfnArgs& a, int sm
   const int pairs = a.tiles < sms / 2 ? a.tiles : sms / 2;
   const dim3 grid(2 * pairs);
   if constexpr (EPI == kPlain || EPI == kGrad) {
-    if (a.product[0].parts > 1)
+    if (a.slots > 0)
       return bn == 256 ? launch_after(ffn_product_kernel<EPI, ACT, 256, true>, grid, kFfnThreads, ffn_smem(EPI, 256), s, maps, a)
                        : launch_after(ffn_product_kernel<EPI, ACT, 128, true>, grid, kFfnThreads, ffn_smem(EPI, 128), s, maps, a);
   }
@@ -739,25 +742,33 @@ void add_product(FfnArgs& a, int64_t M, int64_t N, int cols, int64_t K, bool two
   p.k0 = ceil_div(K, kTileK); p.k1 = two ? p.k0 : 0;
   p.a = am; p.b = bm; p.o = om; p.a_mn = a_mn;
   p.parts = parts;
+  p.slot = a.slots;
+  if (parts > 1) a.slots += p.tiles_m * p.tiles_n;
   a.tiles += p.tiles_m * p.tiles_n * parts;
 }
 
-// Most stages that a pair of CTAs has in a launch.
+// Most stages that a pair of CTAs has in a launch.  Tiles go to the pairs in turn: each pair has
+// n / pairs of a product's n, and one more from where the product begins, around the pairs; the
+// busiest is one that some product begins with.
 int64_t longest_pair(const FfnArgs& a, int pairs) {
-  int64_t all = 0, most = 0;   // tiles go to the pairs in turn: the first pair has the most of each product
+  int64_t all = 0, most = 0;
   for (int i = 0; i < a.products; ++i) {
     const FfnProduct& p = a.product[i];
-    const int n = p.tiles_m * p.tiles_n * p.parts, after = (p.first + n + pairs - 1) / pairs, before = (p.first + pairs - 1) / pairs;
-    const int k = ceil_div(p.k0 + p.k1, p.parts);
-    all += (int64_t)(after - before) * k;
-    most = k > most ? k : most;
+    all += (int64_t)(p.tiles_m * p.tiles_n * p.parts / pairs) * ceil_div(p.k0 + p.k1, p.parts);
+    int64_t more = 0;
+    for (int j = 0; j < a.products; ++j) {
+      const FfnProduct& q = a.product[j];
+      const int from = (p.first - q.first) % pairs, n = q.tiles_m * q.tiles_n * q.parts % pairs;
+      if ((from < 0 ? from + pairs : from) < n) more += ceil_div(q.k0 + q.k1, q.parts);
+    }
+    most = more > most ? more : most;
   }
-  return a.tiles <= pairs ? most : all;
+  return all + most;
 }
 
-// Parts of K at most, and what a cut costs, in stages of a 256-column tile: in any case, and for
-// each part of such a tile.
-constexpr int kMostParts = 8, kCutStages = 12, kPartStages = 3;
+// Parts that K may come in, and what a cut costs, in stages of a 256-column tile: in any case, and
+// for each part of such a tile.
+constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16}, kCutStages = 12, kPartStages = 3;
 
 template <bool GLU, int ACT>
 cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, const bf16_t* res, bf16_t* out, bf16_t* gate,
@@ -782,27 +793,37 @@ int pick_bn(const FfnArgs& wide, const FfnArgs& narrow, int sms) {
   return launch_cost(narrow, 128, sms) < launch_cost(wide, 256, sms) ? 128 : 256;
 }
 
-// The launch `build(cols, parts)` with the columns and the parts of K of its first product that
-// take least.  A long sum over few tiles leaves most SMs idle; a cut one pays for its partial sums,
-// which go through L2 and are added up by whoever comes last (output product of 2048 x 5632, 64
-// rows, with the projections before it: 44 us uncut, 39, 36.5 and 35.5 in 2, 3 and 4 parts; of 520 x
-// 1384, 22 stages: 15.6 uncut, 16.5 in 2).
+// Fewest stages of a cut product.
+int least_stages(const FfnArgs& a) {
+  int k = INT_MAX;
+  for (int i = 0; i < a.products; ++i)
+    if (a.product[i].parts > 1 && a.product[i].k0 + a.product[i].k1 < k) k = a.product[i].k0 + a.product[i].k1;
+  return k;
+}
+
+// The launch `build(cols, what, parts)` with the columns and the parts of K that take least; `what`:
+// the group of products that is cut, of `groups`.  A long sum over few tiles leaves most SMs idle; a
+// cut one pays for its partial sums, which go through L2 and are added up by whoever comes last
+// (output product of 2048 x 5632, 64 rows, with the projections before it: 44 us uncut, 39, 36.5 and
+// 35.5 in 2, 3 and 4 parts; of 520 x 1384, 22 stages: 15.6 uncut, 16.5 in 2; the weights' gradients of
+// 12544 x 256 x 1024, in the whole backward pass: 96 us uncut, 76).
 template <typename Build>
-FfnArgs pick_launch(int sms, bool may_cut, int& bn, const Build& build) {
+FfnArgs pick_launch(int sms, int groups, int& bn, const Build& build) {
   FfnArgs best{};
   int64_t least = INT64_MAX;
   for (int cols = 256; cols >= 128; cols -= 128)
-    for (int parts = 1; parts <= (may_cut ? kMostParts : 1); ++parts) {
-      const FfnArgs a = build(cols, parts);
-      const FfnProduct& p = a.product[0];
-      if (parts > 1 && (p.tiles_m * p.tiles_n * parts > sms / 2 || p.k0 + p.k1 < parts)) break;
-      const int64_t cost = launch_cost(a, cols, sms) + (parts > 1 ? 12 * (kCutStages + kPartStages * parts * cols / 256) : 0);
-      if (cost < least) {
-        least = cost;
-        best = a;
-        bn = cols;
+    for (int what = 0; what < groups; ++what)
+      for (const int parts : kParts) {
+        if (parts == 1 && what > 0) continue;
+        const FfnArgs a = build(cols, what, parts);
+        if (a.slots * parts > sms / 2 || least_stages(a) < parts) break;   // the workspace; no part is empty
+        const int64_t cost = launch_cost(a, cols, sms) + (parts > 1 ? 12 * (kCutStages + kPartStages * parts * cols / 256) : 0);
+        if (cost < least) {
+          least = cost;
+          best = a;
+          bn = cols;
+        }
       }
-    }
   return best;
 }
 
@@ -975,7 +996,7 @@ srnl_status srnl_ffn_forward(srnl_ffn* h, const void* x, const srnl_ffn_params* 
   cudaError_t e = c.activation == SRNL_ACT_SILU ? launch_product<kGlu, SRNL_ACT_SILU>(bn, m, a[bn == 128], h->sms, s)
                                                 : launch_product<kGlu, SRNL_ACT_GELU>(bn, m, a[bn == 128], h->sms, s);
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward projections launch");
-  const FfnArgs b = pick_launch(h->sms, true, bn, [&](int cols, int parts) {
+  const FfnArgs b = pick_launch(h->sms, 1, bn, [&](int cols, int, int parts) {
     FfnArgs l{};
     add_product(l, M, D, cols, F, false, 0, 0, 0, false, parts);
     l.res = res != nullptr;
@@ -1042,12 +1063,14 @@ srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* gate, cons
   if (e != cudaSuccess) return ffn_cuda_fail(h, e, "feed-forward backward launch");
   // what is asked for of dx and the weights' gradients in one launch: the longest sums first, the
   // others' tiles fill up the SMs behind them
-  const FfnArgs b = pick_launch(h->sms, dx != nullptr, bn, [&](int cols, int parts) {
+  const bool weights = g.W_gate != nullptr || g.W_up != nullptr || g.W_down != nullptr;
+  const FfnArgs b = pick_launch(h->sms, 1 + (dx != nullptr && weights), bn, [&](int cols, int what, int parts) {
     FfnArgs l{};
-    if (dx != nullptr) add_product(l, M, D, cols, F, true, 0, 0, 0, false, parts);
-    if (g.W_gate != nullptr) add_product(l, F, D, cols, M, false, 2, 2, 1, true);
-    if (g.W_up != nullptr) add_product(l, F, D, cols, M, false, 3, 2, 2, true);
-    if (g.W_down != nullptr) add_product(l, D, F, cols, M, false, 4, 3, 3, true);
+    const int pd = dx == nullptr || what == 1 ? 1 : parts, pw = dx == nullptr || what == 1 ? parts : 1;
+    if (dx != nullptr) add_product(l, M, D, cols, F, true, 0, 0, 0, false, pd);
+    if (g.W_gate != nullptr) add_product(l, F, D, cols, M, false, 2, 2, 1, true, pw);
+    if (g.W_up != nullptr) add_product(l, F, D, cols, M, false, 3, 2, 2, true, pw);
+    if (g.W_down != nullptr) add_product(l, D, F, cols, M, false, 4, 3, 3, true, pw);
     l.partial = h->partial;
     l.arrived = h->arrived;
     l.err = h->dev_err;

@@ -61,7 +61,8 @@ def within(got, ref, magnitude, spread2, K, slack=0.0):
 SHAPES = [(1, 8, 8), (3, 64, 128), (7, 72, 136), (16, 128, 256), (33, 264, 520), (64, 256, 1024), (128, 512, 648),
           (129, 136, 1384), (256, 256, 256), (300, 520, 1384), (777, 1024, 2056), (2050, 264, 264),
           # long sums over few tiles: K goes to the CTAs in parts
-          (40, 72, 2056), (65, 264, 4104), (301, 136, 4104), (300, 136, 4104), (34, 1096, 3000)]
+          (40, 72, 2056), (65, 264, 4104), (301, 136, 4104), (300, 136, 4104), (34, 1096, 3000),
+          (3000, 72, 136), (5001, 136, 264)]   # and of many rows the weights' gradients
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
