@@ -18,7 +18,8 @@
 // Roundings: the state is fp32 throughout.  As an operand of a Z it is split into two bf16
 // parts (16 bits), and so are the decayed rows of the state's update, into three where the state
 // itself is asked for; the masked a b^T is rounded to bf16 once; out is rounded once.
-// The passes are in srnl_lattn_tc.cu; here are the single-token form and the entry points.
+// The passes are in srnl_lattn_tc.cu, and for at most 16 tokens, without those splits, in
+// srnl_lattn_short.cu; here are the single-token form and the entry points.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -174,7 +175,7 @@ srnl_status la_check(srnl_lattn* h, const Rows* in, int ni, const Rows* out, int
 cudaError_t la_run(srnl_lattn* h, srnl::LaArgs& a, cudaStream_t s) {
   a.B = h->cfg.B; a.T = h->cfg.T; a.heads = h->cfg.heads; a.d = h->cfg.d;
   a.log2g = h->log2g; a.seg_state = h->seg_state; a.err = h->dev_err;
-  return srnl::launch_la_tc(a, h->sms, s);
+  return a.T <= srnl::kShortTokens ? srnl::launch_la_short(a, s) : srnl::launch_la_tc(a, h->sms, s);
 }
 
 }  // namespace

@@ -1,5 +1,5 @@
-// Interface between the linear attention entry points (srnl_lattn.cu) and the tensor-core
-// passes (srnl_lattn_tc.cu).
+// Interface between the linear attention entry points (srnl_lattn.cu) and the passes, on the tensor
+// cores (srnl_lattn_tc.cu) and for a few tokens (srnl_lattn_short.cu).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -35,5 +35,8 @@ int la_groups(int heads, int d);
 int la_tc_segments(int T, int seqs, int sms);
 cudaError_t launch_la_tc(LaArgs& a, int sms, cudaStream_t s);
 cudaError_t prepare_la_tc(int d);
+// The same passes over at most kShortTokens tokens (srnl_lattn_short.cu).
+constexpr int kShortTokens = 16;
+cudaError_t launch_la_short(const LaArgs& a, cudaStream_t s);
 
 }  // namespace srnl

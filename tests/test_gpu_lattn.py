@@ -103,6 +103,9 @@ CASES = [  # B, T, heads, d, lengths, packed
     (3, 129, 2, 128, [129, 0, 128], False), (2, 300, 5, 64, [300, 299], False), (4, 333, 3, 32, [1, 333, 200, 64], True),
     (1, 2100, 2, 64, None, False), (2, 1500, 1, 128, [1500, 700], False), (2, 1200, 2, 32, [900, 1200], True),
     (40, 70, 4, 64, None, False),
+    # at most 32 tokens, and one more
+    (3, 8, 2, 32, [8, 0, 3], True), (2, 9, 3, 64, [9, 1], False), (2, 31, 1, 128, [31, 8], True), (5, 32, 3, 32, None, False),
+    (3, 32, 2, 128, [32, 17, 0], False), (2, 33, 2, 64, [33, 32], False),
     # more CTAs than run at once, lengths in no order, several equal: the longest go first
     (60, 260, 3, 64, [(97 * i) % 261 for i in range(30)] * 2, False), (50, 200, 3, 128, [200 - (i * i) % 190 for i in range(50)], False),
 ]
