@@ -768,7 +768,7 @@ int64_t longest_pair(const FfnArgs& a, int pairs) {
 
 // Parts that K may come in, and what a cut costs, in stages of a 256-column tile: in any case, and
 // for each part of such a tile.
-constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16}, kCutStages = 12, kPartStages = 3;
+constexpr int kParts[] = {2, 3, 4, 6, 8, 12, 16}, kCutStages = 12, kPartStages = 3;
 
 template <bool GLU, int ACT>
 cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, const bf16_t* res, bf16_t* out, bf16_t* gate,
@@ -811,18 +811,23 @@ template <typename Build>
 FfnArgs pick_launch(int sms, int groups, int& bn, const Build& build) {
   FfnArgs best{};
   int64_t least = INT64_MAX;
+  const auto take = [&](const FfnArgs& a, int cols, int64_t cost) {
+    if (cost >= least) return;
+    least = cost;
+    best = a;
+    bn = cols;
+  };
+  for (int cols = 256; cols >= 128; cols -= 128) {
+    const FfnArgs a = build(cols, 0, 1);
+    take(a, cols, launch_cost(a, cols, sms));
+  }
   for (int cols = 256; cols >= 128; cols -= 128)
     for (int what = 0; what < groups; ++what)
       for (const int parts : kParts) {
-        if (parts == 1 && what > 0) continue;
+        if (least <= 12 * (kCutStages + kPartStages)) return best;   // no cut costs less
         const FfnArgs a = build(cols, what, parts);
         if (a.slots * parts > sms / 2 || least_stages(a) < parts) break;   // the workspace; no part is empty
-        const int64_t cost = launch_cost(a, cols, sms) + (parts > 1 ? 12 * (kCutStages + kPartStages * parts * cols / 256) : 0);
-        if (cost < least) {
-          least = cost;
-          best = a;
-          bn = cols;
-        }
+        take(a, cols, launch_cost(a, cols, sms) + 12 * (kCutStages + kPartStages * parts * cols / 256));
       }
   return best;
 }
