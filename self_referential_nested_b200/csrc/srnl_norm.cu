@@ -19,9 +19,9 @@
 // that enough loads are in flight.  The arithmetic goes in pairs (two fp32 operations an
 // instruction): at full bandwidth the issue slots, not the loads, come next.
 //
-// Rows that are not whole 16-byte vectors: a group strides over the rows by a multiple of the
+// Rows that are not whole 16-byte vectors: a block's groups stride over the rows by a multiple of the
 // vector's length, so all its rows start at the same offset within a vector.  Its lanes stay on
-// aligned vectors; only the two at a row's ends, shared with its neighbours, go value by value.
+// aligned vectors, and the weights are copied to shared memory at that offset; only the two at a row's ends, shared with its neighbours, go value by value.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -104,6 +104,8 @@ __device__ __forceinline__ uint4 clip(const uint4& raw, int c, int dim) {
     }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
+// A bf16 unit at one of an odd row's ends goes in pieces of 8, 4 and 2 bytes, each where it is aligned:
+// at the row's end from the unit's first value on, at its start up to the unit's last.
 template <typename T, bool ODD>
 __device__ __forceinline__ void store_cols(T* row, int c, int dim, const float2* v) {
   constexpr int V = 16 / sizeof(T);
@@ -112,32 +114,41 @@ __device__ __forceinline__ void store_cols(T* row, int c, int dim, const float2*
     *reinterpret_cast<uint4*>(row + c) = raw;
     return;
   }
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  if (sizeof(T) == 2 && c >= 0) {
+    const int n = dim - c;   // the first n
+    if (n & 4) *reinterpret_cast<uint2*>(row + c) = make_uint2(raw.x, raw.y);
+    if (n & 2) *reinterpret_cast<uint32_t*>(row + c + (n & 4)) = n & 4 ? raw.z : raw.x;
+    if (n & 1) *reinterpret_cast<unsigned short*>(row + dim - 1) = (unsigned short)(n & 4 ? (n & 2 ? raw.w : raw.z) : n & 2 ? raw.y : raw.x);
+  } else if (sizeof(T) == 2 && c + V <= dim) {
+    const int n = c + V;     // the last n
+    if (n & 4) *reinterpret_cast<uint2*>(row + n - 4) = make_uint2(raw.z, raw.w);
+    if (n & 2) *reinterpret_cast<uint32_t*>(row + n - (n & 4) - 2) = n & 4 ? raw.y : raw.w;
+    if (n & 1) *reinterpret_cast<unsigned short*>(row) = (unsigned short)((n & 4 ? (n & 2 ? raw.x : raw.y) : n & 2 ? raw.z : raw.w) >> 16);
+  } else {                   // fp32, or a row within one unit
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-  for (int e = 0; e < V; ++e)
-    if (c + e >= 0 && c + e < dim) {
-      if constexpr (sizeof(T) == 2) row[c + e] = __ushort_as_bfloat16((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
-      else row[c + e] = __uint_as_float(w[e]);
-    }
-}
-// V weights at column c, as pairs.
-template <int V, bool ODD>
-__device__ __forceinline__ void load_weights(const float* p, int c, int dim, float2* v) {
-  if (!ODD) {
-#pragma unroll
-    for (int i = 0; i < V / 4; ++i) {
-      const float4 f = *reinterpret_cast<const float4*>(p + c + 4 * i);
-      v[2 * i] = make_float2(f.x, f.y);
-      v[2 * i + 1] = make_float2(f.z, f.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const int k = c + 2 * i;
-      v[i].x = k >= 0 && k < dim ? p[k] : 0.f;
-      v[i].y = k + 1 >= 0 && k + 1 < dim ? p[k + 1] : 0.f;
-    }
+    for (int e = 0; e < V; ++e)
+      if (c + e >= 0 && c + e < dim) {
+        if constexpr (sizeof(T) == 2) row[c + e] = __ushort_as_bfloat16((unsigned short)(w[e >> 1] >> (16 * (e & 1))));
+        else row[c + e] = __uint_as_float(w[e]);
+      }
   }
+}
+// V weights, 16-byte aligned, as pairs.
+template <int V>
+__device__ __forceinline__ void load_weights(const float* p, float2* v) {
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const float4 f = *reinterpret_cast<const float4*>(p + 4 * i);
+    v[2 * i] = make_float2(f.x, f.y);
+    v[2 * i + 1] = make_float2(f.z, f.w);
+  }
+}
+// An odd row's weights come from a copy in shared memory that is shifted as the block's rows are:
+// column c is at c + sh; zeros around them.
+__host__ __device__ constexpr int shifted(int dim) { return (dim + 16) / 4 * 4 + 4; }
+__device__ __forceinline__ void shift_weights(float* to, const float* p, int sh, int dim) {
+  for (int i = threadIdx.x; i < shifted(dim); i += blockDim.x) to[i] = i >= sh && i < dim + sh ? p[i - sh] : 0.f;
 }
 
 __device__ __forceinline__ uint32_t cluster_block() {
@@ -190,33 +201,49 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* red) {
 }
 
 constexpr int kLongThreads = 32 * kLongWarps;   // 8192 columns and an odd start: 1025 bf16 vectors by two, 2049 fp32 ones by four
-// Most threads of a block, and the blocks whose registers an SM has to hold.
+// Most threads of a block, and the blocks whose registers an SM has to hold: one fewer where a row's
+// values and weights would not fit (20000 x 256 bf16: 7.0 us with three, 5.1 with two).
 __host__ __device__ constexpr int norm_threads(int lpr, int per, int r, bool bwd) {
   return lpr == 0 ? (per > 1 ? kLongThreads : r > 1 ? 256 : 1024) : bwd ? 128 : 256;
 }
-__host__ __device__ constexpr int norm_resident(int lpr, int per, int r, bool bwd) {
-  return lpr == 0 ? (per > 1 ? (bwd ? 1 : 2) : r > 1 ? (bwd ? 2 : 4) : 1) : bwd ? 4 : 3;
+__host__ __device__ constexpr int norm_resident(int lpr, int per, int r, int esize, bool odd, bool bwd) {
+  return lpr == 0 ? (per > 1 ? (bwd ? 1 : 2) : r > 1 ? (bwd ? 2 : 4) : 1) 
+         : bwd    ? (esize == 2 && per == 4 ? 3 : 4)
+                  : (esize == 2 && per == 2 && r == 2) || (odd && r == 4) ? 2 : 3;
 }
 
 // LPR: lanes per row (0: CL blocks, a cluster); PER: vectors per lane; R: rows at once.
 template <typename T, int LPR, int PER, int R, bool ODD, int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, PER, R, false), norm_resident(LPR, PER, R, false))
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, PER, R, false), norm_resident(LPR, PER, R, sizeof(T), ODD, false))
     norm_forward_kernel(const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
                         T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out, int64_t rows,
                         int dim, float eps) {
   constexpr int V = 16 / sizeof(T), H = V / 2;
   if constexpr (CL > 1) cluster_barrier();   // its blocks are all there
-  // gamma and beta in registers, else from L1 for each R rows (an odd row's value by value)
-  constexpr bool kKeep = LPR != 0 && PER * V <= (ODD ? 24 : 16);
+  // gamma and beta in registers, else from L1 or shared memory for each R rows
+  constexpr bool kKeep = LPR != 0 && PER * V <= 16;
   constexpr int kRed = CL * kMostWarps * R;
   __shared__ float red[LPR == 0 ? 2 * kRed : 1];
   const int lanes = LPR == 0 ? CL * blockDim.x : LPR;
   const int lane = LPR != 0 ? threadIdx.x % LPR : CL == 1 ? threadIdx.x : cluster_block() * blockDim.x + threadIdx.x;
-  const int64_t group = LPR == 0 ? blockIdx.x / CL : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
+  // the groups of a block are spread over the rows where those are odd: the grid is a multiple of a
+  // vector's length then, and all of its rows start at the same offset
+  const int64_t group = LPR == 0 ? blockIdx.x / CL
+                        : ODD ? (int64_t)(threadIdx.x / (LPR ? LPR : 1)) * gridDim.x + blockIdx.x
+                              : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / (LPR ? LPR : 1);
   const int64_t groups = LPR == 0 ? gridDim.x / CL : (int64_t)gridDim.x * blockDim.x / LPR;
   // of the warp's first group: all lanes of a warp make the same passes
-  const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (threadIdx.x % 32) / LPR;
-  const int c0 = lane * V - (ODD ? (int)(group * dim % V) : 0), cs = lanes * V;
+  const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (int64_t)((threadIdx.x % 32) / (LPR ? LPR : 1)) * (ODD ? gridDim.x : 1);
+  const int sh = ODD ? (int)(group * dim % V) : 0, c0 = lane * V - sh, cs = lanes * V;
+  extern __shared__ __align__(16) float copies[];   // odd rows: gamma, beta
+  const float *gp = gamma, *bp = beta;
+  if constexpr (ODD) {
+    shift_weights(copies, gamma, sh, dim);
+    shift_weights(copies + shifted(dim), beta, sh, dim);
+    __syncthreads();
+    gp = copies + sh;
+    bp = copies + shifted(dim) + sh;
+  }
   const float inv_d = 1.f / (float)dim;
   bool on[PER];
   float2 g[kKeep ? PER * H : 1], b[kKeep ? PER * H : 1];
@@ -225,8 +252,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
     on[i] = c0 + i * cs < dim && (!ODD || c0 + i * cs + V > 0);
     if constexpr (kKeep)
       if (on[i]) {
-        load_weights<V, ODD>(gamma, c0 + i * cs, dim, g + i * H);
-        load_weights<V, ODD>(beta, c0 + i * cs, dim, b + i * H);
+        load_weights<V>(gp + c0 + i * cs, g + i * H);
+        load_weights<V>(bp + c0 + i * cs, b + i * H);
       }
   }
   uint4 raw[R][PER];
@@ -292,8 +319,8 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 #pragma unroll
         for (int e = 0; e < H; ++e) { gw[e] = g[i * H + e]; bw[e] = b[i * H + e]; }
       } else {
-        load_weights<V, ODD>(gamma, c, dim, gw);
-        load_weights<V, ODD>(beta, c, dim, bw);
+        load_weights<V>(gp + c, gw);
+        load_weights<V>(bp + c, bw);
       }
 #pragma unroll
       for (int q = 0; q < R; ++q) {
@@ -319,22 +346,33 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 
 // dx per row, and per block the partial sums of dgamma and dbeta: part[block][2][dim].
 template <typename T, int LPR, int PER, int R, bool ODD, int CL>
-__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, PER, R, true), norm_resident(LPR, PER, R, true))
+__global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, PER, R, true), norm_resident(LPR, PER, R, sizeof(T), ODD, true))
     norm_backward_kernel(const T* __restrict__ x, const T* __restrict__ dy, const T* __restrict__ dres,
                          const float* __restrict__ gamma, const float* __restrict__ mean_in,
                          const float* __restrict__ rstd_in, T* __restrict__ dx, float* __restrict__ part,
                          int64_t rows, int dim) {
   constexpr int V = 16 / sizeof(T), H = V / 2;
   if constexpr (CL > 1) cluster_barrier();   // its blocks are all there
-  extern __shared__ float fold[];   // [warps][2][dim]: groups of different warps share columns
+  extern __shared__ __align__(16) float copies[];   // odd rows: gamma; then [warps][2][dim]: groups of different warps share columns
+  float* fold = copies + (ODD ? shifted(dim) : 0);
   constexpr int kRed = CL * kMostWarps * 2 * R;
   __shared__ float red[LPR == 0 ? 2 * kRed : 1];
   const int lanes = LPR == 0 ? CL * blockDim.x : LPR;
   const int lane = LPR != 0 ? threadIdx.x % LPR : CL == 1 ? threadIdx.x : cluster_block() * blockDim.x + threadIdx.x;
-  const int64_t group = LPR == 0 ? blockIdx.x / CL : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / LPR;
+  // the groups of a block are spread over the rows where those are odd: the grid is a multiple of a
+  // vector's length then, and all of its rows start at the same offset
+  const int64_t group = LPR == 0 ? blockIdx.x / CL
+                        : ODD ? (int64_t)(threadIdx.x / (LPR ? LPR : 1)) * gridDim.x + blockIdx.x
+                              : ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / (LPR ? LPR : 1);
   const int64_t groups = LPR == 0 ? gridDim.x / CL : (int64_t)gridDim.x * blockDim.x / LPR;
-  const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (threadIdx.x % 32) / LPR;
+  const int64_t lead = LPR == 0 || LPR == 32 ? group : group - (int64_t)((threadIdx.x % 32) / (LPR ? LPR : 1)) * (ODD ? gridDim.x : 1);
   const int sh = ODD ? (int)(group * dim % V) : 0, c0 = lane * V - sh, cs = lanes * V;
+  const float* gp = gamma;
+  if constexpr (ODD) {
+    shift_weights(copies, gamma, sh, dim);
+    __syncthreads();
+    gp = copies + sh;
+  }
   const float inv_d = 1.f / (float)dim;
   bool on[PER];
   constexpr bool kKeep = LPR != 0 && PER * V <= 16;
@@ -343,7 +381,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
   for (int i = 0; i < PER; ++i) {
     on[i] = c0 + i * cs < dim && (!ODD || c0 + i * cs + V > 0);
     if constexpr (kKeep)
-      if (on[i]) load_weights<V, ODD>(gamma, c0 + i * cs, dim, g + i * H);
+      if (on[i]) load_weights<V>(gp + c0 + i * cs, g + i * H);
 #pragma unroll
     for (int e = 0; e < H; ++e) dg[i * H + e] = db[i * H + e] = make_float2(0.f, 0.f);
   }
@@ -392,7 +430,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 #pragma unroll
           for (int e = 0; e < H; ++e) gw[e] = g[i * H + e];
         } else {
-          load_weights<V, ODD>(gamma, c0 + i * cs, dim, gw);
+          load_weights<V>(gp + c0 + i * cs, gw);
         }
 #pragma unroll
         for (int e = 0; e < H; ++e) {
@@ -435,10 +473,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
   }
   asm volatile("griddepcontrol.launch_dependents;");
   if constexpr (CL > 1) cluster_barrier();   // no block leaves while another may still write to it
-  // groups in one order: those of a warp with equal columns, then the warps; an odd row's groups
-  // start at different columns, so each adds its own in turn
+  // groups in one order: those of a warp, then the warps
   float* mine = part + (int64_t)(blockIdx.x / CL) * 2 * dim;
-  auto put = [&](float* to, bool add) {
+  auto put = [&](float* to) {
 #pragma unroll
     for (int i = 0; i < PER; ++i)
 #pragma unroll
@@ -446,32 +483,25 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
         const int c = c0 + i * cs + e, k = i * H + e / 2;
         if (!on[i] || c >= dim || (ODD && c < 0)) continue;
         const float p = e & 1 ? dg[k].y : dg[k].x, q = e & 1 ? db[k].y : db[k].x;
-        to[c] = add ? to[c] + p : p;
-        to[dim + c] = add ? to[dim + c] + q : q;
+        to[c] = p;
+        to[dim + c] = q;
       }
   };
   if constexpr (LPR == 0) {
-    put(mine, false);
+    put(mine);
   } else {
     const int warp = threadIdx.x >> 5;
     float* to = fold + warp * 2 * dim;
-    if constexpr (!ODD) {
 #pragma unroll
-      for (int o = LPR; o < 32; o <<= 1)
+    for (int o = LPR; o < 32; o <<= 1)
 #pragma unroll
-        for (int k = 0; k < PER * H; ++k) {
-          dg[k].x += __shfl_xor_sync(0xffffffffu, dg[k].x, o);
-          dg[k].y += __shfl_xor_sync(0xffffffffu, dg[k].y, o);
-          db[k].x += __shfl_xor_sync(0xffffffffu, db[k].x, o);
-          db[k].y += __shfl_xor_sync(0xffffffffu, db[k].y, o);
-        }
-      if ((threadIdx.x & 31) < LPR) put(to, false);
-    } else {
-      for (int k = 0; k < 32 / LPR; ++k) {
-        if ((int)(threadIdx.x & 31) / LPR == k) put(to, k > 0);
-        __syncwarp();
+      for (int k = 0; k < PER * H; ++k) {
+        dg[k].x += __shfl_xor_sync(0xffffffffu, dg[k].x, o);
+        dg[k].y += __shfl_xor_sync(0xffffffffu, dg[k].y, o);
+        db[k].x += __shfl_xor_sync(0xffffffffu, db[k].x, o);
+        db[k].y += __shfl_xor_sync(0xffffffffu, db[k].y, o);
       }
-    }
+    if ((threadIdx.x & 31) < LPR) put(to);
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * dim; c += blockDim.x) {
       float t = 0.f;
@@ -540,14 +570,19 @@ NormPlan norm_plan(int dim, int esize, bool bwd) {
   return p;
 }
 
-// Blocks of a call: what the SMs hold at once, or fewer for few rows; groups a multiple of 8 (a
-// vector's values), which an odd row's groups rely on.
+// Blocks of a call: what the SMs hold at once, or fewer for few rows; a multiple of 8 (a vector's
+// values) for odd rows, whose groups rely on it.
 int norm_blocks(const NormPlan& p, int threads, int64_t rows, int sms, int per_sm) {
   const int per_block = p.lpr == 0 ? 1 : threads / p.lpr, each = p.lpr == 0 ? p.blocks : 1;
   const int64_t need = (rows + per_block - 1) / per_block, most = (int64_t)sms * per_sm / each;
   int n = (int)(need < most ? need : most);
-  if (p.odd && per_block % 8 != 0) n = n < 8 || (n + 7) / 8 * 8 <= most ? (n + 7) / 8 * 8 : n / 8 * 8;   // never a few more than fit at once
+  if (p.odd) n = n < 8 || (n + 7) / 8 * 8 <= most ? (n + 7) / 8 * 8 : n / 8 * 8;   // never a few more than fit at once
   return n * each;
+}
+
+// Shared memory of a block: an odd row's weights; backward, the warps' sums.
+size_t norm_smem(const NormPlan& p, int dim, int threads, bool bwd) {
+  return ((p.odd ? (size_t)shifted(dim) * (bwd ? 1 : 2) : 0) + (bwd && p.lpr != 0 ? (size_t)(threads / 32) * 2 * dim : 0)) * sizeof(float);
 }
 
 // Short rows go several at a time, so that a lane has two to four vectors in flight.
@@ -641,18 +676,25 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
     {
       const srnl::NormPlan& p = h->fwd;
       const int threads = p.lpr == 0 ? p.threads : 256;
+      const size_t smem = srnl::norm_smem(p, cfg->dim, threads, false);
 #define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                             \
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>,    \
-                                                    threads, 0)
+  if (smem > 48 * 1024)                                                                                                    \
+    e = cudaFuncSetAttribute(srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
+                             (int)smem);                                                                                   \
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>,    \
+                                                    threads, smem)
       SRNL_NORM_DISPATCH(true, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
     }
     if (e == cudaSuccess) {
       const srnl::NormPlan& p = h->bwd;
       const int threads = p.lpr == 0 ? p.threads : 128;
-      const size_t smem = p.lpr == 0 ? 0 : (size_t)(threads / 32) * 2 * cfg->dim * sizeof(float);
+      const size_t smem = srnl::norm_smem(p, cfg->dim, threads, true);
 #define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                             \
-  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>,   \
+  if (smem > 48 * 1024)                                                                                                    \
+    e = cudaFuncSetAttribute(srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
+                             (int)smem);                                                                                   \
+  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>,   \
                                                     threads, smem)
       SRNL_NORM_DISPATCH(false, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
@@ -699,7 +741,7 @@ srnl_status srnl_ln_forward(srnl_ln* h, const void* x, const float* gamma, const
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int threads = p.lpr == 0 ? p.threads : 256, blocks = srnl::norm_blocks(p, threads, rows, h->sms, h->fwd_per_sm);
 #define SRNL_NORM_RUN(T, LPR, PER, R, ODD, CL)                                                      \
-  srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL><<<blocks, threads, 0, s>>>(                    \
+  srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL><<<blocks, threads, srnl::norm_smem(p, dim, threads, false), s>>>( \
       static_cast<const T*>(x), gamma, beta, static_cast<T*>(y), mean, rstd, rows, dim, h->cfg.eps)
   SRNL_NORM_DISPATCH(true, SRNL_NORM_RUN);
 #undef SRNL_NORM_RUN
@@ -736,7 +778,7 @@ srnl_status srnl_ln_backward(srnl_ln* h, const void* x, const void* dy, const vo
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int threads = p.lpr == 0 ? p.threads : 128, blocks = srnl::norm_blocks(p, threads, rows, h->sms, h->bwd_per_sm);
   if (rows > 0) {
-    const size_t smem = p.lpr == 0 ? 0 : (size_t)(threads / 32) * 2 * dim * sizeof(float);
+    const size_t smem = srnl::norm_smem(p, dim, threads, true);
 #define SRNL_NORM_RUN(T, LPR, PER, R, ODD, CL)                                                                     \
   srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL><<<blocks, threads, smem, s>>>(                               \
       static_cast<const T*>(x), static_cast<const T*>(dy), static_cast<const T*>(dres), gamma, mean, rstd,     \
