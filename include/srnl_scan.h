@@ -538,7 +538,8 @@ SRNL_API srnl_status srnl_ffn_backward(srnl_ffn* h, const void* x, const void* g
                                        int rows, void* stream);
 
 /* Synchronously reads the status word of the handle's kernels: SRNL_OK, or SRNL_E_TIMEOUT once
- * a bounded in-kernel wait gave up. */
+ * a bounded in-kernel wait gave up: the handle's results are not to be used then, nor the handle
+ * any further. */
 SRNL_API srnl_status srnl_ffn_device_status(srnl_ffn* h);
 
 /* Message for the last failure on this handle (h == NULL: the calling thread's last
@@ -595,7 +596,8 @@ SRNL_API srnl_status srnl_lattn_step(srnl_lattn* h, const void* q, const void* k
                                      void* stream);
 
 /* Synchronously reads the status word of the handle's kernels: SRNL_OK, or SRNL_E_TIMEOUT once
- * a bounded in-kernel wait gave up. */
+ * a bounded in-kernel wait gave up: the handle's results are not to be used then, nor the handle
+ * any further. */
 SRNL_API srnl_status srnl_lattn_device_status(srnl_lattn* h);
 
 /* Message for the last failure on this handle (h == NULL: the calling thread's last

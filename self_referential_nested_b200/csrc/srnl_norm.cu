@@ -692,11 +692,13 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
       const srnl::NormPlan& p = h->fwd;
       const int threads = p.lpr == 0 ? p.threads : 256;
       const size_t smem = srnl::norm_smem(p, cfg->dim, threads, false);
-#define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                             \
-  if (smem > 48 * 1024)                                                                                                    \
-    e = cudaFuncSetAttribute(srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
-                             (int)smem);                                                                                   \
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>,    \
+// the limit is the kernel's, not the handle's: always the longest row's
+#define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                              \
+  if (smem > 48 * 1024)                                                                                                     \
+    e = cudaFuncSetAttribute(srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
+                             (int)(2 * srnl::shifted(srnl::kNormMaxDim) * sizeof(float)));                                  \
+  if (e == cudaSuccess)                                                                                                     \
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->fwd_per_sm, srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>,     \
                                                     threads, smem)
       SRNL_NORM_DISPATCH(true, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
@@ -705,12 +707,9 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
       const srnl::NormPlan& p = h->bwd;
       const int threads = p.lpr == 0 ? p.threads : 128;
       const size_t smem = srnl::norm_smem(p, cfg->dim, threads, true);
-#define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                             \
-  if (smem > 48 * 1024)                                                                                                    \
-    e = cudaFuncSetAttribute(srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize,   \
-                             (int)smem);                                                                                   \
-  if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>,   \
-                                                    threads, smem)
+#define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                              \
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&h->bwd_per_sm, srnl::norm_backward_kernel<T, LPR, PER, R, ODD, CL>,    \
+                                                    threads, smem)   /* at most 37 KB */
       SRNL_NORM_DISPATCH(false, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
     }

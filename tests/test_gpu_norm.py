@@ -189,6 +189,22 @@ def test_an_odd_row_keeps_its_neighbours_out(dim, dtype):
         h.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_handles_of_long_odd_rows_side_by_side(dtype):
+    """A later handle of shorter rows leaves an earlier one's calls as they are."""
+    ts = [make(9, dim, dtype, seed=dim) for dim in (8191, 6205, 7001)]
+    hs = [S.srnl_ln_create(dict(dim=t["gamma"].numel(), act_dtype=dtype)) for t in ts]
+    try:
+        for h, t in list(zip(hs, ts)) + list(zip(hs, ts))[::-1]:
+            y, _, _ = forward(h, t)
+            ref = reference(t, float(np.float32(1e-6)))[0]
+            # a rounding of the output, and fp32 sums and products a hundred steps long
+            assert float((y.double() - ref).norm()) <= (torch.finfo(DT[dtype]).eps / 2 + 100 * U) * float(ref.norm())
+    finally:
+        for h in hs:
+            h.close()
+
+
 def test_large_offset_keeps_the_spread():
     """The variance is taken from the centred values: an offset of 4096 spreads leaves it right."""
     x = torch.randn(64, 512, generator=torch.Generator().manual_seed(1)).cuda() + 4096.0
