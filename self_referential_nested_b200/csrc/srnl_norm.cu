@@ -9,7 +9,7 @@
 //
 // Both passes are bound by memory: each input is read once and each output written once (backward of
 // 8209 x 2560 fp32: 49 us, 5.1 TB/s; of 25088 x 384 bf16 with dres: 20 us, 3.9 TB/s; forward of 100352 x
-// 64 bf16: 5.6 us, 4.6 TB/s, in L2), short calls by their launches.  All statistics, sums and gradients of gamma and beta are fp32; only y and dx are rounded, once,
+// 64 bf16: 5.9 us, 4.4 TB/s, in L2), short calls by their launches.  All statistics, sums and gradients of gamma and beta are fp32; only y and dx are rounded, once,
 // to the activations' type.
 //
 // Layout of the work: a row belongs to a group of lanes that hold it in registers between the
