@@ -726,9 +726,9 @@ cudaError_t launch_product(int bn, const FfnMaps& maps, const FfnArgs& a, int sm
 
 template <int EPI, int ACT, bool CUT = false>
 cudaError_t prepare_product() {
-  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 256, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 256));
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 128, CUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)ffn_smem(EPI, 128));
+  constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 256, CUT>, kSmem, (int)ffn_smem(EPI, 256));
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ffn_product_kernel<EPI, ACT, 128, CUT>, kSmem, (int)ffn_smem(EPI, 128));
   return e;
 }
 

@@ -28,7 +28,8 @@ template <int D, int TT>
 constexpr size_t short_smem() { return (size_t)(2 * D * TT + TT * (TT + 4) + 32 * (D + 4)) * sizeof(float); }
 
 template <int D, int TT>
-__global__ void __launch_bounds__(short_threads(D), D == 128 ? (TT == 8 ? 4 : 3) : TT == 8 ? 6 : 4) decay_short_kernel(const __grid_constant__ LaArgs args) {
+__global__ void __launch_bounds__(short_threads(D), D == 128 ? (TT == 8 ? 4 : 3) : TT == 8 ? 6 : 4)
+    decay_short_kernel(const __grid_constant__ LaArgs args) {
   constexpr int kThreads = short_threads(D), G = kThreads / D, TG = TT / G;   // threads of a channel, tokens of a thread
   constexpr int kP = TT + 4;
   extern __shared__ __align__(16) float sm[];

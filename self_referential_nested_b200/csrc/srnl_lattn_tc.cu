@@ -290,7 +290,10 @@ __device__ __forceinline__ void prefetch_chunk(const CUtensorMap* map, int group
   for (int h = 0; h < 2; ++h) tma_prefetch_4d(map, 2 * group + h, token, batch);
 }
 
-enum { kFullA, kFullB = kFullA + 2, kFullC = kFullB + 2, kFreeA, kFreeB = kFreeA + 2, kFreeC = kFreeB + 2, kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars };   // two of those whose next name is 2 further
+enum {   // barriers; two each of those that the next name leaves room for
+  kFullA, kFullB = kFullA + 2, kFullC = kFullB + 2, kFreeA, kFreeB = kFreeA + 2, kFreeC = kFreeB + 2,
+  kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars
+};
 
 template <int D>
 __global__ void __launch_bounds__(la_threads(kC / D), 1)
@@ -419,7 +422,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
 #pragma unroll
           for (int s = 0; s < 8; ++s) {
             const int h = NH == 2 ? s >> 2 : 0;
-            const uint64_t az = (part == 0 ? dzh : dzl) + (NH == 2 ? (uint64_t)h * (kTile >> 6) + (uint64_t)(s & 3) * 128 : (uint64_t)s * 128);   // 16 rows of Z
+            const uint64_t az = (part == 0 ? dzh : dzl) +   // 16 rows of Z
+                                (NH == 2 ? (uint64_t)h * (kTile >> 6) + (uint64_t)(s & 3) * 128 : (uint64_t)s * 128);
             mma_k16_desc(tO + h * 64, da + (uint64_t)(s >> 2) * kBox16 + (uint64_t)(s & 3) * 2, az, iO,
                          part > 0 || (NH == 2 ? (s & 3) > 0 : s > 0));
           }
@@ -822,7 +826,8 @@ __global__ void __launch_bounds__(kSegThreads, 1)
         clear_rows(cc, c.cnt, tid - 128, kSegThreads - 128);
         fence_async();
       }
-      form_tmem<kC / 32 * 4 / kSegFormers>(smem_u32(b), tP + (k & 1) * 192, q, share * (kC * 4 / kSegFormers), wt + h * kC, f, exact ? kThree : kTwo, lane);
+      form_tmem<kC / 32 * 4 / kSegFormers>(smem_u32(b), tP + (k & 1) * 192, q, share * (kC * 4 / kSegFormers), wt + h * kC, f,
+                                           exact ? kThree : kTwo, lane);
       tmem_wait_st();
       warp_arrive(&bar[sParts + (k & 1)], lane);
       if (lane == 0) mbar_arrive(&bar[sFree + s]);

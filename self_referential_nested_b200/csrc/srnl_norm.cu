@@ -9,19 +9,20 @@
 //
 // Both passes are bound by memory: each input is read once and each output written once (backward of
 // 8209 x 2560 fp32: 49 us, 5.1 TB/s; of 25088 x 384 bf16 with dres: 20 us, 3.9 TB/s; forward of 100352 x
-// 64 bf16: 5.9 us, 4.4 TB/s, in L2), short calls by their launches.  All statistics, sums and gradients of gamma and beta are fp32; only y and dx are rounded, once,
-// to the activations' type.
+// 64 bf16: 5.9 us, 4.4 TB/s, in L2), short calls by their launches.  All statistics, sums and
+// gradients of gamma and beta are fp32; only y and dx are rounded, once, to the activations' type.
 //
 // Layout of the work: a row belongs to a group of lanes that hold it in registers between the
 // sums and the output: 8 to 32 lanes of a warp for rows of up to 128 16-byte vectors, a block for
-// longer ones.  A lane owns the same columns in every row it meets, so the weights' gradients
+// longer ones (two blocks of a cluster for the longest fp32 rows backward).  A lane owns the same columns in every row it meets, so the weights' gradients
 // stay in its registers until the end.  Several rows are taken at once where they are short, so
 // that enough loads are in flight.  The arithmetic goes in pairs (two fp32 operations an
 // instruction): at full bandwidth the issue slots, not the loads, come next.
 //
 // Rows that are not whole 16-byte vectors: a block's groups stride over the rows by a multiple of the
 // vector's length, so all its rows start at the same offset within a vector.  Its lanes stay on
-// aligned vectors, and the weights are copied to shared memory at that offset; only the two at a row's ends, shared with its neighbours, go value by value.
+// aligned vectors, and the weights are copied to shared memory at that offset; the two vectors at a
+// row's ends are shared with its neighbours.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

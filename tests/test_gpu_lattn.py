@@ -103,7 +103,8 @@ CASES = [  # B, T, heads, d, lengths, packed
     (3, 129, 2, 128, [129, 0, 128], False), (2, 300, 5, 64, [300, 299], False), (4, 333, 3, 32, [1, 333, 200, 64], True),
     (1, 2100, 2, 64, None, False), (2, 1500, 1, 128, [1500, 700], False), (2, 1200, 2, 32, [900, 1200], True),
     (40, 70, 4, 64, None, False),
-    # at most 32 tokens, and one more
+    # a few tokens, on both sides of what the kernel for them takes
+    (2, 16, 2, 128, [16, 3], False), (3, 12, 3, 32, None, True), (2, 17, 2, 64, [17, 0], True), (4, 16, 1, 64, None, False),
     (3, 8, 2, 32, [8, 0, 3], True), (2, 9, 3, 64, [9, 1], False), (2, 31, 1, 128, [31, 8], True), (5, 32, 3, 32, None, False),
     (3, 32, 2, 128, [32, 17, 0], False), (2, 33, 2, 64, [33, 32], False),
     # more CTAs than run at once, lengths in no order, several equal: the longest go first
