@@ -453,6 +453,8 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
 #pragma unroll 1
       for (int k = 0; k < chunks_z; ++k) {
         mbar_pass(&bar[kFullC], k & 1, failed);
+        // c's spare rows are zeros: all state warps clear them, and a wide head's first parts come from half of those
+        if (!rev && k == chunks - 1 && (end - begin) % kC != 0) mbar_pass(&bar[kClear], 0, failed);
         if constexpr (NH == 1) {   // in TMEM, half the tokens a step; then the rest in the first part's place
           constexpr uint32_t iZ = idesc_mn(128, 128, false, true);
 #pragma unroll 1

@@ -402,3 +402,35 @@ def test_refusals():
             hp.close()
     finally:
         h.close()
+
+
+@pytest.mark.parametrize("lo", [1, 129])
+def test_padding_of_a_short_last_chunk_stays_out_of_the_state(lo):
+    """128-wide heads whose last chunk is shorter than half: what lies behind the last token (NaN, infinities) reaches
+    neither the state nor the outputs, whichever of the CTA's warps clears it.  Many CTAs, several calls."""
+    B, H, d = 63, 4, 128
+    T = lo + 190
+    t = make(B, T, H, d, seed=lo)
+    lens = [lo + i for i in range(B)]   # 1 to 63 tokens in the last chunk
+    n = torch.tensor(lens, device="cuda", dtype=torch.int32)
+    decay = np.array([1.0, 0.9, 0.99, 0.5], np.float32)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+    try:
+        def go():
+            o, st = torch.zeros(B, T, H * d, device="cuda", dtype=BF), torch.empty_like(t["s0"])
+            g, dsi = [torch.zeros_like(t["q"]) for _ in range(3)], torch.empty_like(t["s0"])
+            S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=n, state_in=t["s0"], state_out=st)
+            S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], *g, lengths=n, state_in=t["s0"], dstate_out=t["ds"],
+                                  dstate_in=dsi)
+            torch.cuda.synchronize()
+            return [o, st, *g, dsi]
+
+        clean = go()
+        for x in ("q", "k", "v", "do"):
+            for b in range(B):
+                t[x][b, lens[b]:] = (float("nan"), float("inf"), -float("inf"))[b % 3]
+        for _ in range(5):
+            assert all(torch.equal(a, b) for a, b in zip(go(), clean))
+        S.srnl_lattn_device_status(h)
+    finally:
+        h.close()
