@@ -33,6 +33,7 @@
 
 #include "srnl_common.cuh"
 #include "srnl_internal.h"
+#include "srnl_norm.h"
 #include "srnl_scan.h"
 
 namespace srnl {
@@ -74,15 +75,14 @@ __device__ __forceinline__ uint4 repack(const float2* v) {
 // neighbours too.  They are read whole and the neighbours' values taken out once they have arrived
 // (clip): value by value a lane packs bf16 ones, and so waits for each unit in turn (8000 x 1533
 // backward: 81 us, 40 whole).  fp32 ones need no packing, and blocks of long rows take them value by
-// value (44 us whole, 41 so).  Behind the last row there is nothing to read.
+// value (44 us whole, 41 so).  Nothing is read behind the buffer's end (room: values up to there).
 template <typename T, int LPR, bool ODD>
 __host__ __device__ constexpr bool whole_units() { return ODD && (sizeof(T) == 2 || LPR != 0); }
 
 template <typename T, int LPR, bool ODD>
-__device__ __forceinline__ uint4 load_cols(const T* row, int c, int dim, bool last) {
+__device__ __forceinline__ uint4 load_cols(const T* row, int c, int dim, int room) {
   constexpr int V = 16 / sizeof(T);
-  constexpr bool kWhole = whole_units<T, LPR, ODD>();
-  if (!ODD || (c + V <= dim && (kWhole || c >= 0)) || (kWhole && !last)) return *reinterpret_cast<const uint4*>(row + c);
+  if (!ODD || unit_in_one_piece(c, V, dim, room, whole_units<T, LPR, ODD>())) return *reinterpret_cast<const uint4*>(row + c);
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < V; ++e)
@@ -280,7 +280,7 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
       for (int i = 0; i < PER; ++i) {
         raw[q][i] = make_uint4(0u, 0u, 0u, 0u);
         const int64_t r = from + q * groups;
-        if (on[i] && r < rows) raw[q][i] = load_cols<T, LPR, ODD>(x + r * dim, c0 + i * cs, dim, r + 1 == rows);
+        if (on[i] && r < rows) raw[q][i] = load_cols<T, LPR, ODD>(x + r * dim, c0 + i * cs, dim, row_room(r, rows, dim));
       }
   };
   if (LPR == 0) load(group);
@@ -414,9 +414,9 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
       for (int i = 0; i < PER; ++i) {
         xr[q][i] = yr[q][i] = er[q][i] = make_uint4(0u, 0u, 0u, 0u);
         if (on[i] && r < rows) {
-          xr[q][i] = load_cols<T, LPR, ODD>(x + r * dim, c0 + i * cs, dim, r + 1 == rows);
-          yr[q][i] = load_cols<T, LPR, ODD>(dy + r * dim, c0 + i * cs, dim, r + 1 == rows);
-          if (dres != nullptr) er[q][i] = load_cols<T, LPR, ODD>(dres + r * dim, c0 + i * cs, dim, r + 1 == rows);
+          xr[q][i] = load_cols<T, LPR, ODD>(x + r * dim, c0 + i * cs, dim, row_room(r, rows, dim));
+          yr[q][i] = load_cols<T, LPR, ODD>(dy + r * dim, c0 + i * cs, dim, row_room(r, rows, dim));
+          if (dres != nullptr) er[q][i] = load_cols<T, LPR, ODD>(dres + r * dim, c0 + i * cs, dim, row_room(r, rows, dim));
         }
       }
     }
