@@ -693,9 +693,10 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
       const srnl::NormPlan& p = h->fwd;
       const int threads = p.lpr == 0 ? p.threads : 256;
       const size_t smem = srnl::norm_smem(p, cfg->dim, threads, false);
-// the limit is the kernel's, not the handle's: always the longest row's
+// the limit is the kernel's, not the handle's, and counts its static shared memory too: raised to the
+// longest row's for every odd row of a block's own
 #define SRNL_NORM_OCC(T, LPR, PER, R, ODD, CL)                                                                              \
-  if (smem > 48 * 1024)                                                                                                     \
+  if (p.odd && p.lpr == 0)                                                                                                  \
     e = cudaFuncSetAttribute(srnl::norm_forward_kernel<T, LPR, PER, R, ODD, CL>, cudaFuncAttributeMaxDynamicSharedMemorySize, \
                              (int)(2 * srnl::shifted(srnl::kNormMaxDim) * sizeof(float)));                                  \
   if (e == cudaSuccess)                                                                                                     \
@@ -714,8 +715,7 @@ srnl_status srnl_ln_create(srnl_ln** out, const srnl_ln_config* cfg) {
       SRNL_NORM_DISPATCH(false, SRNL_NORM_OCC);
 #undef SRNL_NORM_OCC
     }
-    if (h->fwd_per_sm < 1) h->fwd_per_sm = 1;
-    if (h->bwd_per_sm < 1) h->bwd_per_sm = 1;
+    if (e == cudaSuccess && (h->fwd_per_sm < 1 || h->bwd_per_sm < 1)) e = cudaErrorLaunchOutOfResources;
     if (h->bwd_per_sm > srnl::kNormBlocks) h->bwd_per_sm = srnl::kNormBlocks;
   }
   if (e == cudaSuccess)

@@ -6,6 +6,10 @@ difference adds u each, rsqrtf 2 u.  An output rounded to its type adds eps / 2 
 column's sum over rows is at most rows / 148 + 8 + 4 + 37 + 32 additions (a block's rows, its groups and
 warps, 1184 partials over 32 warps), under 200 for the rows used here.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -286,3 +290,30 @@ def test_refusals():
             S.srnl_ln_forward(h, x, g, g, y)
     finally:
         h.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_odd_rows_whose_weights_just_fill_a_block(dtype):
+    """Odd rows keep gamma and beta in shared memory: 48 KB and a little less or more of them, in a process of its own,
+    so that no handle of longer rows has raised the kernels' limit before."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = f"""
+import numpy as np, torch, sys
+sys.path[:0] = [{here!r}, {os.path.dirname(here)!r}]
+import self_referential_nested_b200 as S
+from test_gpu_norm import DT, U, forward, make, reference
+for dim in (6091, 6095, 6097, 6101, 6113, 6121, 6127, 6129, 6135):
+    t = make(5, dim, {dtype!r}, seed=dim)
+    h = S.srnl_ln_create(dict(dim=dim, act_dtype={dtype!r}))
+    y, mean, rstd = forward(h, t)
+    ref = reference(t, float(np.float32(1e-6)))[0]
+    # a rounding of the output, and fp32 sums and products a hundred steps long
+    assert float((y.double() - ref).norm()) <= (torch.finfo(DT[{dtype!r}]).eps / 2 + 100 * U) * float(ref.norm()), dim
+    dx = torch.full_like(y, float("nan"))
+    S.srnl_ln_backward(h, t["x"], t["dy"], t["gamma"], mean, rstd, dx)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(dx).all())
+    h.close()
+"""
+    done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
