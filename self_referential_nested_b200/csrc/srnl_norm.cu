@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -434,11 +435,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float2 t = make_float2(0.f, 0.f), u = make_float2(0.f, 0.f);
+      const bool far = ODD && fabsf(mean[q] * rstd[q]) > FLT_MAX;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
+        const int c = c0 + i * cs;
+        const float2 off = both(on[i] ? -mean[q] : 0.f);
         float2 xv[H], yv[H], gw[H];
-        unpack<T>(clip<T, LPR, ODD>(xr[q][i], c0 + i * cs, dim), xv);
-        unpack<T>(clip<T, LPR, ODD>(yr[q][i], c0 + i * cs, dim), yv);
+        unpack<T>(clip<T, LPR, ODD>(xr[q][i], c, dim), xv);
+        unpack<T>(clip<T, LPR, ODD>(yr[q][i], c, dim), yv);
         if (!on[i]) {
 #pragma unroll
           for (int e = 0; e < H; ++e) gw[e] = make_float2(0.f, 0.f);
@@ -446,12 +450,20 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 #pragma unroll
           for (int e = 0; e < H; ++e) gw[e] = g[i * H + e];
         } else {
-          load_weights<V>(gp + c0 + i * cs, gw);
+          load_weights<V>(gp + c, gw);
         }
+#pragma unroll
+        for (int e = 0; e < H; ++e) xh[q][i * H + e] = __fmul2_rn(__fadd2_rn(xv[e], off), both(rstd[q]));
+        // outside the row xhat only has to be finite, as dy is zero there; mean rstd may not be
+        if (ODD && far && (c < 0 || c + V > dim))
+#pragma unroll
+          for (int e = 0; e < H; ++e) {
+            if (c + 2 * e < 0 || c + 2 * e >= dim) xh[q][i * H + e].x = 0.f;
+            if (c + 2 * e + 1 < 0 || c + 2 * e + 1 >= dim) xh[q][i * H + e].y = 0.f;
+          }
 #pragma unroll
         for (int e = 0; e < H; ++e) {
           const int k = i * H + e;
-          xh[q][k] = __fmul2_rn(__fadd2_rn(xv[e], both(-mean[q])), both(rstd[q]));
           dg[k] = __ffma2_rn(yv[e], xh[q][k], dg[k]);
           db[k] = __fadd2_rn(db[k], yv[e]);
           w[q][k] = __fmul2_rn(yv[e], gw[e]);

@@ -317,3 +317,32 @@ for dim in (6091, 6095, 6097, 6101, 6113, 6121, 6127, 6129, 6135):
 """
     done = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert done.returncode == 0, done.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dim", [3, 20, 33, 100, 301, 1000, 1533, 2052, 2500, 8191])
+def test_backward_of_a_row_far_from_zero(dim, dtype):
+    """A constant row of 1e36 with 1 / sqrt(eps) as its rstd: x - mean is zero, mean rstd beyond fp32.  No column outside
+    the row, on a lane with nothing to do or in a unit shared with a neighbour, enters its sums."""
+    t = make(6, dim, dtype, seed=dim)
+    t["x"][2] = 1e36
+    mean, rstd = t["x"].double().mean(1).float(), torch.ones(6, device="cuda")
+    mean[2], rstd[2] = t["x"][2, 0].float(), 1000.0
+    h = S.srnl_ln_create(dict(dim=dim, act_dtype=dtype))
+    try:
+        dx = torch.full_like(t["x"], float("nan"))
+        dg, db = torch.empty(dim, device="cuda"), torch.empty(dim, device="cuda")
+        S.srnl_ln_backward(h, t["x"], t["dy"], t["gamma"], mean, rstd, dx, dg, db)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    r64, dy = rstd.double()[:, None], t["dy"].double()
+    xh = (t["x"].double() - mean.double()[:, None]) * r64
+    w = dy * t["gamma"].double()
+    ref = r64 * (w - w.mean(1, keepdim=True) - xh * (w * xh).mean(1, keepdim=True))
+    half = torch.finfo(DT[dtype]).eps / 2
+    # as for the shapes above
+    big = r64 * (6 * w.abs() + 50 * w.abs().mean(1, keepdim=True) + 56 * xh.abs() * (w * xh).abs().mean(1, keepdim=True))
+    assert bool(((dx.double() - ref).abs() <= half * ref.abs() + U * (big + 4 * ref.abs())).all())
+    assert bool(((dg.double() - (dy * xh).sum(0)).abs() <= 200 * U * (dy * xh).abs().sum(0)).all())
+    assert bool(((db.double() - dy.sum(0)).abs() <= 200 * U * dy.abs().sum(0)).all())
