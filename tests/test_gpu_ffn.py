@@ -292,3 +292,45 @@ def test_no_rows_and_refusals():
         refused("training", S.srnl_ffn_backward, t["x"], gate, gate.clone(), t["dy"], t["p"], y)
     finally:
         h.close()
+
+
+@pytest.mark.parametrize("rows", [8, 300])   # few rows, and tiles
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_over_their_range(act, rows):
+    """act(v) and its slope for every v on a grid from far below zero, where they are small beside v, to above: identity
+    weights make y act(v), and the gradients act(v) and act'(v), each after one or two roundings.
+
+    Relative to the magnitude of its terms each is off by at most 2^-14: the exponential's argument by two roundings and
+    its own, 2.5 u |v|^2 / 2 ln 2 / ln 2 = 210 u at -13 (SiLU: 2 u |v| = 174 u at -87), the exponential and the reciprocal
+    by 4 u each, the rest of the formula by 2^-18; 2^-14 is 1024 u.  Beside that only what lies below fp32's smallest
+    normal number is lost."""
+    n = 64
+    eye, zero = torch.eye(n, device="cuda", dtype=BF), torch.zeros(n, n, device="cuda", dtype=BF)
+    lowest = -12.75 if act == "gelu" else -80.0
+    v = torch.linspace(lowest, 6, rows * n, device="cuda").to(BF).view(rows, n)
+    one = torch.ones(rows, n, device="cuda", dtype=BF)
+    x, dy = torch.cat([v, one], 1), torch.cat([one, 0 * one], 1)
+    p = {"W_gate": torch.cat([eye, zero], 1), "W_up": torch.cat([zero, eye], 1), "W_down": torch.cat([eye, zero], 0)}
+    h = S.srnl_ffn_create(dict(dim=2 * n, hidden=n, max_rows=rows, activation=act, training=True))
+    try:
+        y, dx = torch.empty_like(x), torch.empty_like(x)
+        gate, up = torch.empty_like(v), torch.empty_like(v)
+        S.srnl_ffn_forward(h, x, p, y, gate=gate, up=up)
+        S.srnl_ffn_backward(h, x, gate, up, dy, p, dx)
+        torch.cuda.synchronize()
+        S.srnl_ffn_device_status(h)
+    finally:
+        h.close()
+    assert torch.equal(gate, v) and torch.equal(up, one) and not bool(y[:, n:].any())
+    u = v.double()
+    f, df = act64(u, act)
+    if act == "silu":
+        s = torch.sigmoid(u)
+        terms = s + u.abs() * s * torch.sigmoid(-u)
+        df = s + u * s * torch.sigmoid(-u)   # 1 - s without cancellation
+    else:
+        terms = 0.5 * torch.special.erfc(-u / math.sqrt(2)) + u.abs() * torch.exp(-u * u / 2) / math.sqrt(2 * math.pi)
+    for name, got, ref, size in (("y", y[:, :n], f, f.abs()), ("act", dx[:, n:], f, f.abs()), ("slope", dx[:, :n], df, terms)):
+        # rounded to bf16 once; the second time it is a bf16 number already
+        off = (got.double() - ref).abs() / (HALF * ref.abs() + 2.0 ** -14 * size + 2.0 ** -120)
+        assert float(off.max()) <= 1, (name, float(off.max()), float(u.flatten()[off.argmax()]))
