@@ -51,7 +51,7 @@ constexpr uint32_t kBoxBytes = kC * 128; // 128 tokens x 64 channels
 constexpr uint32_t kTile = 2 * kBoxBytes;
 __host__ __device__ constexpr int la_threads(int nh) { return 128 * (3 + nh); }   // loads and products, 4 row warps a head, 8 state warps
 constexpr int kMaxSorted = 512;          // sequences that a CTA ranks by length
-constexpr int kSegFormers = 16, kSegThreads = 128 + 32 * kSegFormers;   // of the segments' kernel
+constexpr int kSegFormers = 8, kSegThreads = 128 + 32 * kSegFormers;   // of the segments' kernel
 constexpr int kStateThreads = 256;
 
 struct LaMaps {
@@ -734,9 +734,12 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
 
 // ------------------------------------------------------------------ the segments' states
 // What a segment adds to the state, from zero: sum_j g^(tokens behind j) b_j c_j^T.  The weights
-// reach to the segment's end, so the products of all its chunks add up in TMEM.
+// reach to the segment's end, so the chunks' products add up as they are: in the formers' fp32 registers,
+// not in TMEM, where a segment of 128 chunks with a decay next to one came out 3.7e-5 of its norm too
+// small (now 0.4e-6; 1 x 16384, 16 heads of 128, returned state included: 114 us either way).  Eight
+// formers have the registers for it, and form as fast as sixteen.
 constexpr int kSegStages = 3;
-enum { sFull = 0, sFree = kSegStages, sParts = 2 * kSegStages, sDone = sParts + 2, sBars = sDone + 2 };   // parts and done: one for each buffer
+enum { sFull = 0, sFree = kSegStages, sParts = 2 * kSegStages, sDone = sParts + 2, sTaken = sDone + 2, sBars };   // parts and done: one for each buffer
 
 template <int D>
 __global__ void __launch_bounds__(kSegThreads, 1)
@@ -762,7 +765,7 @@ __global__ void __launch_bounds__(kSegThreads, 1)
   }
   if (tid == 0) {
     *failed = 0;
-    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], i >= sParts && i < sDone ? kSegFormers : i >= sFree && i < sParts ? kSegFormers + 1 : 1);
+    for (int i = 0; i < sBars; ++i) mbar_init(&bar[i], (i >= sParts && i < sDone) || i == sTaken ? kSegFormers : i >= sFree && i < sParts ? kSegFormers + 1 : 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   for (int i = tid; i < NH * kC; i += kSegThreads) {   // weights of a whole chunk
@@ -800,20 +803,39 @@ __global__ void __launch_bounds__(kSegThreads, 1)
         const uint64_t dc = desc_mn_major(smem_u32(sm + (2 * s + 1) * kTile), kBoxBytes);
         mbar_pass(&bar[sFull + s], k / kSegStages & 1, failed);
         mbar_pass(&bar[sParts + (k & 1)], k >> 1 & 1, failed);
+        if (k > 0) mbar_pass(&bar[sTaken], (k - 1) & 1, failed);
         tmem_fence_after();
         for (int part = exact ? 2 : 1; part >= 0; --part)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             mma_k16_tmem_a(tmem, tP + (k & 1) * 192 + part * 64 + i * 8, dc + (uint64_t)i * 128, iZ,
-                            k > 0 || part < (exact ? 2 : 1) || i > 0);
+                            part < (exact ? 2 : 1) || i > 0);
         mma_commit(&bar[sDone + (k & 1)]);
         mma_commit(&bar[sFree + s]);
       }
     }
   } else if (warp >= 4) {
-    // 32 channels and a share of the tokens a warp
+    // 32 channels and a share of the tokens a warp; of the sum, those channels' rows and a share of the columns
+    constexpr int kCols = D / (kSegFormers / 4);
     const int q = warp & 3, share = (warp - 4) >> 2, h = NH == 2 ? q >> 1 : 0, head = group * NH + h;
     const float lg = head < args.heads ? args.log2g[head] : 0.f;
+    float sum[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) sum[j] = 0.f;
+    auto take = [&](int k) {   // chunk k's products
+      mbar_pass(&bar[sDone + (k & 1)], k >> 1 & 1, failed);
+      __syncwarp();
+      tmem_fence_after();
+#pragma unroll
+      for (int cb = 0; cb < kCols / 32; ++cb) {
+        float v[32];
+        tmem_ld32(v, tmem + ((uint32_t)(32 * q) << 16) + (NH == 2 ? h * 64 : 0) + share * kCols + cb * 32);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[32 * cb + j] += v[j];
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    };
     for (int k = 0; k < chunks; ++k) {
       const int s = k % kSegStages, t0 = begin + k * kC;
       const Chunk c = chunk_of(t0, end, n, rev);
@@ -842,29 +864,18 @@ __global__ void __launch_bounds__(kSegThreads, 1)
       tmem_wait_st();
       warp_arrive(&bar[sParts + (k & 1)], lane);
       if (lane == 0) mbar_arrive(&bar[sFree + s]);
-    }
-    if (warp < 8) {
-      const int r = 32 * q + lane;
-      if (chunks > 0) mbar_pass(&bar[sDone + ((chunks - 1) & 1)], (chunks - 1) >> 1 & 1, failed);
-      tmem_fence_after();
-      float* dst = args.seg_state +
-                   ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * dr * dr + (int64_t)(r % D) * dr;
-#pragma unroll
-      for (int cb = 0; cb < D / 32; ++cb) {
-        float v[32];
-        if (chunks > 0) {
-          tmem_ld32(v, tmem + ((uint32_t)(32 * q) << 16) + (NH == 2 ? h * 64 : 0) + cb * 32);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.f;
-        }
-        if (head < args.heads && r % D < dr && cb * 32 < dr)
-#pragma unroll
-          for (int j = 0; j < 32; j += 4)
-            *reinterpret_cast<float4*>(dst + cb * 32 + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+      if (k > 0) {
+        take(k - 1);
+        warp_arrive(&bar[sTaken], lane);
       }
     }
+    if (chunks > 0) take(chunks - 1);
+    const int r = 32 * q + lane;
+    float* dst = args.seg_state + ((((int64_t)which * args.B + batch) * args.heads + head) * args.segs + seg) * dr * dr +
+                 (int64_t)(r % D) * dr + share * kCols;
+    if (head < args.heads && r % D < dr && share * kCols < dr)
+#pragma unroll
+      for (int j = 0; j < kCols; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(sum[j], sum[j + 1], sum[j + 2], sum[j + 3]);
   }
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
@@ -893,6 +904,12 @@ __global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant_
   float cur = P.z0 != nullptr ? P.z0[sq * D * D + (P.z0_t ? (i % D) * D + i / D : i)] : 0.f;
   float* at = args.seg_state + ((int64_t)which * args.B * args.heads + sq) * args.segs * D * D + i;
   const float lg = args.log2g[head];
+  // g^m as its difference from one where that is small, as where the state is updated chunk by chunk
+  auto factor = [&](int m) {
+    const float e = lg * (float)m;
+    return e > -1.f ? make_float2(expm1f(e * 0.69314718055994531f), 1.f) : make_float2(exp2f(e), 0.f);
+  };
+  const float2 whole = factor(args.seg_len);
   constexpr int kAhead = 8;   // loads in flight
   for (int s0 = 0; s0 < args.segs; s0 += kAhead) {
     float add[kAhead];
@@ -905,7 +922,11 @@ __global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant_
       const int len = min(max(n - s * args.seg_len, 0), args.seg_len);
       at[(int64_t)s * D * D] = cur;
       // z0 of a reversed pass meets its first token undecayed
-      if (len > 0) cur = fmaf(exp2f(lg * (float)(P.reverse && s == 0 ? len - 1 : len)), cur, add[j]);
+      if (len > 0) {
+        const bool lead = P.reverse && s == 0;
+        const float2 f = len == args.seg_len && !lead ? whole : factor(lead ? len - 1 : len);
+        cur = fmaf(f.x, cur, f.y * cur) + add[j];
+      }
     }
   }
 }

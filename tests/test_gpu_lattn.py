@@ -434,3 +434,44 @@ def test_padding_of_a_short_last_chunk_stays_out_of_the_state(lo):
         S.srnl_lattn_device_status(h)
     finally:
         h.close()
+
+
+def long_sum(a, b, w, H, d):
+    """sum_t w[h, t] a_t b_t^T in 64 bits, a piece at a time: [B, H, d, d]."""
+    B, T, _ = a.shape
+    out = torch.zeros(B, H, d, d, device="cuda", dtype=torch.float64)
+    for x in range(B):
+        for t in range(0, T, 8192):
+            p, r = (y[x, t:t + 8192].double().view(-1, H, d).transpose(0, 1) for y in (a, b))
+            out[x] += (p * w[:, t:t + 8192, None]).transpose(-1, -2) @ r
+    return out
+
+
+@pytest.mark.parametrize("B,T,H,d", [(4, 32768, 32, 64), (1, 16384, 16, 128), (2, 8192, 37, 64), (1, 65536, 3, 32), (3, 300, 6, 128),
+                                     (2, 500, 6, 64), (1, 600, 6, 32)])
+def test_states_of_long_memories(B, T, H, d):
+    """The returned state and its gradient, head by head, to 2e-6 of their norm with memories that never fade.
+
+    A chunk's products are summed in steps of 16 tokens, three parts each: 24 steps, which cut off half of a unit (2^-24 of
+    the sum so far, itself half of the whole on average): 0.7e-6.  The chunks' sums, 256 of them at most, add 2^-25 each at
+    random, 0.5e-6; weights and factors 4 u = 0.25e-6."""
+    gen = torch.Generator(device="cuda").manual_seed(T + d)
+    q, k, v = (torch.randn(B, T, H * d, device="cuda", generator=gen).to(BF) for _ in range(3))
+    decay = np.array([[1.0, 1 - 2.0 ** -20, 0.999][i % 3] for i in range(H)], dtype=np.float32)
+    st, ds = torch.empty(B, H, d, d, device="cuda"), torch.empty(B, H, d, d, device="cuda")
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+    try:
+        o = torch.empty_like(q)
+        S.srnl_lattn_forward(h, q, k, v, o, state_out=st)
+        g = [torch.empty_like(q) for _ in range(3)]
+        S.srnl_lattn_backward(h, q, k, v, v, *g, dstate_in=ds)
+        torch.cuda.synchronize()
+        S.srnl_lattn_device_status(h)
+    finally:
+        h.close()
+    lg = torch.tensor(decay, device="cuda", dtype=torch.float64).log()[:, None]
+    i = torch.arange(T, device="cuda")
+    for got, a, e in ((st, k, T - 1 - i), (ds, q, i + 1)):
+        ref = long_sum(a, v, torch.exp(lg * e), H, d)
+        off = (got.double() - ref).flatten(2).norm(dim=2) / ref.flatten(2).norm(dim=2)
+        assert float(off.max()) <= 2e-6, off
