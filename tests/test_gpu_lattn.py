@@ -475,3 +475,31 @@ def test_states_of_long_memories(B, T, H, d):
         ref = long_sum(a, v, torch.exp(lg * e), H, d)
         off = (got.double() - ref).flatten(2).norm(dim=2) / ref.flatten(2).norm(dim=2)
         assert float(off.max()) <= 2e-6, off
+
+
+@pytest.mark.parametrize("T,at,g", [(300, 270, 0.97), (300, 100, 0.99), (1000, 200, 0.999), (1000, 990, 0.97)])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_one_token_in_the_state(d, T, at, g):
+    """All tokens but one are zeros: its trace in the returned state holds g^m k v^T to 32 u (u = 2^-24), where two bf16 parts
+    of g^m k would leave up to 64 u.  Roundings: the power 4 u and its argument 4 u, the factor it is split into and the
+    product with k 2 u, three cut sums 6 u, two chunks' or three segments' factors 3 u each."""
+    H = 8
+    gen = torch.Generator(device="cuda").manual_seed(d + at)
+    k, v = torch.zeros(1, T, H * d, device="cuda", dtype=BF), torch.zeros(1, T, H * d, device="cuda", dtype=BF)
+    k[:, at], v[:, at] = (torch.randn(1, H * d, device="cuda", generator=gen).to(BF) for _ in range(2))
+    st, o = torch.empty(1, H, d, d, device="cuda"), torch.empty_like(k)
+    h = S.srnl_lattn_create(dict(B=1, T=T, heads=H, d=d), np.full(H, g, np.float32))
+    try:
+        S.srnl_lattn_forward(h, k, k, v, o, state_out=st)
+        torch.cuda.synchronize()
+    finally:
+        h.close()
+    x = k[0, at].double().view(H, d) * float(np.float32(g)) ** (T - 1 - at)
+    y = v[0, at].double().view(H, d)
+    ref = x[:, :, None] * y[:, None, :]
+    assert bool(((st[0].double() - ref).abs() <= 32 * 2.0 ** -24 * ref.abs()).all())
+    # the inputs do tell two parts from three, whichever power the kernel splits: the chunk's own
+    w = k[0, at].float() * np.float32(g) ** np.float32(127 - at % 128 if T - at > 128 else T - 1 - at)
+    hi = w.to(BF).float()
+    two = hi.double() + (w - hi).to(BF).double()
+    assert float(((two - w.double()).abs() / w.abs()).max()) > 34 * 2.0 ** -24
