@@ -596,15 +596,39 @@ def _torch_dtype(act_dtype: int):
     return torch.bfloat16 if act_dtype == SRNL_BF16 else torch.float32
 
 
-def _dense(h: "_OpHandle", t, where: str, name: str, dtype, n: int) -> int:
-    """Address of a dense tensor of n values of dtype on the handle's device (0 for None);
-    raises otherwise."""
+def _lies_as(shape, full) -> bool:
+    """Whether a dense tensor of this shape lies in memory as one of the shape `full` does: the same
+    dimensions in the same order, some of them merged or split, those of size one left out."""
+    shape, full = [n for n in shape if n != 1], [n for n in full if n != 1]
+    while shape and full:
+        a, b = shape.pop(), full.pop()
+        if a < b:     # several of the tensor's make one
+            while a < b and shape:
+                a *= shape.pop()
+        else:
+            while b < a and full:
+                b *= full.pop()
+        if a != b:
+            return False
+    return not shape and not full
+
+
+def _dense(h: "_OpHandle", t, where: str, name: str, dtype, full) -> int:
+    """Address of a dense tensor of dtype on the handle's device, of the shape `full` or one that
+    lies in memory the same way (0 for None); raises otherwise."""
     if t is None:
         return 0
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != h._device or not t.is_contiguous():
-        raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a dense CUDA tensor of {n} {dtype} values on device "
-                                             f"{h._device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.dtype is not dtype or t.get_device() != h._device or not t.is_contiguous() \
+            or not (t.shape == full or _lies_as(t.shape, full)):
+        raise SrnlError(SRNL_E_INVAL, where, f"{name} must be a dense CUDA tensor of {'x'.join(map(str, full))} {dtype} values "
+                                             f"on device {h._device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
+
+
+def _row_shape(x, width: int):
+    """x's rows of `width` values: their number, and x's own shape where it ends in the width."""
+    rows, n = x.numel() // width, x.shape
+    return rows, (n if n and n[-1] == width else (rows, width))
 
 
 class _OpHandle:
@@ -664,11 +688,11 @@ def srnl_ln_forward(h: SrnlLn, x, gamma, beta, y, mean=None, rstd=None, stream=N
     """y <- layer norm of x ([..., dim] CUDA tensors of the handle's act dtype; gamma, beta
     float32 [dim]); mean, rstd: float32 [rows], written when given."""
     w, hd, d, f32 = "srnl_ln_forward", h.handle, h._dim, h._f32
-    rows = x.numel() // d
-    n = rows * d
+    rows, n = _row_shape(x, d)
+    r, d = (rows,), (d,)
     h._check(load_library().srnl_ln_forward(
         hd, _dense(h, x, w, "x", h._dtype, n), _dense(h, gamma, w, "gamma", f32, d), _dense(h, beta, w, "beta", f32, d),
-        _dense(h, y, w, "y", h._dtype, n), _dense(h, mean, w, "mean", f32, rows), _dense(h, rstd, w, "rstd", f32, rows), rows,
+        _dense(h, y, w, "y", h._dtype, n), _dense(h, mean, w, "mean", f32, r), _dense(h, rstd, w, "rstd", f32, r), rows,
         _stream(stream)), w)
 
 
@@ -676,12 +700,12 @@ def srnl_ln_backward(h: SrnlLn, x, dy, gamma, mean, rstd, dx, dgamma=None, dbeta
     """dx <- dL/dx for upstream dy (+ dres when given); dgamma, dbeta (float32 [dim]) are
     overwritten when given.  mean, rstd: the forward's."""
     w, hd, d, f32 = "srnl_ln_backward", h.handle, h._dim, h._f32
-    rows = x.numel() // d
-    n = rows * d
+    (rows, n), dt = _row_shape(x, d), h._dtype
+    r, d = (rows,), (d,)
     h._check(load_library().srnl_ln_backward(
-        hd, _dense(h, x, w, "x", h._dtype, n), _dense(h, dy, w, "dy", h._dtype, n), _dense(h, dres, w, "dres", h._dtype, n),
-        _dense(h, gamma, w, "gamma", f32, d), _dense(h, mean, w, "mean", f32, rows), _dense(h, rstd, w, "rstd", f32, rows),
-        _dense(h, dx, w, "dx", h._dtype, n), _dense(h, dgamma, w, "dgamma", f32, d), _dense(h, dbeta, w, "dbeta", f32, d), rows,
+        hd, _dense(h, x, w, "x", dt, n), _dense(h, dy, w, "dy", dt, n), _dense(h, dres, w, "dres", dt, n),
+        _dense(h, gamma, w, "gamma", f32, d), _dense(h, mean, w, "mean", f32, r), _dense(h, rstd, w, "rstd", f32, r),
+        _dense(h, dx, w, "dx", dt, n), _dense(h, dgamma, w, "dgamma", f32, d), _dense(h, dbeta, w, "dbeta", f32, d), rows,
         _stream(stream)), w)
 
 
@@ -709,8 +733,8 @@ def srnl_ffn_create(cfg: Dict) -> SrnlFfn:
 
 
 def _ffn_weights(h: SrnlFfn, t: Optional[Dict], where: str) -> _FfnWeights:
-    n, t = h._dim * h._hidden, t or {}
-    return _FfnWeights(*[_dense(h, t.get(k), where, k, h._dtype, n) for k in FFN_KEYS])
+    d, f, t = h._dim, h._hidden, t or {}
+    return _FfnWeights(*[_dense(h, t.get(k), where, k, h._dtype, (d, f) if k == "W_down" else (f, d)) for k in FFN_KEYS])
 
 
 def srnl_ffn_forward(h: SrnlFfn, x, params: Dict, y, res=None, gate=None, up=None, stream=None) -> None:
@@ -718,20 +742,21 @@ def srnl_ffn_forward(h: SrnlFfn, x, params: Dict, y, res=None, gate=None, up=Non
     [..., dim]; params: W_gate, W_up [hidden, dim], W_down [dim, hidden] in bf16; gate, up
     [rows, hidden] keep the pre-activations for the backward pass when given."""
     w, hd, dt = "srnl_ffn_forward", h.handle, h._dtype
-    rows = x.numel() // h._dim
-    n, f = rows * h._dim, rows * h._hidden
+    rows, n = _row_shape(x, h._dim)
+    f = (rows, h._hidden)
     p = _ffn_weights(h, params, w)
     h._check(load_library().srnl_ffn_forward(
-        hd, _dense(h, x, w, "x", dt, n), ctypes.byref(p), _dense(h, res, w, "res", dt, n), _dense(h, y, w, "y", dt, n),
-        _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f), rows, _stream(stream)), w)
+        hd, _dense(h, x, w, "x", dt, n), ctypes.byref(p), _dense(h, res, w, "res", dt, n),
+        _dense(h, y, w, "y", dt, n), _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f), rows,
+        _stream(stream)), w)
 
 
 def srnl_ffn_backward(h: SrnlFfn, x, gate, up, dy, params: Dict, dx, grads: Optional[Dict] = None, stream=None) -> None:
     """dx <- dL/dx for upstream dy (dx None skips it); ``grads`` maps any of FFN_KEYS to bf16
     CUDA tensors in the weights' layouts, which are overwritten.  gate, up: the forward's."""
     w, hd, dt = "srnl_ffn_backward", h.handle, h._dtype
-    rows = x.numel() // h._dim
-    n, f = rows * h._dim, rows * h._hidden
+    rows, n = _row_shape(x, h._dim)
+    f = (rows, h._hidden)
     p, g = _ffn_weights(h, params, w), _ffn_weights(h, grads, w)
     h._check(load_library().srnl_ffn_backward(
         hd, _dense(h, x, w, "x", dt, n), _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f),
@@ -788,10 +813,10 @@ def srnl_lattn_forward(h: SrnlLattn, q, k, v, o, lengths=None, state_in=None, st
     """o <- linear attention of q, k, v (bf16 [B, T, heads * d], tokens ld elements apart).
     lengths: int32 [B]; state_in, state_out: float32 [B, heads, d, d]."""
     w, hd, c = "srnl_lattn_forward", h.handle, h._c
-    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, h._f32
+    n, s, f32 = (c.B, c.T, c.heads * c.d), (c.B, c.heads, c.d, c.d), h._f32
     h._check(load_library().srnl_lattn_forward(
         hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(h, o, w, "o", h._dtype, n),
-        _dense(h, lengths, w, "lengths", h._i32, c.B), _dense(h, state_in, w, "state_in", f32, s),
+        _dense(h, lengths, w, "lengths", h._i32, (c.B,)), _dense(h, state_in, w, "state_in", f32, s),
         _dense(h, state_out, w, "state_out", f32, s), _stream(stream)), w)
 
 
@@ -800,11 +825,11 @@ def srnl_lattn_backward(h: SrnlLattn, q, k, v, do, dq, dk, dv, lengths=None, sta
     """dq, dk, dv <- the gradients for upstream do (dense) and dstate_out; dstate_in receives the
     gradient of state_in when given."""
     w, hd, c = "srnl_lattn_backward", h.handle, h._c
-    n, s, f32 = c.B * c.T * c.heads * c.d, c.B * c.heads * c.d * c.d, h._f32
+    n, s, f32 = (c.B, c.T, c.heads * c.d), (c.B, c.heads, c.d, c.d), h._f32
     h._check(load_library().srnl_lattn_backward(
         hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(h, do, w, "do", h._dtype, n),
         h._rows(dq, w, "dq", 1), h._rows(dk, w, "dk", 1), h._rows(dv, w, "dv", 1),
-        _dense(h, lengths, w, "lengths", h._i32, c.B), _dense(h, state_in, w, "state_in", f32, s),
+        _dense(h, lengths, w, "lengths", h._i32, (c.B,)), _dense(h, state_in, w, "state_in", f32, s),
         _dense(h, dstate_out, w, "dstate_out", f32, s), _dense(h, dstate_in, w, "dstate_in", f32, s), _stream(stream)), w)
 
 
@@ -814,8 +839,8 @@ def srnl_lattn_step(h: SrnlLattn, q, k, v, o, state, stream=None) -> None:
     w, hd, c = "srnl_lattn_step", h.handle, h._c
     h._check(load_library().srnl_lattn_step(
         hd, h._rows(q, w, "q", 0), h._rows(k, w, "k", 0), h._rows(v, w, "v", 0),
-        _dense(h, o, w, "o", h._dtype, c.B * c.heads * c.d),
-        _dense(h, state, w, "state", h._f32, c.B * c.heads * c.d * c.d), _stream(stream)), w)
+        _dense(h, o, w, "o", h._dtype, (c.B, c.heads * c.d)),
+        _dense(h, state, w, "state", h._f32, (c.B, c.heads, c.d, c.d)), _stream(stream)), w)
 
 
 def srnl_lattn_device_status(h: SrnlLattn) -> None:

@@ -1,8 +1,10 @@
 """Host-side refusals of the trainable block's operators: bad configurations and NULL arguments
 are turned away before any device work."""
 import ctypes
+import types
 
 import pytest
+import torch
 
 import self_referential_nested_b200 as S
 
@@ -100,3 +102,32 @@ def test_lattn_null_arguments_fail_cleanly(lib):
     assert lib.srnl_lattn_step(*[None] * 7) == S.SRNL_E_INVAL
     assert lib.srnl_lattn_device_status(None) == S.SRNL_E_INVAL
     lib.srnl_lattn_destroy(None)
+
+
+@pytest.mark.parametrize("shape,full,lies", [
+    ((5, 64), (5, 64), True), ((64, 5), (5, 64), False), ((2, 3, 64), (6, 64), True), ((2, 3, 4, 16), (6, 64), True),
+    ((384,), (6, 64), True), ((1, 6, 1, 64), (6, 64), True), ((6, 64, 1), (6, 64), True), ((4, 96), (6, 64), False),
+    ((3, 2, 64), (2, 3, 64), False), ((6, 64), (2, 3, 64), True), ((2, 192), (2, 3, 64), True), ((64, 2, 3), (2, 3, 64), False),
+    ((2, 3, 8, 8), (2, 3, 8, 8), True), ((3, 2, 8, 8), (2, 3, 8, 8), False), ((2, 8, 3, 8), (2, 3, 8, 8), False),
+    ((1, 1), (1,), True), ((), (1, 1), True), ((7,), (1,), False), ((7,), (1, 7), True), ((7, 1), (1, 7), True), ((14,), (7,), False),
+])
+def test_shapes_that_lie_as_they_should(shape, full, lies):
+    h = types.SimpleNamespace(_device=-1)   # of a host tensor
+    t = torch.zeros(shape, dtype=torch.bfloat16)
+    if lies:
+        assert S._dense(h, t, "call", "x", torch.bfloat16, full) == t.data_ptr()
+        return
+    with pytest.raises(S.SrnlError) as e:
+        S._dense(h, t, "call", "x", torch.bfloat16, full)
+    assert e.value.status == S.SRNL_E_INVAL and "x must be" in str(e.value)
+
+
+def test_dense_tensors_of_no_rows_and_other_kinds():
+    h = types.SimpleNamespace(_device=-1)
+    assert S._dense(h, None, "call", "x", torch.float32, (4,)) == 0
+    S._dense(h, torch.zeros(0, 40), "call", "x", torch.float32, (0, 40))
+    for bad in (torch.zeros(4, dtype=torch.float64), torch.zeros(5), torch.zeros(8)[::2], torch.zeros(0)):
+        with pytest.raises(S.SrnlError):
+            S._dense(h, bad, "call", "x", torch.float32, (4,))
+    with pytest.raises(S.SrnlError):   # on another device than the handle
+        S._dense(types.SimpleNamespace(_device=0), torch.zeros(4), "call", "x", torch.float32, (4,))

@@ -334,3 +334,25 @@ def test_activations_over_their_range(act, rows):
         # rounded to bf16 once; the second time it is a bf16 number already
         off = (got.double() - ref).abs() / (HALF * ref.abs() + 2.0 ** -14 * size + 2.0 ** -120)
         assert float(off.max()) <= 1, (name, float(off.max()), float(u.flatten()[off.argmax()]))
+
+
+def test_transposed_weights_and_rows_are_refused():
+    dim, hidden = 64, 128
+    t = make(4, dim, hidden)
+    h = S.srnl_ffn_create(dict(dim=dim, hidden=hidden, max_rows=4, training=True))
+    try:
+        y, gate, up = (torch.empty(4, n, device="cuda", dtype=BF) for n in (dim, hidden, hidden))
+        g = {k: torch.empty_like(v) for k, v in t["p"].items()}
+        flip = lambda v: v.t().contiguous()
+        calls = [(k, lambda k=k: S.srnl_ffn_forward(h, t["x"], dict(t["p"], **{k: flip(t["p"][k])}), y)) for k in S.FFN_KEYS]
+        calls += [(k, lambda k=k: S.srnl_ffn_backward(h, t["x"], gate, up, t["dy"], t["p"], y, dict(g, **{k: flip(g[k])})))
+                  for k in S.FFN_KEYS]
+        calls += [("x", lambda: S.srnl_ffn_forward(h, flip(t["x"]), t["p"], y)), ("res", lambda: S.srnl_ffn_forward(h, t["x"], t["p"], y, res=flip(y))),
+                  ("gate", lambda: S.srnl_ffn_forward(h, t["x"], t["p"], y, gate=flip(gate), up=up)),
+                  ("dy", lambda: S.srnl_ffn_backward(h, t["x"], gate, up, flip(t["dy"]), t["p"], y))]
+        for name, call in calls:
+            with pytest.raises(S.SrnlError) as e:
+                call()
+            assert e.value.status == S.SRNL_E_INVAL and f"{name} must be" in str(e.value)
+    finally:
+        h.close()

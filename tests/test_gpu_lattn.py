@@ -503,3 +503,28 @@ def test_one_token_in_the_state(d, T, at, g):
     hi = w.to(BF).float()
     two = hi.double() + (w - hi).to(BF).double()
     assert float(((two - w.double()).abs() / w.abs()).max()) > 34 * 2.0 ** -24
+
+
+def test_other_orders_of_the_axes_are_refused():
+    B, T, H, d = 2, 9, 3, 32
+    t = make(B, T, H, d)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.full(H, 0.9, np.float32))
+    try:
+        q, k, v, o = t["q"], t["k"], t["v"], torch.empty_like(t["q"])
+        flip = lambda x: x.transpose(0, 1).contiguous()
+        one = [x[:, 0].contiguous() for x in (q, k, v)]
+        g = [torch.empty_like(q) for _ in range(3)]
+        calls = [("o", lambda: S.srnl_lattn_forward(h, q, k, v, flip(o))), ("o", lambda: S.srnl_lattn_step(h, *one, flip(one[0]), t["s0"])),
+                 ("state_in", lambda: S.srnl_lattn_forward(h, q, k, v, o, state_in=flip(t["s0"]))),
+                 ("state_out", lambda: S.srnl_lattn_forward(h, q, k, v, o, state_out=flip(t["s0"]))),
+                 ("do", lambda: S.srnl_lattn_backward(h, q, k, v, flip(o), *g)),
+                 ("dstate_out", lambda: S.srnl_lattn_backward(h, q, k, v, o, *g, dstate_out=flip(t["s0"]))),
+                 ("state", lambda: S.srnl_lattn_step(h, *one, o[:, 0].contiguous(), flip(t["s0"])))]
+        for name, call in calls:
+            with pytest.raises(S.SrnlError) as e:
+                call()
+            assert e.value.status == S.SRNL_E_INVAL and f"{name} must be" in str(e.value)
+        S.srnl_lattn_forward(h, q, k, v, o.view(B, T, H, d), state_in=t["s0"].view(B * H, d, d))   # the same layout, told otherwise
+        torch.cuda.synchronize()
+    finally:
+        h.close()

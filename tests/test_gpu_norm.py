@@ -346,3 +346,22 @@ def test_backward_of_a_row_far_from_zero(dim, dtype):
     assert bool(((dx.double() - ref).abs() <= half * ref.abs() + U * (big + 4 * ref.abs())).all())
     assert bool(((dg.double() - (dy * xh).sum(0)).abs() <= 200 * U * (dy * xh).abs().sum(0)).all())
     assert bool(((db.double() - dy.sum(0)).abs() <= 200 * U * dy.abs().sum(0)).all())
+
+
+def test_transposed_rows_are_refused():
+    h = S.srnl_ln_create(dict(dim=64, act_dtype="bf16"))
+    try:
+        x, g = torch.zeros(5, 64, device="cuda", dtype=torch.bfloat16), torch.ones(64, device="cuda")
+        y, m = torch.empty_like(x), torch.zeros(5, device="cuda")
+        other = torch.zeros(64, 5, device="cuda", dtype=torch.bfloat16)
+        calls = [("x", lambda: S.srnl_ln_forward(h, other, g, g, y)), ("y", lambda: S.srnl_ln_forward(h, x, g, g, other)),
+                 ("dy", lambda: S.srnl_ln_backward(h, x, other, g, m, m, y)), ("dx", lambda: S.srnl_ln_backward(h, x, x, g, m, m, other)),
+                 ("dres", lambda: S.srnl_ln_backward(h, x, x, g, m, m, y, dres=other))]
+        for name, call in calls:
+            with pytest.raises(S.SrnlError) as e:
+                call()
+            assert e.value.status == S.SRNL_E_INVAL and f"{name} must be" in str(e.value)
+        S.srnl_ln_forward(h, x.view(5, 1, 64), g, g, y.view(5, 8, 8))   # the same rows, told otherwise
+        torch.cuda.synchronize()
+    finally:
+        h.close()
