@@ -943,6 +943,7 @@ srnl_status srnl_ffn_create(srnl_ffn** out, const srnl_ffn_config* cfg) {
   if (e == cudaSuccess) e = cudaMemset(h->arrived, 0, pairs * 2 * kEpiWarps * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // a call's stream need not wait for the one these ran on
   if (e == cudaSuccess) e = prepare_product<kGlu, SRNL_ACT_SILU>();
   if (e == cudaSuccess) e = prepare_product<kGlu, SRNL_ACT_GELU>();
   if (e == cudaSuccess) e = prepare_product<kPlain, 0>();

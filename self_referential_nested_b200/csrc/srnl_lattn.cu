@@ -229,6 +229,7 @@ srnl_status srnl_lattn_create(srnl_lattn** out, const srnl_lattn_config* cfg, co
   }
   if (e == cudaSuccess) e = cudaMalloc(&h->dev_err, sizeof(int));
   if (e == cudaSuccess) e = cudaMemset(h->dev_err, 0, sizeof(int));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);   // a call's stream need not wait for the one these and the copies ran on
   if (e == cudaSuccess) e = prepare_la_tc(cfg->d);
   if (e != cudaSuccess) {
     const srnl_status st = la_cuda_fail(nullptr, e, "linear attention create");

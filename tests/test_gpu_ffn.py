@@ -356,3 +356,29 @@ def test_transposed_weights_and_rows_are_refused():
             assert e.value.status == S.SRNL_E_INVAL and f"{name} must be" in str(e.value)
     finally:
         h.close()
+
+
+def test_a_new_handle_is_ready_for_any_stream():
+    """Creation clears the counters that products in parts rely on, on the default stream: behind work of that stream's own,
+    the handle is not returned before they are clear, and a call on a stream that waits for nothing finds them so."""
+    rows, dim, hidden = 300, 136, 4104
+    t = make(rows, dim, hidden, seed=3)
+    busy = torch.randn(8192, 8192, device="cuda", dtype=BF)
+    side = torch.cuda.Stream()
+    ys = []
+    for i in range(3):
+        torch.cuda.synchronize()
+        for _ in range(10):
+            busy @ busy
+        h = S.srnl_ffn_create(dict(dim=dim, hidden=hidden, max_rows=rows))
+        assert torch.cuda.default_stream().query()
+        try:
+            y = torch.full((rows, dim), float("nan"), device="cuda", dtype=BF)
+            torch.cuda.synchronize()
+            S.srnl_ffn_forward(h, t["x"], t["p"], y, stream=side)
+            torch.cuda.synchronize()
+            S.srnl_ffn_device_status(h)
+            ys.append(y)
+        finally:
+            h.close()
+    assert bool(torch.isfinite(ys[0]).all()) and all(torch.equal(y, ys[0]) for y in ys)

@@ -528,3 +528,29 @@ def test_other_orders_of_the_axes_are_refused():
         torch.cuda.synchronize()
     finally:
         h.close()
+
+
+def test_a_new_handle_is_ready_for_any_stream():
+    """Creation copies the decays on the default stream: behind work of that stream's own, the handle is not returned before
+    they are there, and a call on a stream that waits for nothing finds them."""
+    B, T, H, d = 2, 40, 3, 64
+    t = make(B, T, H, d, seed=4)
+    busy = torch.randn(8192, 8192, device="cuda", dtype=BF)
+    side = torch.cuda.Stream()
+    outs = []
+    for i in range(3):
+        torch.cuda.synchronize()
+        for _ in range(10):
+            busy @ busy
+        h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.full(H, 0.9, np.float32))
+        assert torch.cuda.default_stream().query()
+        try:
+            o, st = torch.full_like(t["q"], float("nan")), torch.empty_like(t["s0"])
+            torch.cuda.synchronize()
+            S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, state_in=t["s0"], state_out=st, stream=side)
+            torch.cuda.synchronize()
+            outs.append((o, st))
+        finally:
+            h.close()
+    assert all(torch.equal(a, b) for x in outs for a, b in zip(x, outs[0]))
+    within(outs[0][0], *reference(t, [0.9] * H, [T] * B, True, False)["o"])
