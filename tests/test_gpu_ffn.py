@@ -382,3 +382,24 @@ def test_a_new_handle_is_ready_for_any_stream():
         finally:
             h.close()
     assert bool(torch.isfinite(ys[0]).all()) and all(torch.equal(y, ys[0]) for y in ys)
+
+
+# More tiles than pairs of CTAs (74), so that a pair takes a second and a third one, in either tile width (columns, tiles):
+MANY_TILES = [
+    (5000, 1032, 1544),    # projections 256, 260; output 256, 100; hidden gradients 256, 140; gradients 256, 205
+    (20000, 264, 520),     # 256, 395; 256, 158; 256, 237; gradients in parts, 256, 230
+    (9473, 264, 264),      # output 128, 114; hidden gradients 128, 114
+    (4943, 64, 888),       # hidden gradients 128, 140
+    (3721, 8, 552),        # projections 128, 135
+    (257, 1032, 9000),     # output in parts, 128, 72; gradients in parts, 256, 600
+    (34, 3136, 7296),      # output in parts, 256, 52
+    (37, 1424, 832),       # gradients 128, 150
+    (157, 16, 8744),       # gradients in parts, 128, 151
+    (8885, 1392, 8),       # output 256, 210
+]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("rows,dim,hidden", MANY_TILES)
+def test_forward_and_backward_of_many_tiles(rows, dim, hidden, act):
+    test_forward_and_backward(rows, dim, hidden, act)
