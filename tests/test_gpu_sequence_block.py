@@ -300,3 +300,65 @@ def test_around_the_sequence_layer():
     finally:
         for h in (seq, ln, ff):
             h.close()
+
+
+def test_around_the_sequence_layer_value_by_value():
+    """The same chain: the feed-forward branch's pre-activations, output and gradients against its formulas in 64 bits, given
+    what the norms returned, to the branch's own tolerances; the sequence layer's output and gradient against its
+    oracle, to the bars of its own tests for bf16 outputs (1e-2 of the norm)."""
+    from oracle import srnl_grad as GR
+    from oracle import srnl_oracle as O
+    from test_gpu_ffn import act64
+    from test_gpu_ffn import within as ffn_within
+
+    inp = make_seq_inputs(2, 150, 64, 2, "bf16", seed=5)
+    B, T, D, hidden = inp.B, inp.T, inp.D, 3 * inp.D
+    t = make(B, T, inp.heads, D // inp.heads, hidden, seed=6)
+    x = torch.from_numpy(inp.x_bits.view(np.int16)).cuda().view(BF)
+    params = inp.params()
+    seq = S.srnl_seq_create(dict(B=B, T=T, D=D, heads=inp.heads, d=32, alpha=0.95, eps=1e-6, chunk=64, act_dtype="bf16",
+                                 gen_dtype="f32"), params)
+    ln = S.srnl_ln_create(dict(dim=D, eps=EPS, act_dtype="bf16"))
+    ff = S.srnl_ffn_create(dict(dim=D, hidden=hidden, max_rows=B * T, training=True))
+    try:
+        new = lambda *s, dt=BF: torch.empty(*s, device="cuda", dtype=dt)
+        n1, o, n2, y, dn, dx1, dn1 = (new(B, T, D) for _ in range(7))
+        m2, r2 = (new(B * T, dt=torch.float32) for _ in range(2))
+        gate, up, dW = new(B * T, hidden), new(B * T, hidden), {k: torch.empty_like(t[k]) for k in S.FFN_KEYS}
+        S.srnl_ln_forward(ln, x, t["g1"], t["b1"], n1)
+        S.srnl_seq_forward(seq, n1, o)
+        x1 = x + o
+        S.srnl_ln_forward(ln, x1, t["g2"], t["b2"], n2, m2, r2)
+        S.srnl_ffn_forward(ff, n2, t, y, res=x1, gate=gate, up=up)
+        S.srnl_ffn_backward(ff, n2, gate, up, t["dy"], t, dn, dW)
+        S.srnl_ln_backward(ln, x1, dn, t["g2"], m2, r2, dx1, dres=t["dy"])
+        S.srnl_seq_backward(seq, n1, dx1, dn1)
+        torch.cuda.synchronize()
+        S.srnl_seq_device_status(seq)
+        S.srnl_ffn_device_status(ff)
+    finally:
+        for h in (seq, ln, ff):
+            h.close()
+    rows = lambda v: v.reshape(B * T, -1).double()
+    v, dy, (Wg, Wu, Wd) = rows(n2), rows(t["dy"]), (t[k].double() for k in S.FFN_KEYS)
+    zero = torch.zeros((), device="cuda", dtype=torch.float64)
+    g64, u64 = v @ Wg.t(), v @ Wu.t()
+    ffn_within(gate, g64, v.abs() @ Wg.abs().t(), zero, D)
+    ffn_within(up, u64, v.abs() @ Wu.abs().t(), zero, D)
+    hid = act64(g64, "silu")[0] * u64
+    ffn_within(rows(y), hid @ Wd.t() + rows(x1), hid.abs() @ Wd.abs().t(), (hid ** 2) @ (Wd ** 2).t(), hidden)
+    g, u = gate.double(), up.double()
+    a, da = act64(g, "silu")
+    dh = dy @ Wd
+    dg, du, hid = dh * u * da, dh * a, a * u
+    ffn_within(rows(dn), dg @ Wg + du @ Wu, dg.abs() @ Wg.abs() + du.abs() @ Wu.abs(), (dg ** 2) @ (Wg ** 2) + (du ** 2) @ (Wu ** 2),
+               2 * hidden + D)
+    ffn_within(dW["W_gate"], dg.t() @ v, dg.abs().t() @ v.abs(), (dg ** 2).t() @ (v ** 2), B * T + D)
+    ffn_within(dW["W_up"], du.t() @ v, du.abs().t() @ v.abs(), (du ** 2).t() @ (v ** 2), B * T + D)
+    ffn_within(dW["W_down"], dy.t() @ hid, dy.abs().t() @ hid.abs(), (dy ** 2).t() @ (hid ** 2), B * T)
+    host = lambda v: v.float().cpu().numpy()
+    ref = O.sequence_forward(host(n1), params, alpha_max=0.95, chunk=64, heads=inp.heads)
+    ref = ref[0] if isinstance(ref, tuple) else ref
+    assert O.rel_fro(host(o), ref) <= 1e-2
+    ref = GR.sequence_backward(host(n1), params, host(dx1), alpha_max=0.95, chunk=64, heads=inp.heads)
+    assert O.rel_fro(host(dn1), ref["x"]) <= 1e-2
