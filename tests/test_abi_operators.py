@@ -131,3 +131,11 @@ def test_dense_tensors_of_no_rows_and_other_kinds():
             S._dense(h, bad, "call", "x", torch.float32, (4,))
     with pytest.raises(S.SrnlError):   # on another device than the handle
         S._dense(types.SimpleNamespace(_device=0), torch.zeros(4), "call", "x", torch.float32, (4,))
+
+
+def test_the_current_stream_without_private_names(monkeypatch):
+    """Another torch may lack the short way to the current stream's address; the public one gives the same."""
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=4711))
+    monkeypatch.setattr(torch, "_C", types.SimpleNamespace())
+    assert S._stream(None) == 4711
+    assert S._stream(12) == 12 and S._stream(types.SimpleNamespace(cuda_stream=34)) == 34
