@@ -575,8 +575,10 @@ SRNL_API srnl_status srnl_lattn_create(srnl_lattn** out, const srnl_lattn_config
  * a sequence's tokens from its length on are neither used nor written (a length is clamped to
  * 0..T).  state_in: fp32 [B][heads][d][d] (rows of k, columns of v), the memory before the
  * first token, or NULL for zeros; state_out: the memory after the last one, or NULL.  Outputs
- * overlap neither inputs nor one another.  A NaN or infinity in a token may reach the outputs
- * of its sequence's head from 127 tokens before it on, never other sequences or heads.
+ * overlap neither inputs nor one another.  What is not finite reaches what the recurrence lets
+ * it reach (as NaN, where sums decide): outputs of its sequence's head from its token on and the
+ * state behind them, no earlier outputs, other sequences or heads; segments of a sequence that
+ * meet it take twice their time.
  * Asynchronous on `stream`; calls on one handle must not overlap on the device. */
 SRNL_API srnl_status srnl_lattn_forward(srnl_lattn* h, const void* q, const void* k, const void* v, void* o,
                                         const int* lengths, const float* state_in, float* state_out, void* stream);
@@ -584,7 +586,8 @@ SRNL_API srnl_status srnl_lattn_forward(srnl_lattn* h, const void* q, const void
 /* Backward pass for d_o = dL/do (dense) and, when not NULL, dstate_out = dL/dstate_out: dq, dk
  * and dv (rows ld elements apart; tokens from a sequence's length on are left as they were)
  * and, when not NULL, dstate_in = dL/dstate_in.  Nothing of the forward is kept: the states are
- * formed again.  The decays are constants.  Equal inputs give equal bits.  Asynchronous. */
+ * formed again.  The decays are constants.  What is not finite goes where the gradients go: to
+ * dq from its token on, to dk and dv up to it.  Equal inputs give equal bits.  Asynchronous. */
 SRNL_API srnl_status srnl_lattn_backward(srnl_lattn* h, const void* q, const void* k, const void* v, const void* d_o,
                                          void* dq, void* dk, void* dv, const int* lengths, const float* state_in,
                                          const float* dstate_out, float* dstate_in, void* stream);

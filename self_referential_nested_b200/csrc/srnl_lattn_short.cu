@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(short_threads(D), D == 128 ? (TT == 8 ? 4 : 3)
     if (i < n) {
       float o = acc[k] * exp2f(lg * (float)(i + lead));
 #pragma unroll
-      for (int j = 0; j < TT; ++j) o = fmaf(p[i * kP + j], cv[j], o);
+      for (int j = 0; j < TT; ++j) o = fmaf(p[i * kP + j], j <= i ? cv[j] : 0.f, o);   // a later token may hold anything
       P.out[(row0 + step * i) * P.ldo + head * D + c] = __float2bfloat16_rn(o);
     }
   }

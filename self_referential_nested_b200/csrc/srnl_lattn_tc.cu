@@ -215,6 +215,70 @@ __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, in
   }
 }
 
+// Causality of what is not finite.  P c (3) multiplies a masked pair's zero with the later token's c, and zero
+// times NaN is NaN.  An infinity or NaN anywhere in a chunk's c thus shows in its first token's row, which
+// is watched; once there is one, the CTA makes its pass again with an eye on c: the rows' warps look
+// through their head's c, 32 tokens each, note the first token that has what is not finite, channel by
+// channel, and replace it by zero once the state's product, where it belongs, has taken it; after (3)
+// they put NaN from that token on.  Looking in the first pass cost 6 % and more (8 x 2048, 16 heads of
+// 128: 67 -> 75 us), the watch costs 0 to 2 % (backward of 64: 114 -> 116.5).
+constexpr int kNone = 255;
+// Sums of products of pairs: not finite where a value is not (or where values beyond 2^63 meet, which costs time only).
+__device__ __forceinline__ void add_pairs(uint32_t (&sum)[2], const uint4& x) {
+  asm volatile("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[0]) : "r"(x.x), "r"(x.y));
+  asm volatile("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(sum[1]) : "r"(x.z), "r"(x.w));
+}
+__device__ __forceinline__ bool not_finite(const uint32_t (&sum)[2]) {
+  return ((((sum[0] & 0x7F807F80u) + 0x00800080u) | ((sum[1] & 0x7F807F80u) + 0x00800080u)) & 0x80008000u) != 0u;
+}
+__device__ __forceinline__ bool look_through(const unsigned char* rows32, int rows, int lane) {
+  uint4 v[8];
+  const unsigned char* at = rows32 + lane * 16;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    v[i] = 4 * i + (lane >> 3) < rows ? *reinterpret_cast<const uint4*>(at + i * 512) : make_uint4(0u, 0u, 0u, 0u);
+  uint32_t sum[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) add_pairs(sum, v[i]);
+  return __any_sync(0xFFFFFFFFu, not_finite(sum));
+}
+// The rows in the chunk's order (rev: upwards from the last); a lane has two channels.  first: [64].
+__device__ __noinline__ void take_out(unsigned char* rows32, int rows, int rev, unsigned char* first, int lane) {
+  int at[2] = {kNone, kNone};
+  for (int i = 0; i < rows; ++i) {
+    const int r = rev ? rows - 1 - i : i;
+    unsigned short* v = reinterpret_cast<unsigned short*>(rows32 + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4);
+    for (int e = 0; e < 2; ++e)
+      if ((v[e] & 0x7F80u) == 0x7F80u) {
+        if (at[e] == kNone) at[e] = r;
+        v[e] = 0;
+      }
+  }
+  first[2 * lane] = (unsigned char)at[0];
+  first[2 * lane + 1] = (unsigned char)at[1];
+  fence_async();
+}
+// NaN in a row's channels of a box from the first bad token on.  first: [4 blocks of rows][2 boxes][64], seen: the
+// blocks that have any.
+__device__ __noinline__ void spoil_row(uint32_t acc, const unsigned char* first, uint32_t seen, int row, int rev) {
+#pragma unroll 1
+  for (int b = 0; b < 2; ++b) {
+    float v[32];
+    tmem_ld32(v, acc + 32 * b);
+    tmem_wait_ld();
+#pragma unroll 1
+    for (int q = 0; q < 4; ++q)
+      if (seen >> (8 * q) & 1)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int at = first[q * 128 + 32 * b + j];
+          if (at != kNone && (rev ? row <= 32 * q + at : row >= 32 * q + at)) v[j] = __int_as_float(0x7FC00000);
+        }
+    tmem_st32(acc + 32 * b, v);
+    tmem_wait_st();
+  }
+}
+
 // A warp's rows of a head's G (block q of 32 tokens), masked and decayed, as bf16 pairs over G's own
 // columns: block j's at 32 j .. + 15.  The distance falls along a row's columns (rises, in reverse).
 // Away from the diagonal the powers of g are one product after another from the nearest token on,
@@ -295,81 +359,67 @@ enum {   // barriers; two each of those that the next name leaves room for
   kG, kRows, kO2, kO, kOFree, kParts, kPDone = kParts + 2, kZ = kPDone + 2, kDZ, kClear, kBars
 };
 
-template <int D>
-__global__ void __launch_bounds__(la_threads(kC / D), 1)
-    decay_tc_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
+// A CTA's shared memory behind its seven tiles.
+template <int NH>
+struct LaShared {
+  float* wt;                    // [NH][kC]: weights of the chunk's rows of b
+  unsigned long long* bar;      // two sets: one for the second pass
+  uint32_t* tmem_slot;
+  int *failed, *again;
+  unsigned char* unsound;       // of c, two chunks in turn: the blocks of 32 rows that hold what is not finite [box][block]
+  unsigned char* first_bad;     // and the first such row [block][box][64]
+  __device__ __forceinline__ explicit LaShared(unsigned char* sm) {
+    wt = reinterpret_cast<float*>(sm + 7 * kTile);
+    bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
+    tmem_slot = reinterpret_cast<uint32_t*>(bar + 2 * kBars);
+    failed = reinterpret_cast<int*>(tmem_slot + 1);
+    again = failed + 1;
+    unsound = reinterpret_cast<unsigned char*>(again + 2);
+    first_bad = unsound + 16;
+  }
+};
+// What is a CTA's of a sequence of n tokens.
+struct LaShare {
+  int n, begin, end, chunks;
+  int chunks_z;   // chunks whose update of the state is of use
+  bool exact;     // the state leaves: a third part of w b
+  bool fresh;     // the first chunk meets a zero state
+};
+__device__ __forceinline__ LaShare share_of(const LaArgs& args, const LaPass& P, int batch, int seg) {
+  LaShare s;
+  s.n = args.T;
+  if (args.lengths != nullptr) s.n = min(max(args.lengths[batch], 0), args.T);
+  s.begin = seg * args.seg_len;
+  s.end = min(s.begin + args.seg_len, s.n);
+  s.chunks = s.end > s.begin ? (s.end - s.begin + kC - 1) / kC : 0;
+  // the segment that holds the last token (the first one of an empty sequence) writes the state
+  s.exact = P.zn != nullptr && seg == (s.n > 0 ? (s.n - 1) / args.seg_len : 0);
+  s.chunks_z = s.exact ? s.chunks : s.chunks - 1;
+  s.fresh = P.z0 == nullptr && seg == 0;
+  return s;
+}
+
+// The roles' work on a segment.  WATCH: with an eye on c, after a pass that met what is not finite; a
+// copy of its own, since in one loop both were 10 % slower than the first alone.
+template <int D, bool WATCH>
+__device__ __forceinline__ void decay_pass(const LaMaps& maps, const LaArgs& args, unsigned char* sm, uint32_t tmem, int which, int group, int batch) {
   constexpr int NH = kC / D;
-  extern __shared__ __align__(1024) unsigned char sm[];
   // two tiles of a (O leaves through a's, when its products are done), two of b, c, the state's two
   // parts and, for narrow heads, the ring of w b
   constexpr uint32_t kZPart = NH == 2 ? kTile / 2 : kTile;
   unsigned char *sa = sm, *sb = sa + 2 * kTile, *sc = sb + 2 * kTile, *zh = sc + kTile, *zl = zh + kZPart, *ps = zl + kZPart;
-  float* wt = reinterpret_cast<float*>(sm + 7 * kTile);  // [NH][kC]: weights of the chunk's rows of b
-  unsigned long long* bar = reinterpret_cast<unsigned long long*>(wt + NH * kC);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bar + kBars);
-  int* failed = reinterpret_cast<int*>(tmem_slot + 1);
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int seg = blockIdx.x, groups = (args.heads + NH - 1) / NH;
-  int which = blockIdx.z, group = blockIdx.y % groups, batch = blockIdx.y / groups;
-  if (smem_u32(sm) & 1023u) {           // the swizzled tiles' alignment
-    if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
-    return;
-  }
-
-  if (tid == 0) {
-    *failed = 0;
-    for (int i = 0; i < kBars; ++i) {
-      const bool rows = i == kRows || i == kOFree || i == kFreeA || i == kFreeA + 1, parts = i == kParts || i == kParts + 1;
-      mbar_init(&bar[i], rows || parts ? 4 * NH : i == kZ || i == kClear ? 8 : i == kFreeB || i == kFreeB + 1 ? 9 : i == kFreeC ? 2 : 1);
-    }
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (args.longest_first) {
-    // the CTAs do not all run at once: batch is the one with so many longer sequences
-    int* len = reinterpret_cast<int*>(sm);
-    const int per = groups * gridDim.z, id = blockIdx.z * gridDim.y + blockIdx.y, rank = id / per;
-    which = id % per / groups;
-    group = id % groups;
-    for (int i = tid; i < args.B; i += la_threads(NH)) len[i] = args.lengths[i];
-    __syncthreads();
-    for (int i = tid; i < args.B; i += la_threads(NH)) {
-      const int mine = len[i];
-      int before = 0;
-      for (int j = 0; j < args.B; ++j) before += len[j] > mine || (len[j] == mine && j < i);
-      if (before == rank) *tmem_slot = i;
-    }
-    __syncthreads();
-    batch = *tmem_slot;
-    fence_async();
-    __syncthreads();
-  }
+  const LaShared<NH> sh(sm);
+  float* wt = sh.wt;
+  unsigned long long* bar = sh.bar + (WATCH ? kBars : 0);
+  int *failed = sh.failed, *again = sh.again;
+  unsigned char *unsound = sh.unsound, *first_bad = sh.first_bad;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, seg = blockIdx.x;
   const LaPass& P = args.pass[which];
   const int rev = P.reverse, dr = args.d;   // dr: a head's channels, D or 32 of a 64-wide piece
-  for (int i = tid; i < NH * kC; i += la_threads(NH)) {
-    const int h = group * NH + i / kC, m = i % kC;
-    wt[i - m + (rev ? m : kC - 1 - m)] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;   // of a whole chunk; m tokens behind the row's
-  }
-  if (warp == 2) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-  __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
-  const uint32_t tmem = *tmem_slot, tG = tmem, tP = tmem + 128, tO = tmem + 256, tZ = tmem + 384;   // tP: wide heads' w b
-
-  int n = args.T;
-  if (args.lengths != nullptr) n = min(max(args.lengths[batch], 0), args.T);
-  const int begin = seg * args.seg_len, end = min(begin + args.seg_len, n);
-  const int chunks = end > begin ? (end - begin + kC - 1) / kC : 0;
-  // the segment that holds the last token (the first one of an empty sequence) writes the state
-  // that leaves, and has a third part of w b for it
-  const bool exact = P.zn != nullptr && seg == (n > 0 ? (n - 1) / args.seg_len : 0);
-  const int chunks_z = exact ? chunks : chunks - 1;                 // those whose update of the state is of use
-  const bool fresh = P.z0 == nullptr && seg == 0;                   // the first chunk meets a zero state
+  const uint32_t tG = tmem, tP = tmem + 128, tO = tmem + 256, tZ = tmem + 384;   // tP: wide heads' w b
+  const LaShare share = share_of(args, P, batch, seg);
+  const int n = share.n, begin = share.begin, end = share.end, chunks = share.chunks, chunks_z = share.chunks_z;
+  const bool exact = share.exact, fresh = share.fresh;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -516,6 +566,22 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         bulk_wait_read<0>();
         mbar_arrive(&bar[kFreeA + (ph ^ 1)]);
       }
+      if constexpr (WATCH) {
+        mbar_pass(&bar[kFullC], ph, failed);
+        __syncwarp();
+#pragma unroll 1
+        for (int h = 0; h < 3 - NH; ++h) {   // the head's boxes
+          unsigned char* rows32 = sc + (head + h) * kBoxBytes + q * 4096;
+          const int rows = rev ? 32 : min(max(c.cnt - 32 * q, 0), 32);   // those behind the last token are not c's
+          const bool found = look_through(rows32, rows, lane);
+          if (lane == 0) unsound[8 * ph + 4 * (head + h) + q] = found;
+          if (found) {
+            if (k < chunks_z) mbar_pass(&bar[kDZ], ph, failed);
+            __syncwarp();
+            take_out(rows32, rows, rev, first_bad + 512 * ph + 128 * q + 64 * (head + h), lane);
+          }
+        }
+      }
       // the state's share of O, decayed to the row
       const float f = exp2f(lg * (float)((rev ? kC - 1 - own : own) - (rev ? 32 * q : -32 * q) + c.lead));
       mbar_pass(&bar[kO2], ph, failed);
@@ -541,6 +607,16 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
       mbar_pass(&bar[kO], ph, failed);
       __syncwarp();
       tmem_fence_after();
+      if constexpr (WATCH) {
+        mbar_pass(&bar[kRows], ph, failed);   // what the others found
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 3 - NH; ++h) {   // the head's boxes
+          const uint32_t seen = *reinterpret_cast<const uint32_t*>(unsound + 8 * ph + 4 * (head + h));
+          if (seen != 0) spoil_row(tR + h * 64, first_bad + 512 * ph + (head + h) * 64, seen, r, rev);
+        }
+      }
+      uint32_t sum[2] = {0u, 0u};
       bf16* dst = P.out + ((int64_t)batch * args.T + c.token0 + r) * P.ldo + (int64_t)(group * NH + head) * dr;
 #pragma unroll
       for (int cb = 0; cb < D / 32; ++cb) {
@@ -552,11 +628,13 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         for (int j = 0; j < 4; ++j) {
           const uint4 w = make_uint4(pack_bf16(v[8 * j], v[8 * j + 1]), pack_bf16(v[8 * j + 2], v[8 * j + 3]),
                                      pack_bf16(v[8 * j + 4], v[8 * j + 5]), pack_bf16(v[8 * j + 6], v[8 * j + 7]));
+          if (!WATCH) add_pairs(sum, w);
           const int box = NH == 2 ? head : cb >> 1, unit = (cb & 1) * 4 + j;
           if (c.cnt == kC) *reinterpret_cast<uint4*>(so + box * kBoxBytes + r * 128 + ((unit ^ (r & 7)) << 4)) = w;
           else if (ord < c.cnt && live && cb * 32 < dr) *reinterpret_cast<uint4*>(dst + cb * 32 + j * 8) = w;
         }
       }
+      if (!WATCH && ord == 0 && not_finite(sum)) *again = 1;
       if (c.cnt == kC) {
         fence_async();
         __syncwarp();
@@ -719,8 +797,94 @@ __global__ void __launch_bounds__(la_threads(kC / D), 1)
         for (int i = 0; i < Z; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(f * z[i], f * z[i + 1], f * z[i + 2], f * z[i + 3]);
     }
   }
+}
+
+template <int NH>
+__device__ __forceinline__ void start_barriers(unsigned long long* bar) {
+  for (int i = 0; i < kBars; ++i) {
+    const bool rows = i == kRows || i == kOFree || i == kFreeA || i == kFreeA + 1, parts = i == kParts || i == kParts + 1;
+    mbar_init(&bar[i], rows || parts ? 4 * NH : i == kZ || i == kClear ? 8 : i == kFreeB || i == kFreeB + 1 ? 9 : i == kFreeC ? 2 : 1);
+  }
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+// Weights of a whole chunk's rows of b; m tokens behind the row's.
+template <int NH>
+__device__ __forceinline__ void whole_weights(float* wt, const LaArgs& args, int group, int rev) {
+  for (int i = threadIdx.x; i < NH * kC; i += la_threads(NH)) {
+    const int h = group * NH + i / kC, m = i % kC;
+    wt[i - m + (rev ? m : kC - 1 - m)] = h < args.heads ? exp2f(args.log2g[h] * (float)m) : 0.f;
+  }
+}
+
+// Out of line: the first pass keeps its registers.
+template <int D>
+__device__ __noinline__ void second_pass(const LaMaps& maps, const LaArgs& args, uint32_t tmem, int which, int group, int batch) {
+  constexpr int NH = kC / D;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const LaShared<NH> sh(sm);
+  if (threadIdx.x == 0) start_barriers<NH>(sh.bar + kBars);
+  whole_weights<NH>(sh.wt, args, group, args.pass[which].reverse);
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  decay_pass<D, true>(maps, args, sm, tmem, which, group, batch);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+}
+
+template <int D>
+__global__ void __launch_bounds__(la_threads(kC / D), 1)
+    decay_tc_kernel(const __grid_constant__ LaMaps maps, const __grid_constant__ LaArgs args) {
+  constexpr int NH = kC / D;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const LaShared<NH> sh(sm);
+  int* failed = sh.failed;
+  const int tid = threadIdx.x, warp = tid >> 5, groups = (args.heads + NH - 1) / NH;
+  int which = blockIdx.z, group = blockIdx.y % groups, batch = blockIdx.y / groups;
+  if (smem_u32(sm) & 1023u) {           // the swizzled tiles' alignment
+    if (tid == 0) atomicExch(args.err, SRNL_E_CUDA);
+    return;
+  }
+
+  if (tid == 0) {
+    *failed = *sh.again = 0;
+    start_barriers<NH>(sh.bar);
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (args.longest_first) {
+    // the CTAs do not all run at once: batch is the one with so many longer sequences
+    int* len = reinterpret_cast<int*>(sm);
+    const int per = groups * gridDim.z, id = blockIdx.z * gridDim.y + blockIdx.y, rank = id / per;
+    which = id % per / groups;
+    group = id % groups;
+    for (int i = tid; i < args.B; i += la_threads(NH)) len[i] = args.lengths[i];
+    __syncthreads();
+    for (int i = tid; i < args.B; i += la_threads(NH)) {
+      const int mine = len[i];
+      int before = 0;
+      for (int j = 0; j < args.B; ++j) before += len[j] > mine || (len[j] == mine && j < i);
+      if (before == rank) *sh.tmem_slot = i;
+    }
+    __syncthreads();
+    batch = *sh.tmem_slot;
+    fence_async();
+    __syncthreads();
+  }
+  whole_weights<NH>(sh.wt, args, group, args.pass[which].reverse);
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sh.tmem_slot)), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const uint32_t tmem = *sh.tmem_slot;
+  decay_pass<D, false>(maps, args, sm, tmem, which, group, batch);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(sh.again) != 0 && *reinterpret_cast<volatile int*>(failed) == 0)
+    second_pass<D>(maps, args, tmem, which, group, batch);
   if (*reinterpret_cast<volatile int*>(failed)) {   // a wait gave up: report, and let the copies in flight land
     if (tid == 0) atomicExch(args.err, SRNL_E_TIMEOUT);
     const unsigned long long t0 = global_ns();
@@ -931,7 +1095,7 @@ __global__ void __launch_bounds__(256) decay_start_kernel(const __grid_constant_
   }
 }
 
-constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + (size_t)(kC / d) * kC * 4 + kBars * 8 + 16; }
+constexpr size_t la_smem(int d) { return 7 * (size_t)kTile + (size_t)(kC / d) * kC * 4 + 2 * kBars * 8 + 32 + 1024; }
 
 template <typename... P, typename... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {

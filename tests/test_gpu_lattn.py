@@ -554,3 +554,98 @@ def test_a_new_handle_is_ready_for_any_stream():
             h.close()
     assert all(torch.equal(a, b) for x in outs for a, b in zip(x, outs[0]))
     within(outs[0][0], *reference(t, [0.9] * H, [T] * B, True, False)["o"])
+
+
+@pytest.mark.parametrize("B,T,H,d,lens", [(2, 12, 3, 32, None), (2, 16, 2, 128, [16, 9]), (3, 300, 3, 64, [300, 150, 260]),
+                                          (2, 290, 2, 128, [290, 201]), (2, 200, 3, 32, None), (1, 1000, 2, 64, None), (1, 900, 1, 128, [899]),
+                                          (40, 260, 3, 128, [260 - 3 * i for i in range(40)])])
+def test_what_is_not_finite_reaches_no_earlier_token(B, T, H, d, lens):
+    """One value of one token NaN or infinite: forward nothing before that token changes by a bit, backward nothing behind
+    it but where the definition has it; nor any other head, sequence, or channel that it does not enter.  From the
+    token on its channel is not finite."""
+    decay = np.linspace(0.9, 1.0, H).astype(np.float32)
+    t = make(B, T, H, d, seed=d + T)
+    n = torch.tensor(lens, device="cuda", dtype=torch.int32) if lens else None
+    D = H * d
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), decay)
+
+    def run(t):
+        o, st, dsi = torch.zeros(B, T, D, device="cuda", dtype=BF), torch.empty_like(t["s0"]), torch.empty_like(t["s0"])
+        g = [torch.zeros_like(o) for _ in range(3)]
+        S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=n, state_in=t["s0"], state_out=st)
+        S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], *g, lengths=n, state_in=t["s0"], dstate_out=t["ds"], dstate_in=dsi)
+        torch.cuda.synchronize()
+        return {"o": o, "dq": g[0], "dk": g[1], "dv": g[2], "state": st, "dstate": dsi}
+
+    try:
+        clean = run(t)
+        b, head, ch = B - 1, H - 1, d - 3
+        last = (lens[b] if lens else T) - 1
+        col = head * d + ch
+        for at in sorted({0, 1, last // 3, last // 2 + 1, last}):
+            for name in ("q", "k", "v", "do"):
+                for value in (float("nan"), float("inf")):
+                    u = dict(t)
+                    u[name] = t[name].clone()
+                    u[name][b, at, col] = value
+                    # a second token further on, which adds nothing to what the first one spoils
+                    if at + 5 <= last and name in ("k", "v"):
+                        u[name][b, at + 5, col] = -value
+                    got = run(u)
+                    from_, upto, own = slice(at, last + 1), slice(0, at + 1), slice(at, at + 1)
+                    whole, one = slice(head * d, (head + 1) * d), slice(col, col + 1)
+                    # rows and columns that may change: {output: (rows, columns)}, and those that have to be spoilt
+                    may = {"q": {"o": (own, whole), "dk": (upto, one), "dv": (upto, whole)},
+                           "k": {"o": (from_, whole), "dq": (from_, one), "dv": (None, whole)},
+                           "v": {"o": (from_, one), "dq": (from_, whole), "dk": (None, whole)},
+                           "do": {"dq": (own, whole), "dk": (upto, whole), "dv": (upto, one)}}[name]
+                    for out in ("o", "dq", "dk", "dv"):
+                        a, c = got[out].clone(), clean[out].clone()
+                        rows, cols = may.get(out, (slice(0, 0), whole))
+                        hit = [at] + ([at + 5] if at + 5 <= last and name in ("k", "v") else [])
+                        for r in ([rows] if rows is not None else [slice(x, x + 1) for x in hit]):
+                            if out in may and r.stop > r.start:
+                                assert not bool(torch.isfinite(a[b, r, cols]).any()), (name, value, at, out)
+                            a[b, r, cols] = c[b, r, cols] = 0
+                        assert torch.equal(a, c), (name, value, at, out)
+                    a, c = got["state"].clone(), clean["state"].clone()
+                    if name in ("k", "v"):
+                        part = a[b, head, ch] if name == "k" else a[b, head, :, ch]
+                        assert not bool(torch.isfinite(part).any())
+                        part.zero_()
+                        (c[b, head, ch] if name == "k" else c[b, head, :, ch]).zero_()
+                    assert torch.equal(a, c), (name, value, at, "state")
+                    a, c = got["dstate"].clone(), clean["dstate"].clone()
+                    if name in ("q", "do"):
+                        part = a[b, head, ch] if name == "q" else a[b, head, :, ch]
+                        assert not bool(torch.isfinite(part).any())
+                        part.zero_()
+                        (c[b, head, ch] if name == "q" else c[b, head, :, ch]).zero_()
+                    assert torch.equal(a, c), (name, value, at, "dstate")
+        S.srnl_lattn_device_status(h)
+    finally:
+        h.close()
+
+
+@pytest.mark.parametrize("B,T,H,d", [(2, 16, 2, 64), (2, 300, 3, 64), (3, 400, 2, 128), (1, 1000, 2, 32)])
+def test_values_beyond_half_the_exponents(B, T, H, d):
+    """Values of 2^80: finite, whatever the watch for what is not makes of them.  Every result is linear in v, and in do: a power
+    of two times them is that power times the results, bit by bit."""
+    t = make(B, T, H, d, seed=T)
+    lens = torch.tensor([T - 7 * i for i in range(B)], device="cuda", dtype=torch.int32)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.linspace(0.9, 1.0, H).astype(np.float32))
+    try:
+        def run(v, do, s0):
+            o, st, g, dsi = torch.zeros_like(t["q"]), torch.empty_like(s0), [torch.zeros_like(t["q"]) for _ in range(3)], torch.empty_like(s0)
+            S.srnl_lattn_forward(h, t["q"], t["k"], v, o, lengths=lens, state_in=s0, state_out=st)
+            S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], do, *g, lengths=lens, dstate_in=dsi)
+            torch.cuda.synchronize()
+            return [o, st, *g, dsi]
+
+        big = 2.0 ** 80
+        small, large = run(t["v"], t["do"], t["s0"]), run(t["v"] * big, t["do"] * big, t["s0"] * big)
+        for a, b in zip(small, large):
+            assert bool(torch.isfinite(b).all()) and torch.equal(a.double() * big, b.double())
+        S.srnl_lattn_device_status(h)
+    finally:
+        h.close()
