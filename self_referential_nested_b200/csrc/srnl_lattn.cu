@@ -147,7 +147,7 @@ bool la_meet(const Rows& a, const Rows& b) {
   return d < a.width || d + b.width > a.pitch;
 }
 
-srnl_status la_check(srnl_lattn* h, const Rows* in, int ni, const Rows* out, int no, const void* lengths) {
+srnl_status la_check(srnl_lattn* h, const Rows* in, int ni, const Rows* out, int no, const int* lengths) {
   char msg[256];
   for (int i = 0; i < ni + no; ++i) {
     const Rows& r = i < ni ? in[i] : out[i - ni];
@@ -164,6 +164,12 @@ srnl_status la_check(srnl_lattn* h, const Rows* in, int ni, const Rows* out, int
         snprintf(msg, sizeof msg, "%s overlaps %s", out[i].name, r.name);
         return la_fail(h, SRNL_E_INVAL, msg);
       }
+    }
+  const Rows n{lengths, 1, (int64_t)h->cfg.B * 4, (int64_t)h->cfg.B * 4, "lengths"};
+  for (int i = 0; i < no; ++i)
+    if (la_meet(out[i], n)) {
+      snprintf(msg, sizeof msg, "%s overlaps lengths", out[i].name);
+      return la_fail(h, SRNL_E_INVAL, msg);
     }
   int cur = -1;
   const cudaError_t e = cudaGetDevice(&cur);

@@ -649,3 +649,26 @@ def test_values_beyond_half_the_exponents(B, T, H, d):
         S.srnl_lattn_device_status(h)
     finally:
         h.close()
+
+
+def test_outputs_over_the_lengths_are_refused():
+    B, T, H, d = 4, 40, 2, 32
+    t = make(B, T, H, d)
+    h = S.srnl_lattn_create(dict(B=B, T=T, heads=H, d=d), np.full(H, 0.9, np.float32))
+    try:
+        o, st = torch.empty_like(t["q"]), torch.empty_like(t["s0"])
+        g = [torch.empty_like(o) for _ in range(3)]
+        calls = [("o", o, lambda n: S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=n)),
+                 ("state_out", st, lambda n: S.srnl_lattn_forward(h, t["q"], t["k"], t["v"], o, lengths=n, state_out=st)),
+                 ("dv", g[2], lambda n: S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], *g, lengths=n)),
+                 ("dstate_in", st, lambda n: S.srnl_lattn_backward(h, t["q"], t["k"], t["v"], t["do"], *g, lengths=n, dstate_in=st))]
+        for name, out, call in calls:
+            n = out.view(torch.int32).flatten()[20:20 + B]
+            n.copy_(torch.tensor([40, 0, 7, 33]))
+            with pytest.raises(S.SrnlError) as e:
+                call(n)
+            assert e.value.status == S.SRNL_E_INVAL and f"{name} overlaps lengths" in str(e.value)
+            call(n.clone())
+        torch.cuda.synchronize()
+    finally:
+        h.close()
