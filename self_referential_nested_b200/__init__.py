@@ -627,12 +627,6 @@ def _dense(h: "_OpHandle", t, where: str, name: str, dtype, full) -> int:
     return t.data_ptr()
 
 
-def _row_shape(x, width: int):
-    """x's rows of `width` values: their number, and x's own shape where it ends in the width."""
-    rows, n = x.numel() // width, x.shape
-    return rows, (n if n and n[-1] == width else (rows, width))
-
-
 class _OpHandle:
     """Owns one handle of an operator; ``close()`` (or GC) destroys it."""
 
@@ -689,26 +683,34 @@ def srnl_ln_create(cfg: Dict) -> SrnlLn:
 def srnl_ln_forward(h: SrnlLn, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:
     """y <- layer norm of x ([..., dim] CUDA tensors of the handle's act dtype; gamma, beta
     float32 [dim]); mean, rstd: float32 [rows], written when given."""
-    w, hd, d, f32 = "srnl_ln_forward", h.handle, h._dim, h._f32
-    rows, n = _row_shape(x, d)
+    w, hd, d, f32 = "srnl_ln_forward", h._h or h.handle, h._dim, h._f32
+    rows, n = x.numel() // d, x.shape
+    if not n or n[-1] != d:
+        n = (rows, d)
     r, d = (rows,), (d,)
-    h._check(load_library().srnl_ln_forward(
+    st = _lib.srnl_ln_forward(
         hd, _dense(h, x, w, "x", h._dtype, n), _dense(h, gamma, w, "gamma", f32, d), _dense(h, beta, w, "beta", f32, d),
         _dense(h, y, w, "y", h._dtype, n), _dense(h, mean, w, "mean", f32, r), _dense(h, rstd, w, "rstd", f32, r), rows,
-        _stream(stream)), w)
+        _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 def srnl_ln_backward(h: SrnlLn, x, dy, gamma, mean, rstd, dx, dgamma=None, dbeta=None, dres=None, stream=None) -> None:
     """dx <- dL/dx for upstream dy (+ dres when given); dgamma, dbeta (float32 [dim]) are
     overwritten when given.  mean, rstd: the forward's."""
-    w, hd, d, f32 = "srnl_ln_backward", h.handle, h._dim, h._f32
-    (rows, n), dt = _row_shape(x, d), h._dtype
+    w, hd, d, f32 = "srnl_ln_backward", h._h or h.handle, h._dim, h._f32
+    rows, n, dt = x.numel() // d, x.shape, h._dtype
+    if not n or n[-1] != d:
+        n = (rows, d)
     r, d = (rows,), (d,)
-    h._check(load_library().srnl_ln_backward(
+    st = _lib.srnl_ln_backward(
         hd, _dense(h, x, w, "x", dt, n), _dense(h, dy, w, "dy", dt, n), _dense(h, dres, w, "dres", dt, n),
         _dense(h, gamma, w, "gamma", f32, d), _dense(h, mean, w, "mean", f32, r), _dense(h, rstd, w, "rstd", f32, r),
         _dense(h, dx, w, "dx", dt, n), _dense(h, dgamma, w, "dgamma", f32, d), _dense(h, dbeta, w, "dbeta", f32, d), rows,
-        _stream(stream)), w)
+        _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 class SrnlFfn(_OpHandle):
@@ -743,27 +745,37 @@ def srnl_ffn_forward(h: SrnlFfn, x, params: Dict, y, res=None, gate=None, up=Non
     """y <- (act(x W_gate^T) * (x W_up^T)) W_down^T (+ res).  x, y, res: bf16 CUDA tensors
     [..., dim]; params: W_gate, W_up [hidden, dim], W_down [dim, hidden] in bf16; gate, up
     [rows, hidden] keep the pre-activations for the backward pass when given."""
-    w, hd, dt = "srnl_ffn_forward", h.handle, h._dtype
-    rows, n = _row_shape(x, h._dim)
+    w, hd, dt = "srnl_ffn_forward", h._h or h.handle, h._dtype
+    d = h._dim
+    rows, n = x.numel() // d, x.shape
+    if not n or n[-1] != d:
+        n = (rows, d)
     f = (rows, h._hidden)
     p = _ffn_weights(h, params, w)
-    h._check(load_library().srnl_ffn_forward(
+    st = _lib.srnl_ffn_forward(
         hd, _dense(h, x, w, "x", dt, n), ctypes.byref(p), _dense(h, res, w, "res", dt, n),
         _dense(h, y, w, "y", dt, n), _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f), rows,
-        _stream(stream)), w)
+        _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 def srnl_ffn_backward(h: SrnlFfn, x, gate, up, dy, params: Dict, dx, grads: Optional[Dict] = None, stream=None) -> None:
     """dx <- dL/dx for upstream dy (dx None skips it); ``grads`` maps any of FFN_KEYS to bf16
     CUDA tensors in the weights' layouts, which are overwritten.  gate, up: the forward's."""
-    w, hd, dt = "srnl_ffn_backward", h.handle, h._dtype
-    rows, n = _row_shape(x, h._dim)
+    w, hd, dt = "srnl_ffn_backward", h._h or h.handle, h._dtype
+    d = h._dim
+    rows, n = x.numel() // d, x.shape
+    if not n or n[-1] != d:
+        n = (rows, d)
     f = (rows, h._hidden)
     p, g = _ffn_weights(h, params, w), _ffn_weights(h, grads, w)
-    h._check(load_library().srnl_ffn_backward(
+    st = _lib.srnl_ffn_backward(
         hd, _dense(h, x, w, "x", dt, n), _dense(h, gate, w, "gate", dt, f), _dense(h, up, w, "up", dt, f),
         _dense(h, dy, w, "dy", dt, n), ctypes.byref(p), _dense(h, dx, w, "dx", dt, n), ctypes.byref(g), rows,
-        _stream(stream)), w)
+        _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 def srnl_ffn_device_status(h: SrnlFfn) -> None:
@@ -814,35 +826,41 @@ def srnl_lattn_create(cfg: Dict, decay: np.ndarray) -> SrnlLattn:
 def srnl_lattn_forward(h: SrnlLattn, q, k, v, o, lengths=None, state_in=None, state_out=None, stream=None) -> None:
     """o <- linear attention of q, k, v (bf16 [B, T, heads * d], tokens ld elements apart).
     lengths: int32 [B]; state_in, state_out: float32 [B, heads, d, d]."""
-    w, hd, c = "srnl_lattn_forward", h.handle, h._c
+    w, hd, c = "srnl_lattn_forward", h._h or h.handle, h._c
     n, s, f32 = (c.B, c.T, c.heads * c.d), (c.B, c.heads, c.d, c.d), h._f32
-    h._check(load_library().srnl_lattn_forward(
+    st = _lib.srnl_lattn_forward(
         hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(h, o, w, "o", h._dtype, n),
         _dense(h, lengths, w, "lengths", h._i32, (c.B,)), _dense(h, state_in, w, "state_in", f32, s),
-        _dense(h, state_out, w, "state_out", f32, s), _stream(stream)), w)
+        _dense(h, state_out, w, "state_out", f32, s), _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 def srnl_lattn_backward(h: SrnlLattn, q, k, v, do, dq, dk, dv, lengths=None, state_in=None, dstate_out=None,
                         dstate_in=None, stream=None) -> None:
     """dq, dk, dv <- the gradients for upstream do (dense) and dstate_out; dstate_in receives the
     gradient of state_in when given."""
-    w, hd, c = "srnl_lattn_backward", h.handle, h._c
+    w, hd, c = "srnl_lattn_backward", h._h or h.handle, h._c
     n, s, f32 = (c.B, c.T, c.heads * c.d), (c.B, c.heads, c.d, c.d), h._f32
-    h._check(load_library().srnl_lattn_backward(
+    st = _lib.srnl_lattn_backward(
         hd, h._rows(q, w, "q", 1), h._rows(k, w, "k", 1), h._rows(v, w, "v", 1), _dense(h, do, w, "do", h._dtype, n),
         h._rows(dq, w, "dq", 1), h._rows(dk, w, "dk", 1), h._rows(dv, w, "dv", 1),
         _dense(h, lengths, w, "lengths", h._i32, (c.B,)), _dense(h, state_in, w, "state_in", f32, s),
-        _dense(h, dstate_out, w, "dstate_out", f32, s), _dense(h, dstate_in, w, "dstate_in", f32, s), _stream(stream)), w)
+        _dense(h, dstate_out, w, "dstate_out", f32, s), _dense(h, dstate_in, w, "dstate_in", f32, s), _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 def srnl_lattn_step(h: SrnlLattn, q, k, v, o, state, stream=None) -> None:
     """One token of each sequence: q, k, v, o bf16 [B, heads * d]; state float32
     [B, heads, d, d], updated in place."""
-    w, hd, c = "srnl_lattn_step", h.handle, h._c
-    h._check(load_library().srnl_lattn_step(
+    w, hd, c = "srnl_lattn_step", h._h or h.handle, h._c
+    st = _lib.srnl_lattn_step(
         hd, h._rows(q, w, "q", 0), h._rows(k, w, "k", 0), h._rows(v, w, "v", 0),
         _dense(h, o, w, "o", h._dtype, (c.B, c.heads * c.d)),
-        _dense(h, state, w, "state", h._f32, (c.B, c.heads, c.d, c.d)), _stream(stream)), w)
+        _dense(h, state, w, "state", h._f32, (c.B, c.heads, c.d, c.d)), _stream(stream))
+    if st:
+        h._check(st, w)
 
 
 def srnl_lattn_device_status(h: SrnlLattn) -> None:
