@@ -26,7 +26,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -430,19 +429,17 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
     float s[2 * R], f[R];
     uint4 res[R][PER];
     if (!kAhead) load(r0);
-    // values past a row's ends are zeros in x and dy and add nothing to any sum
+    // w carries rstd from the start.  Values past a row's ends are zeros in x and dy and add nothing to any sum:
+    // w (x - mean) is zero there even where the row lies so far from zero that mean rstd, and xhat, are infinite.
     float2 xh[R][PER * H], w[R][PER * H];
 #pragma unroll
     for (int q = 0; q < R; ++q) {
       float2 t = make_float2(0.f, 0.f), u = make_float2(0.f, 0.f);
-      const bool far = ODD && fabsf(mean[q] * rstd[q]) > FLT_MAX;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int c = c0 + i * cs;
-        const float2 off = both(on[i] ? -mean[q] : 0.f);
         float2 xv[H], yv[H], gw[H];
-        unpack<T>(clip<T, LPR, ODD>(xr[q][i], c, dim), xv);
-        unpack<T>(clip<T, LPR, ODD>(yr[q][i], c, dim), yv);
+        unpack<T>(clip<T, LPR, ODD>(xr[q][i], c0 + i * cs, dim), xv);
+        unpack<T>(clip<T, LPR, ODD>(yr[q][i], c0 + i * cs, dim), yv);
         if (!on[i]) {
 #pragma unroll
           for (int e = 0; e < H; ++e) gw[e] = make_float2(0.f, 0.f);
@@ -450,25 +447,18 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
 #pragma unroll
           for (int e = 0; e < H; ++e) gw[e] = g[i * H + e];
         } else {
-          load_weights<V>(gp + c, gw);
+          load_weights<V>(gp + c0 + i * cs, gw);
         }
-#pragma unroll
-        for (int e = 0; e < H; ++e) xh[q][i * H + e] = __fmul2_rn(__fadd2_rn(xv[e], off), both(rstd[q]));
-        // outside the row xhat only has to be finite, as dy is zero there; mean rstd may not be
-        if (ODD && far && (c < 0 || c + V > dim))
-#pragma unroll
-          for (int e = 0; e < H; ++e) {
-            if (c + 2 * e < 0 || c + 2 * e >= dim) xh[q][i * H + e].x = 0.f;
-            if (c + 2 * e + 1 < 0 || c + 2 * e + 1 >= dim) xh[q][i * H + e].y = 0.f;
-          }
 #pragma unroll
         for (int e = 0; e < H; ++e) {
           const int k = i * H + e;
+          const float2 d = __fadd2_rn(xv[e], both(-mean[q]));
+          xh[q][k] = __fmul2_rn(d, both(rstd[q]));
           dg[k] = __ffma2_rn(yv[e], xh[q][k], dg[k]);
           db[k] = __fadd2_rn(db[k], yv[e]);
-          w[q][k] = __fmul2_rn(yv[e], gw[e]);
+          w[q][k] = __fmul2_rn(__fmul2_rn(yv[e], gw[e]), both(rstd[q]));
           t = __fadd2_rn(t, w[q][k]);
-          u = __ffma2_rn(w[q][k], xh[q][k], u);
+          u = __ffma2_rn(w[q][k], d, u);
         }
       }
       s[2 * q] = t.x + t.y;
@@ -486,15 +476,14 @@ __global__ void __cluster_dims__(CL, 1, 1) __launch_bounds__(norm_threads(LPR, P
     for (int q = 0; q < R; ++q) {
       const int64_t r = r0 + q * groups;
       if (r >= rows) continue;
-      const float2 a = both(-s[2 * q] * inv_d), m = both(-s[2 * q + 1] * inv_d);
+      const float2 a = both(-s[2 * q] * inv_d), m = both(-s[2 * q + 1] * inv_d * f[q]);
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (!on[i]) continue;
         float2 o[H];
         unpack<T>(res[q][i], o);
 #pragma unroll
-        for (int e = 0; e < H; ++e)
-          o[e] = __ffma2_rn(__ffma2_rn(xh[q][i * H + e], m, __fadd2_rn(w[q][i * H + e], a)), both(f[q]), o[e]);
+        for (int e = 0; e < H; ++e) o[e] = __fadd2_rn(__ffma2_rn(xh[q][i * H + e], m, __fadd2_rn(w[q][i * H + e], a)), o[e]);
         store_cols<T, ODD>(dx + r * dim, c0 + i * cs, dim, o);
       }
     }
