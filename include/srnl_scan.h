@@ -483,8 +483,8 @@ SRNL_API const char* srnl_ln_last_error(const srnl_ln* h);
 SRNL_API void srnl_ln_destroy(srnl_ln* h);
 
 /* ------------------------------------------------------------------------
- * Gated feed-forward branch with its backward pass, the counterpart of the residual block's
- * FFN for training and serving:
+ * Gated feed-forward branch with its backward pass, for training and serving the layers around
+ * the memory (the residual block's FFN is another: two weights with biases, no gate, forward only):
  *   y = (act(x Wg^T) * (x Wu^T)) Wd^T + res
  * bf16 tensors, fp32 accumulation on the tensor cores.  Between the products the hidden rows
  * (and in the backward pass the gradients of the two pre-activations) are rounded to bf16.

@@ -19,9 +19,9 @@
 // thread fills a ring of 64-wide K stages by TMA (128-byte swizzle; a ragged edge reads as
 // zeros), one thread of the leading CTA issues the products into one of two accumulators in
 // TMEM, and eight warps empty the other.  Results leave by TMA from per-warp staging tiles,
-// which clips them at the edges.  8192 rows, 2048 x 5632: forward 440 us (1290 TF/s), backward 940
-// (1205 TF/s), bound by the tensor cores under the power limit, but for kGluBack, whose epilogue moves
-// 461 MB; 12544 rows, 256 x 1024, both pre-activations kept: 39 us, bound by the epilogue.
+// which clips them at the edges.  8192 rows, 2048 x 5632: forward 455 to 470 us (1245 to 1205 TF/s), backward
+// 975 to 1025 (1165 to 1105 TF/s), bound by the tensor cores under the power limit, but for kGluBack, whose
+// epilogue moves 461 MB; 12544 rows, 256 x 1024, both pre-activations kept: 41 us, bound by the epilogue.
 //
 // Roundings: h, dgate and dup are rounded to bf16 between the products, as the tensor cores
 // take them; everything else is rounded once, on output.  gate and up are kept in bf16 for the
@@ -790,7 +790,10 @@ cudaError_t launch_few_rows(const bf16_t* x, const bf16_t* W, const bf16_t* W2, 
 // of a 256-column one where the rounds of tiles follow one another (8192 x 2048 x 11264: 409 us in
 // 7 rounds of them, 259 us in 4) and two thirds in a single round (512 x 5632 x 2048, with the
 // projections before it: 58 us against 65; 1024 rows: 70 us, against 74 in 256 columns and two
-// parts).
+// parts).  Where K is short and the epilogue counts, narrow tiles lose as much (projections and hidden
+// gradients in 256 against 128 columns, GELU: forward of 12544 x 256 x 1024 35 us against 39, both
+// pre-activations kept 41 against 47, backward 81 against 84; of 25088 rows 57, 71, 137 against 71, 86, 142;
+// 50176 x 128 x 512 51, 64, 130 against 62, 77, 133).
 int64_t launch_cost(const FfnArgs& a, int bn, int sms) {
   return (bn == 256 ? 12 : a.tiles <= sms / 2 ? 8 : 10) * longest_pair(a, sms / 2);
 }
@@ -811,7 +814,7 @@ int least_stages(const FfnArgs& a) {
 // cut one pays for its partial sums, which go through L2 and are added up by whoever comes last
 // (output product of 2048 x 5632, 64 rows, with the projections before it: 44 us uncut, 39, 36.5 and
 // 35.5 in 2, 3 and 4 parts; of 520 x 1384, 22 stages: 15.6 uncut, 16.5 in 2; the weights' gradients of
-// 12544 x 256 x 1024, in the whole backward pass: 96 us uncut, 76).
+// 12544 x 256 x 1024, in the whole backward pass: 96 us uncut, 76 to 81).
 template <typename Build>
 FfnArgs pick_launch(int sms, int groups, int& bn, const Build& build) {
   FfnArgs best{};

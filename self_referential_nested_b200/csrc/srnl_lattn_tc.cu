@@ -24,8 +24,9 @@
 // What bounds it: a chunk's operands, parts and results pass through shared memory about 4400 times
 // 128 bytes (5400 for narrow heads), two thirds of the 7000 cycles that a chunk takes; the rest is the
 // chain of products, masking and the state's update, which wait for one another.  One sequence of
-// 16384 tokens, 16 heads of 128: 112 us (2.4 TB/s; 31 of them the segments' states); backward of 8 x
-// 2048 tokens, 16 heads of 64, lengths at random: 62 us (3.8 TB/s).
+// 16384 tokens, 16 heads of 128, states in and out: 128 us with cold operands (2.2 TB/s), 51 of them
+// the segments' states, 115 us with operands in L2; backward of 8 x 2048 tokens, 16 heads of 64, lengths
+// at random (a little over half of the tokens, 132 MB): 68 us (1.9 TB/s), the longest sequence's chunks.
 //
 // Sequences that leave SMs idle are cut into segments.  One kernel sums what each segment adds to
 // the state, a second turns the sums into the states they start from, and the pass itself follows.
@@ -1130,6 +1131,11 @@ cudaError_t launch_tc(LaArgs& a, const LaMaps& m, cudaStream_t s) {
 int la_groups(int heads, int d) { return d == 128 ? heads : (heads + 1) / 2; }
 
 int la_tc_segments(int T, int seqs, int sms) {
+  // As many segments as fill the SMs once.  Between half the SMs and all of them, or above, that is one:
+  // the segments' states are most of a pass by themselves, so that two waves of half the length, or a
+  // second half of the SMs, do not pay for them (4096 tokens, one head of 128, whole, in 2 and in 3
+  // segments: 80 sequences 129, 176, 162 us; 112: 128, 191, 216; 148: 138, 230, 260; 75 of 8192: 240,
+  // 309, 269; backward of 8 x 2048, 16 heads of 64, 192 passes of a sequence: 116, 151, 169).
   const int chunks = (T + kC - 1) / kC, want = sms / seqs;
   // two chunks a segment at least, and six chunks: below, the two launches before the pass cost more
   // than the chunks that follow one another (512 tokens, 4 heads of 64: 15.6 us whole, 18.6 cut; 1024:

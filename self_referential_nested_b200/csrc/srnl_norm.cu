@@ -8,8 +8,8 @@
 //             dgamma = sum_rows dy xhat, dbeta = sum_rows dy
 //
 // Both passes are bound by memory: each input is read once and each output written once (backward of
-// 8209 x 2560 fp32: 49 us, 5.1 TB/s; of 25088 x 384 bf16 with dres: 20 us, 3.9 TB/s; forward of 100352 x
-// 64 bf16: 5.9 us, 4.4 TB/s, in L2), short calls by their launches.  All statistics, sums and
+// 8209 x 2560 fp32: 52 us, 4.9 TB/s; of 25088 x 384 bf16 with dres: 21 us, 3.6 TB/s; forward of 100352 x
+// 64 bf16: 5.4 us, 4.9 TB/s, in L2), short calls by their launches.  All statistics, sums and
 // gradients of gamma and beta are fp32; only y and dx are rounded, once, to the activations' type.
 //
 // Layout of the work: a row belongs to a group of lanes that hold it in registers between the
@@ -74,8 +74,8 @@ __device__ __forceinline__ uint4 repack(const float2* v) {
 // The 16-byte unit at column c of a row.  An odd row's units at its ends hold values of its
 // neighbours too.  They are read whole and the neighbours' values taken out once they have arrived
 // (clip): value by value a lane packs bf16 ones, and so waits for each unit in turn (8000 x 1533
-// backward: 81 us, 40 whole).  fp32 ones need no packing, and blocks of long rows take them value by
-// value (44 us whole, 41 so).  Nothing is read behind the buffer's end (room: values up to there).
+// backward: 81 us, 41 whole).  fp32 ones need no packing, and blocks of long rows take them value by
+// value (41 us whole, 38 so).  Nothing is read behind the buffer's end (room: values up to there).
 template <typename T, int LPR, bool ODD>
 __host__ __device__ constexpr bool whole_units() { return ODD && (sizeof(T) == 2 || LPR != 0); }
 
