@@ -577,8 +577,8 @@ SRNL_API srnl_status srnl_lattn_create(srnl_lattn** out, const srnl_lattn_config
  * first token, or NULL for zeros; state_out: the memory after the last one, or NULL.  Outputs
  * overlap neither inputs nor one another.  What is not finite reaches what the recurrence lets
  * it reach (as NaN, where sums decide): outputs of its sequence's head from its token on and the
- * state behind them, no earlier outputs, other sequences or heads; segments of a sequence that
- * meet it take twice their time.
+ * state behind them, no earlier outputs, other sequences or heads.  A sequence that meets it takes
+ * twice its time, one of nothing else several times.
  * Asynchronous on `stream`; calls on one handle must not overlap on the device. */
 SRNL_API srnl_status srnl_lattn_forward(srnl_lattn* h, const void* q, const void* k, const void* v, void* o,
                                         const int* lengths, const float* state_in, float* state_out, void* stream);

@@ -222,7 +222,8 @@ __device__ __forceinline__ void clear_rows(unsigned char* c, int from, int t, in
 // through their head's c, 32 tokens each, note the first token that has what is not finite, channel by
 // channel, and replace it by zero once the state's product, where it belongs, has taken it; after (3)
 // they put NaN from that token on.  Looking in the first pass cost 6 % and more (8 x 2048, 16 heads of
-// 128: 67 -> 75 us), the watch costs 0 to 2 % (backward of 64: 114 -> 116.5).
+// 128: 67 -> 75 us), the watch costs 0 to 2 % (backward of 64: 114 -> 116.5).  The second pass is not
+// made fast: 1 x 16384, 16 heads of 128, all NaN: 684 us.
 constexpr int kNone = 255;
 // Sums of products of pairs: not finite where a value is not (or where values beyond 2^63 meet, which costs time only).
 __device__ __forceinline__ void add_pairs(uint32_t (&sum)[2], const uint4& x) {
